@@ -15,7 +15,9 @@ Names match the C ABI in include/ssd.h:
     ssd_fwd_config_workspace_size, ssd_fwd_status, ssd_fwd_noalloc, ssd_bwd,
     ssd_bwd_workspace_size, ssd_bwd_workspace_min_size, ssd_status_string,
     ssd_last_error_message, ssd_abi_version
-(ssd_fwd_config is reached through ssd_fwd(..., config=...).)
+(ssd_fwd_config is reached through ssd_fwd(..., config=...).)  The operators
+around the scan (include/ssd_layer.h: ssd_conv_*, ssd_selscan_*,
+ssd_gated_norm_*) are in layer.py and exported here too.
 """
 from __future__ import annotations
 
@@ -156,6 +158,7 @@ def load_library():
         lib.ssd_bwd_workspace_min_size.argtypes = [P, ctypes.POINTER(sz)]
         lib.ssd_bwd.restype = ctypes.c_int
         lib.ssd_bwd.argtypes = [P, X] + [vp] * 18 + [sz, vp]
+        layer.declare(lib, ssd_dt_transform)
         _lib = lib
         return lib
 
@@ -581,3 +584,10 @@ def ssd_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch.Tensor,
                      workspace.numel() * workspace.element_size(), _stream(x.device))
     _check(st)
     return out
+
+
+# The operators around the scan (include/ssd_layer.h).
+from . import layer  # noqa: E402
+from .layer import *  # noqa: E402,F401,F403
+
+__all__ += layer.__all__

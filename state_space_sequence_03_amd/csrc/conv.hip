@@ -1,0 +1,398 @@
+// conv.hip -- the short depthwise causal convolution that makes a layer's x, B
+// and C out of its projection, its gradients, and its single-token form.
+//
+// For every batch b, channel c and token t, with width W:
+//     u[t] = bias[c] + sum_{k < W} w[c, k] x[t - (W - 1) + k]
+//     y[t] = u[t]                (no activation)  or  u[t] sigmoid(u[t])
+// where x at t < 0 is the caller's state of the W - 1 inputs before the first
+// (zero without one).  The gradients, with du = dy act'(u):
+//     dx[t] = sum_k w[c, k] du[t + (W - 1) - k]     (du = 0 past the last token)
+//     dw[c, k] = sum_{b, t} du[t] x[t - (W - 1) + k],   dbias[c] = sum du[t]
+//
+// Both directions are bound by HBM: 2 elements moved per output forwards, 3
+// backwards, against ~20 and ~40 VALU operations.  A thread owns V channels
+// (16 bytes of io elements where sizes and alignment allow, else one) of a run of
+// tokens and slides a window of W - 1 rows in registers, so each row is loaded
+// once per run plus W - 1 rows of overlap.
+#include "layer_device.hpp"
+#include "layer_host.hpp"
+
+namespace ssd {
+
+// Up to three outputs (or upstream gradients) side by side along the channels,
+// each a contiguous [batch, seqlen, size] tensor; `end` are running channel counts.
+struct ConvParts {
+  void* p[3];
+  int64_t end[3];
+};
+
+template <typename T>
+struct PartRow {
+  T* p;        // element (b, 0, c)
+  int64_t ld;  // elements per token
+};
+template <typename T>
+__device__ __forceinline__ PartRow<T> part_of(const ConvParts& q, int64_t b, int64_t L, int64_t c) {
+  const int s = (c >= q.end[0]) + (c >= q.end[1]);
+  T* const p = static_cast<T*>(s == 0 ? q.p[0] : s == 1 ? q.p[1] : q.p[2]);
+  const int64_t lo = s == 0 ? 0 : s == 1 ? q.end[0] : q.end[1];
+  const int64_t hi = s == 0 ? q.end[0] : s == 1 ? q.end[1] : q.end[2];
+  return {p + (b * L * (hi - lo) + (c - lo)), hi - lo};
+}
+
+constexpr int kConvThreads = 256;
+constexpr int kConvAhead = 4;   // rows loaded ahead of the one in use
+
+// Threads of a workgroup: lc lanes along the channels (a power of two up to
+// 64), kConvThreads / lc runs of tokens.
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(kConvThreads)
+conv_fwd_kernel(const T* __restrict__ x, Strides xs, const float* __restrict__ w,
+                const float* __restrict__ bias, const T* init, ConvParts y, T* fin, int silu,
+                int64_t L, int64_t C, int64_t bx, int lc_log, int64_t run) {
+  const int lane = threadIdx.x & ((1 << lc_log) - 1);
+  const int64_t c = ((int64_t)(blockIdx.x % bx) * (1 << lc_log) + lane) * V;
+  const int64_t t0 =
+      ((int64_t)(blockIdx.x / bx) * (blockDim.x >> lc_log) + (threadIdx.x >> lc_log)) * run;
+  const int64_t b = blockIdx.y;
+  if (c >= C || t0 >= L) return;
+  const int64_t t1 = t0 + run < L ? t0 + run : L;
+  float wt[W][V], bs[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    bs[v] = bias ? bias[c + v] : 0.0f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) wt[k][v] = w[(c + v) * W + k];
+  }
+  typedef typename RawV<T, V>::type Raw;
+  const T* xp = x + b * xs.batch + c;
+  Raw win[W - 1];   // rows t - (W - 1) .. t - 1
+#pragma unroll
+  for (int k = 0; k < W - 1; ++k) {
+    const int64_t t = t0 - (W - 1) + k;
+    if (t >= 0)
+      win[k] = load_raw<T, V>(xp + t * xs.token);
+    else if (init)
+      win[k] = load_raw<T, V>(init + (b * (W - 1) + (t + W - 1)) * C + c);
+    else
+      win[k] = zero_raw<T, V>();
+  }
+  const PartRow<T> o = part_of<T>(y, b, L, c);
+  Raw next[kConvAhead];
+#pragma unroll
+  for (int a = 0; a < kConvAhead; ++a)
+    next[a] = t0 + a < t1 ? load_raw<T, V>(xp + (t0 + a) * xs.token) : zero_raw<T, V>();
+  for (int64_t t = t0; t < t1; t += kConvAhead) {
+    Raw cur[kConvAhead];
+#pragma unroll
+    for (int a = 0; a < kConvAhead; ++a) cur[a] = next[a];
+#pragma unroll
+    for (int a = 0; a < kConvAhead; ++a)
+      if (t + kConvAhead + a < t1) next[a] = load_raw<T, V>(xp + (t + kConvAhead + a) * xs.token);
+#pragma unroll
+    for (int a = 0; a < kConvAhead; ++a) {
+      if (t + a >= t1) break;
+      float u[V], r[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) u[v] = bs[v];
+#pragma unroll
+      for (int k = 0; k < W - 1; ++k) {
+        widen<T, V>(win[k], r);
+#pragma unroll
+        for (int v = 0; v < V; ++v) u[v] = fmaf(wt[k][v], r[v], u[v]);
+      }
+      widen<T, V>(cur[a], r);
+#pragma unroll
+      for (int v = 0; v < V; ++v) u[v] = fmaf(wt[W - 1][v], r[v], u[v]);
+      if (silu) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) u[v] *= sigmoid_f32(u[v]);
+      }
+      store_v<V>(o.p + (t + a) * o.ld, u);
+#pragma unroll
+      for (int k = 0; k + 1 < W - 1; ++k) win[k] = win[k + 1];
+      win[W - 2] = cur[a];
+    }
+  }
+  if (fin && t1 == L) {   // the run that ends the sequence holds the last W - 1 inputs
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k)
+      *reinterpret_cast<Raw*>(fin + (b * (W - 1) + k) * C + c) = win[k];
+  }
+}
+
+// Gradients.  A run of tokens [t0, t1) forms dx there (and, at the sequence's
+// start, the W - 1 rows of dinit) and adds its tokens to dw and dbias, which
+// needs du up to W - 1 tokens past the run.  The runs of a workgroup add up
+// their dw and dbias in LDS, in order, and leave one row of part sums
+// [W + 1][C] in the workspace; conv_reduce_kernel adds those rows in order, so the
+// same call gives the same bits.
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(kConvThreads)
+conv_bwd_kernel(const T* __restrict__ x, Strides xs, const float* __restrict__ w,
+                const float* __restrict__ bias, const T* __restrict__ init, ConvParts dy,
+                const T* __restrict__ dfin, T* __restrict__ dx, Strides dxs, T* __restrict__ dinit,
+                float* __restrict__ part, int silu, int64_t L, int64_t C, int64_t bx, int lc_log,
+                int64_t run) {
+  const int lanes = 1 << lc_log;
+  const int lane = threadIdx.x & (lanes - 1);
+  const int row = threadIdx.x >> lc_log;
+  const int rows = blockDim.x >> lc_log;
+  const int64_t c0 = (int64_t)(blockIdx.x % bx) * lanes * V;   // the workgroup's first channel
+  const int64_t c = c0 + lane * V;
+  const int64_t tile = blockIdx.x / bx;
+  const int64_t t0 = (tile * rows + row) * run;
+  const int64_t b = blockIdx.y;
+  typedef typename RawV<T, V>::type Raw;
+  float dw[W][V], db[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    db[v] = 0.0f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) dw[k][v] = 0.0f;
+  }
+  if (c < C && t0 < L) {
+    const int64_t t1 = t0 + run < L ? t0 + run : L;
+    float wt[W][V], bs[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      bs[v] = bias ? bias[c + v] : 0.0f;
+#pragma unroll
+      for (int k = 0; k < W; ++k) wt[k][v] = w[(c + v) * W + k];
+    }
+    const T* xp = x + b * xs.batch + c;
+    T* dxp = dx + b * dxs.batch + c;
+    const PartRow<const T> g = part_of<const T>(dy, b, L, c);
+    float xw[W - 1][V], gw[W - 1][V];   // the W - 1 rows of x and of du before the current one
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+      const int64_t t = t0 - (W - 1) + k;
+      Raw r = zero_raw<T, V>();
+      if (t >= 0)
+        r = load_raw<T, V>(xp + t * xs.token);
+      else if (init)
+        r = load_raw<T, V>(init + (b * (W - 1) + (t + W - 1)) * C + c);
+      widen<T, V>(r, xw[k]);
+#pragma unroll
+      for (int v = 0; v < V; ++v) gw[k][v] = 0.0f;
+    }
+    const int64_t first = t0 == 0 ? -(int64_t)(W - 1) : t0;   // first row of dx (or dinit) formed here
+    Raw xn = load_raw<T, V>(xp + t0 * xs.token), gn = load_raw<T, V>(g.p + t0 * g.ld);
+    for (int64_t t = t0; t < t1 + W - 1; ++t) {
+      const Raw xr = xn, gr = gn;
+      if (t + 1 < L && t + 1 < t1 + W - 1) {
+        xn = load_raw<T, V>(xp + (t + 1) * xs.token);
+        gn = load_raw<T, V>(g.p + (t + 1) * g.ld);
+      }
+      float xc[V], du[V];
+#pragma unroll
+      for (int v = 0; v < V; ++v) xc[v] = du[v] = 0.0f;
+      if (t < L) {
+        float gc[V];
+        widen<T, V>(xr, xc);
+        widen<T, V>(gr, gc);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float u = fmaf(wt[W - 1][v], xc[v], bs[v]);
+#pragma unroll
+          for (int k = 0; k < W - 1; ++k) u = fmaf(wt[k][v], xw[k][v], u);
+          du[v] = silu ? gc[v] * silu_slope(u, sigmoid_f32(u)) : gc[v];
+        }
+        if (t < t1) {
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            db[v] += du[v];
+            dw[W - 1][v] = fmaf(du[v], xc[v], dw[W - 1][v]);
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) dw[k][v] = fmaf(du[v], xw[k][v], dw[k][v]);
+          }
+        }
+      }
+      // row s = t - (W - 1) of dx takes du[s .. s + W - 1] = gw[0 .. W - 2], du
+      const int64_t s = t - (W - 1);
+      if (s >= first && s < t1) {
+        float o[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          o[v] = wt[0][v] * du[v];
+#pragma unroll
+          for (int k = 0; k < W - 1; ++k) o[v] = fmaf(wt[W - 1 - k][v], gw[k][v], o[v]);
+        }
+        const int64_t f = s - (L - (W - 1));   // this input's row in the final state
+        if (dfin && f >= 0) {
+          float d[V];
+          load_v<V>(dfin + (b * (W - 1) + f) * C + c, d);
+#pragma unroll
+          for (int v = 0; v < V; ++v) o[v] += d[v];
+        }
+        if (s >= 0)
+          store_v<V>(dxp + s * dxs.token, o);
+        else if (dinit)
+          store_v<V>(dinit + (b * (W - 1) + s + (W - 1)) * C + c, o);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int k = 0; k + 1 < W - 1; ++k) {
+          xw[k][v] = xw[k + 1][v];
+          gw[k][v] = gw[k + 1][v];
+        }
+        xw[W - 2][v] = xc[v];
+        gw[W - 2][v] = du[v];
+      }
+    }
+  }
+  __shared__ float sums[kConvThreads][V];
+  float* out = part + (b * (gridDim.x / bx) + tile) * (W + 1) * C;
+#pragma unroll
+  for (int k = 0; k <= W; ++k) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) sums[threadIdx.x][v] = k < W ? dw[k < W ? k : 0][v] : db[v];
+    __syncthreads();
+    for (int i = threadIdx.x; i < lanes * V; i += blockDim.x) {
+      const int64_t cc = c0 + i;
+      if (cc < C) {
+        float s = 0.0f;
+        for (int r = 0; r < rows; ++r) s += sums[r * lanes + i / V][i % V];
+        out[k * C + cc] = s;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// dweight [C, W] and dbias [C] from `n` rows of part sums [W + 1][C]: a
+// workgroup takes 64 of the (W + 1) C columns, four waves every fourth row.
+__global__ void __launch_bounds__(256)
+conv_reduce_kernel(const float* __restrict__ part, int64_t n, int64_t C, int W,
+                   float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ double sums[4][64];
+  const int64_t cols = (W + 1) * C;
+  const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x % 64;
+  double s = 0.0;
+  if (i < cols)
+    for (int64_t r = threadIdx.x / 64; r < n; r += 4) s += (double)part[r * cols + i];
+  sums[threadIdx.x / 64][threadIdx.x % 64] = s;
+  __syncthreads();
+  if (threadIdx.x < 64 && i < cols) {
+    const double v = (sums[0][threadIdx.x] + sums[1][threadIdx.x]) +
+                     (sums[2][threadIdx.x] + sums[3][threadIdx.x]);
+    const int64_t k = i / C, c = i % C;
+    if (k < W)
+      dw[c * W + k] = (float)v;
+    else if (db)
+      db[c] = (float)v;
+  }
+}
+
+// ---- host ----
+
+namespace {
+
+struct ConvGrid {
+  int lc_log, rows;     // lanes along the channels (their log2) and runs per workgroup
+  int64_t run, bx, by;  // tokens per run; workgroups along the channels and the tokens
+  int threads() const { return rows << lc_log; }
+};
+
+// Lanes along the channels and tokens per run.  Runs are long (fewer
+// overlapping rows) as long as the launch keeps `enough` waves.
+ConvGrid conv_grid(int64_t batch, int64_t L, int64_t C, int V, int longest, int64_t enough) {
+  ConvGrid g;
+  const int64_t cv = (C + V - 1) / V;
+  g.lc_log = 0;
+  while (g.lc_log < 6 && (int64_t(1) << g.lc_log) < cv) ++g.lc_log;
+  g.bx = (cv + (int64_t(1) << g.lc_log) - 1) >> g.lc_log;
+  g.run = longest;
+  while (g.run > 4 && batch * g.bx * (int64_t(1) << g.lc_log) * ((L + g.run - 1) / g.run) < enough * 64)
+    g.run /= 2;
+  g.by = 1;
+  g.rows = kConvThreads >> g.lc_log;
+  const int64_t runs = (L + g.run - 1) / g.run;
+  while (g.rows > 1 && g.rows / 2 >= runs && g.threads() > 64) g.rows /= 2;
+  g.by = (runs + g.rows - 1) / g.rows;
+  return g;
+}
+constexpr int kConvBwdRun = 64;
+ConvGrid conv_bwd_grid(int64_t batch, int64_t L, int64_t C, int V) {
+  return conv_grid(batch, L, C, V, kConvBwdRun, 4096);
+}
+
+}  // namespace
+
+size_t conv_bwd_workspace(int64_t batch, int64_t L, int64_t C, int W, int io_bf16) {
+  // either vector width may be taken, by the call's pointers and strides
+  size_t most = 0;
+  for (int V : {1, io_bf16 ? 8 : 4}) {
+    const ConvGrid g = conv_bwd_grid(batch, L, C, V);
+    const size_t n = size_t(batch) * g.by * (W + 1) * C * sizeof(float);
+    if (n > most) most = n;
+  }
+  return most;
+}
+
+// Every launch has fewer than 2^32 threads along x (V = 1 has the most).
+int conv_grid_ok(int64_t batch, int64_t L, int64_t C) {
+  if (batch > 65535 || C > (1 << 24) || L > (int64_t(1) << 32)) return 0;
+  const ConvGrid g = conv_grid(batch, L, C, 1, 32, 4096);
+  return (__int128)g.bx * g.by * kConvThreads < (int64_t(1) << 32);
+}
+
+template <typename T, int V>
+static hipError_t conv_fwd_v(const ConvArgs& a, hipStream_t stream) {
+  ConvGrid g = conv_grid(a.batch, a.L, a.C, V, 32, 4096);
+  if (a.one_run) {   // the state is updated in place: one thread per (b, c) reads and writes it
+    g.run = a.L;
+    g.by = 1;
+    g.rows = g.lc_log < 6 ? 64 >> g.lc_log : 1;
+  }
+  const ConvParts y{{a.y[0], a.y[1], a.y[2]}, {a.end[0], a.end[1], a.end[2]}};
+  const dim3 grid((unsigned)(g.bx * g.by), (unsigned)a.batch);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(g.threads()), 0, stream, static_cast<const T*>(a.x),
+                       Strides{a.xs[0], a.xs[1]}, a.w, a.bias, static_cast<const T*>(a.init), y,
+                       static_cast<T*>(a.fin), a.silu, a.L, a.C, g.bx, g.lc_log, g.run);
+  };
+  if (a.W == 2) go(conv_fwd_kernel<T, V, 2>);
+  else if (a.W == 3) go(conv_fwd_kernel<T, V, 3>);
+  else go(conv_fwd_kernel<T, V, 4>);
+  return hipGetLastError();
+}
+
+hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t stream) {
+  if (a.bf16)
+    return a.vec ? conv_fwd_v<bf16, 8>(a, stream) : conv_fwd_v<bf16, 1>(a, stream);
+  return a.vec ? conv_fwd_v<float, 4>(a, stream) : conv_fwd_v<float, 1>(a, stream);
+}
+
+template <typename T, int V>
+static hipError_t conv_bwd_v(const ConvArgs& a, hipStream_t stream) {
+  const ConvGrid g = conv_bwd_grid(a.batch, a.L, a.C, V);
+  const ConvParts dy{{a.y[0], a.y[1], a.y[2]}, {a.end[0], a.end[1], a.end[2]}};
+  const dim3 grid((unsigned)(g.bx * g.by), (unsigned)a.batch);
+  float* part = static_cast<float*>(a.workspace);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, grid, dim3(g.threads()), 0, stream, static_cast<const T*>(a.x),
+                       Strides{a.xs[0], a.xs[1]}, a.w, a.bias, static_cast<const T*>(a.init), dy,
+                       static_cast<const T*>(a.dfin), static_cast<T*>(a.dx),
+                       Strides{a.dxs[0], a.dxs[1]}, static_cast<T*>(a.dinit), part, a.silu, a.L,
+                       a.C, g.bx, g.lc_log, g.run);
+  };
+  if (a.W == 2) go(conv_bwd_kernel<T, V, 2>);
+  else if (a.W == 3) go(conv_bwd_kernel<T, V, 3>);
+  else go(conv_bwd_kernel<T, V, 4>);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t cols = (a.W + 1) * a.C;
+  hipLaunchKernelGGL(conv_reduce_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, stream,
+                     part, a.batch * g.by, a.C, (int)a.W, a.dw, a.db);
+  return hipGetLastError();
+}
+
+hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t stream) {
+  if (a.bf16)
+    return a.vec ? conv_bwd_v<bf16, 8>(a, stream) : conv_bwd_v<bf16, 1>(a, stream);
+  return a.vec ? conv_bwd_v<float, 4>(a, stream) : conv_bwd_v<float, 1>(a, stream);
+}
+
+}  // namespace ssd

@@ -1,0 +1,504 @@
+// selscan_bwd.hip -- gradients of the selective scan.
+//
+// With ds_t = dy_t z_t sigmoid(z_t) (dy without z), a_t = exp(dt_t A) and g_t the
+// gradient of the loss with respect to h_t:
+//     g_t = ds_t C_t + a_{t+1} g_{t+1}          (dfinal enters after the last token)
+//     q_t = sum_n g_t B_t,   r_t = sum_n A a_t g_t h_{t-1}
+//     dx_t = dt_t q_t + D ds_t,                 ddt_t = (x_t q_t + r_t) d(dt)/d(raw)
+//     dB_t[g] = sum_c dt_t x_t g_t,             dC_t[g] = sum_c ds_t h_t
+//     dA = sum_t dt_t a_t g_t h_{t-1},          dD = sum_t ds_t x_t
+//     dz_t = dy_t s_t silu'(z_t)                dinit = a_0 g_0
+//
+// The states are needed from the last token to the first.  Chunks of T tokens:
+// selscan_kernel<both> and its chains (selscan.hip) give each chunk's start state
+// and the gradient at its end; selscan_bwd_kernel then walks one chunk forwards,
+// leaving the state every 8 tokens in LDS, and backwards 8 tokens at a time,
+// forming their states and decays again in registers.  Each decay is formed
+// three times in all; keeping the states of all tokens would move 4 N bytes per (t, c),
+// 64 at dstate 16 against the 14 that the gradients themselves move.
+//
+// dB and dC are sums over channels: over the lane groups of a wave by lane
+// swaps, over a workgroup's waves in LDS, and over workgroups by
+// selscan_reduce_bc_kernel from the workspace, each in a fixed order.  dA, dD
+// and the bias gradient are sums over tokens: per chunk in registers, then over
+// chunks by selscan_reduce_a_kernel.
+#include <type_traits>
+
+#include "layer_host.hpp"
+#include "selscan_device.hpp"
+
+namespace ssd {
+
+constexpr int kBwdThreads = 256;
+constexpr int kBwdWaves = kBwdThreads / kWave;
+constexpr int kSub = 8;             // tokens whose states are held in registers
+constexpr int kPairs = kSub / 2;    // lanes prepare two tokens of two channels at a time
+
+// Tokens per chunk: the checkpoints of all of it share LDS with its B and C.
+__host__ __device__ constexpr int bwd_tokens(int RN) { return RN == 16 ? 32 : 64; }
+// Floats of one checkpoint of a wave (8 per lane), which the 8 tokens' 16 NP sums
+// of dB and dC replace once they are formed.
+__host__ __device__ constexpr int bwd_slot(int RN) { return 16 * 4 * RN > 512 ? 16 * 4 * RN : 512; }
+constexpr int bwd_smem_floats(int RN) {
+  return bwd_tokens(RN) * 4 * RN * 2 + kBwdWaves * (bwd_tokens(RN) / kSub) * bwd_slot(RN);
+}
+
+template <typename T>
+struct ScanBwdIo {
+  const T *x, *dt;
+  const float* A;
+  const T* B;
+  Strides bs;
+  const T* C;
+  Strides cs;
+  const float* Dv;
+  const T* z;
+  Strides zs;
+  const T* dy;
+  const float* init;
+  const float *H, *R;   // [batch][K][D][NP]
+  float* dApart;        // [batch][K][D][NP]: H's slots, each read before it is written
+  float *dDpart, *dbpart;   // [batch][K][D]
+  float* bcpart;        // [batch][L][G][tiles][2][NP]
+  T *dx, *ddt, *dz;
+  Strides dzs;
+  float* dinit;
+  DtXform xf;
+};
+
+template <typename T, int RN, bool GATE>
+__global__ void __launch_bounds__(kBwdThreads, 2)
+selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
+  constexpr int NP = 4 * RN, CW = 128 / RN, TB = bwd_tokens(RN), SUBS = TB / kSub;
+  constexpr int SLOT = bwd_slot(RN);
+  extern __shared__ float smem[];
+  float* const sB = smem;                 // [TB][NP]
+  float* const sC = smem + TB * NP;       // [TB][NP]
+  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  float* const slots = smem + 2 * TB * NP + wave * SUBS * SLOT;   // [SUBS][SLOT], this wave's
+  const int64_t tile = blockIdx.x % (sh.tiles * sh.G);
+  const int64_t k = blockIdx.x / (sh.tiles * sh.G);
+  const int64_t b = blockIdx.y;
+  const int64_t g = tile / sh.tiles;
+  const int64_t base = ((tile % sh.tiles) * kBwdWaves + wave) * CW;
+  const bool live = base < sh.Dg;
+  const int nl = lane % RN, dl = lane / RN, n0 = 4 * nl;
+  const int par = (lane >> 1) & 1;                   // which token of a pair this lane prepares
+  const int64_t own = base + dl * 2 + (lane & 1);    // and which channel
+  const int64_t c = g * sh.Dg + (own < sh.Dg ? own : sh.Dg - 1);
+  const bool mine = own < sh.Dg && nl < 4;
+  const int64_t t0 = k * TB, t1 = t0 + TB < sh.L ? t0 + TB : sh.L;
+
+  {
+    const T* Bp = io.B + b * io.bs.batch + g * sh.N;
+    const T* Cp = io.C + b * io.cs.batch + g * sh.N;
+    for (int i = tid; i < TB * NP; i += kBwdThreads) {
+      const int64_t tok = t0 + i / NP;
+      const int n = i % NP;
+      const bool in = tok < t1 && n < sh.N;
+      sB[i] = in ? to_f32(Bp[tok * io.bs.token + n]) : 0.0f;
+      sC[i] = in ? to_f32(Cp[tok * io.cs.token + n]) : 0.0f;
+    }
+  }
+  __syncthreads();
+
+  if (live) {
+    float A2[2][4], h[2][4], gr[2][4], dA[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t lc = base + dl * 2 + j;
+      const int64_t cj = g * sh.Dg + (lc < sh.Dg ? lc : sh.Dg - 1);
+      const int64_t at = ((b * sh.K + k) * sh.D + cj) * NP + n0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int n = n0 + i;
+        A2[j][i] = n < sh.N ? io.A[cj * sh.N + n] * kLog2e : 0.0f;
+        h[j][i] = k > 0 ? io.H[at + i]
+                        : io.init && n < sh.N ? io.init[(b * sh.D + cj) * sh.N + n] : 0.0f;
+        gr[j][i] = io.R[at + i];
+        dA[j][i] = 0.0f;
+      }
+    }
+    const DtLane f = dt_lane(io.xf, c);
+    const float Dc = io.Dv ? io.Dv[c] : 0.0f;
+    float dD = 0.0f, dbias = 0.0f;
+    const int64_t row = b * sh.L;
+    const T* xp = io.x + row * sh.D + c;
+    const T* dp = io.dt + row * sh.D + c;
+    const T* gp = io.dy + row * sh.D + c;
+    const T* zp = GATE ? io.z + b * io.zs.batch + c : nullptr;
+    const int subs = (int)((t1 - t0 + kSub - 1) / kSub);
+
+    // forwards, one checkpoint per 8 tokens
+    T xr[kPairs], dr[kPairs], zr[kPairs], yr[kPairs];
+    auto load = [&](int s, bool all) {
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) {
+        const int64_t t = t0 + s * kSub + 2 * p + par;
+        const int64_t tok = t < t1 ? t : t1 - 1;
+        xr[p] = xp[tok * sh.D];
+        dr[p] = dp[tok * sh.D];
+        if (all) {
+          yr[p] = gp[tok * sh.D];
+          if constexpr (GATE) zr[p] = zp[tok * io.zs.token];
+        }
+      }
+    };
+    load(0, false);
+    for (int s = 0; s < subs; ++s) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        *reinterpret_cast<floatx4*>(slots + s * SLOT + (j * kWave + lane) * 4) =
+            floatx4{h[j][0], h[j][1], h[j][2], h[j][3]};
+      if (s + 1 == subs) break;
+      float d[kPairs], dx[kPairs];
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) {   // only the last 8 tokens can lie past the end
+        d[p] = dt_value(f, to_f32(dr[p]));
+        dx[p] = d[p] * to_f32(xr[p]);
+      }
+      if (s + 2 < subs) load(s + 1, false);
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) {
+        auto token = [&](auto Q) {
+          constexpr int q = decltype(Q)::value;
+          const floatx4 Bv = *reinterpret_cast<const floatx4*>(sB + (s * kSub + 2 * p + q) * NP + n0);
+          const float d0 = quad_bcast<2 * q>(d[p]), d1 = quad_bcast<2 * q + 1>(d[p]);
+          const float x0 = quad_bcast<2 * q>(dx[p]), x1 = quad_bcast<2 * q + 1>(dx[p]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            h[0][i] = fmaf(fast_exp2(d0 * A2[0][i]), h[0][i], x0 * Bv[i]);
+            h[1][i] = fmaf(fast_exp2(d1 * A2[1][i]), h[1][i], x1 * Bv[i]);
+          }
+        };
+        token(std::integral_constant<int, 0>{});
+        token(std::integral_constant<int, 1>{});
+      }
+    }
+
+    // backwards, 8 tokens at a time
+    load(subs - 1, true);
+    for (int s = subs - 1; s >= 0; --s) {
+      float* const slot = slots + s * SLOT;
+      float h0[2][4], hist[kSub][2][4], dec[kSub][2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const floatx4 v = *reinterpret_cast<const floatx4*>(slot + (j * kWave + lane) * 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h0[j][i] = v[i];
+      }
+      wave_sync();   // other lanes' sums will be written over this checkpoint
+      float d[kPairs], dx[kPairs], ds[kPairs], xv[kPairs], raw[kPairs], yv[kPairs], zv[kPairs];
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) {
+        // past the last token and past the group's last channel nothing is added
+        const bool in = t0 + s * kSub + 2 * p + par < t1 && own < sh.Dg;
+        xv[p] = to_f32(xr[p]);
+        raw[p] = to_f32(dr[p]);
+        yv[p] = in ? to_f32(yr[p]) : 0.0f;
+        zv[p] = GATE ? to_f32(zr[p]) : 0.0f;
+        d[p] = in ? dt_value(f, raw[p]) : 0.0f;
+        dx[p] = in ? d[p] * xv[p] : 0.0f;
+        ds[p] = GATE ? yv[p] * (zv[p] * sigmoid_f32(zv[p])) : yv[p];
+      }
+      if (s > 0) load(s - 1, true);
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) {
+        float yp[4];
+        auto token = [&](auto Q) {
+          constexpr int q = decltype(Q)::value;
+          const int t = 2 * p + q;
+          const floatx4 Bv = *reinterpret_cast<const floatx4*>(sB + (s * kSub + t) * NP + n0);
+          const floatx4 Cv = *reinterpret_cast<const floatx4*>(sC + (s * kSub + t) * NP + n0);
+          const float dj[2] = {quad_bcast<2 * q>(d[p]), quad_bcast<2 * q + 1>(d[p])};
+          const float xj[2] = {quad_bcast<2 * q>(dx[p]), quad_bcast<2 * q + 1>(dx[p])};
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float y = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              dec[t][j][i] = fast_exp2(dj[j] * A2[j][i]);
+              hist[t][j][i] = fmaf(dec[t][j][i], t ? hist[t ? t - 1 : 0][j][i] : h0[j][i], xj[j] * Bv[i]);
+              if constexpr (GATE) y = fmaf(Cv[i], hist[t][j][i], y);
+            }
+            yp[2 * q + j] = y;
+          }
+        };
+        token(std::integral_constant<int, 0>{});
+        token(std::integral_constant<int, 1>{});
+        if constexpr (GATE) {
+          const float o = fmaf(Dc, xv[p], quads_sum<RN>(quad_fold(yp, lane)));
+          const int64_t t = t0 + s * kSub + 2 * p + par;
+          const float sg = sigmoid_f32(zv[p]);
+          if (mine && t < t1)
+            io.dz[b * io.dzs.batch + t * io.dzs.token + c] = to_io<T>(yv[p] * o * silu_slope(zv[p], sg));
+        }
+      }
+#pragma unroll
+      for (int p = kPairs - 1; p >= 0; --p) {
+        float vq[4], vr[4], vB[8], vC[8];
+        auto token = [&](auto Q) {
+          constexpr int q = decltype(Q)::value;
+          const int t = 2 * p + q;
+          const floatx4 Bv = *reinterpret_cast<const floatx4*>(sB + (s * kSub + t) * NP + n0);
+          const floatx4 Cv = *reinterpret_cast<const floatx4*>(sC + (s * kSub + t) * NP + n0);
+          const float dj[2] = {quad_bcast<2 * q>(d[p]), quad_bcast<2 * q + 1>(d[p])};
+          const float xj[2] = {quad_bcast<2 * q>(dx[p]), quad_bcast<2 * q + 1>(dx[p])};
+          const float sj[2] = {quad_bcast<2 * q>(ds[p]), quad_bcast<2 * q + 1>(ds[p])};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vB[4 * q + i] = vC[4 * q + i] = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float qs = 0.0f, rs = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float gt = fmaf(sj[j], Cv[i], gr[j][i]);
+              vC[4 * q + i] = fmaf(sj[j], hist[t][j][i], vC[4 * q + i]);
+              vB[4 * q + i] = fmaf(xj[j], gt, vB[4 * q + i]);
+              qs = fmaf(gt, Bv[i], qs);
+              const float ag = dec[t][j][i] * gt;
+              const float flow = ag * (t ? hist[t ? t - 1 : 0][j][i] : h0[j][i]);
+              dA[j][i] = fmaf(dj[j], flow, dA[j][i]);
+              rs = fmaf(A2[j][i], flow, rs);
+              gr[j][i] = ag;
+            }
+            vq[2 * q + j] = qs;
+            vr[2 * q + j] = rs;
+          }
+        };
+        token(std::integral_constant<int, 1>{});
+        token(std::integral_constant<int, 0>{});
+        const float qv = quads_sum<RN>(quad_fold(vq, lane));
+        const float rv = quads_sum<RN>(quad_fold(vr, lane)) * 0.6931471805599453f;   // A2 = A log2 e
+        const int64_t t = t0 + s * kSub + 2 * p + par;
+        if (t < t1) {
+          const float ddt = fmaf(xv[p], qv, rv) * dt_slope(f, raw[p]);
+          dbias += ddt;
+          dD = fmaf(ds[p], xv[p], dD);
+          if (mine) {
+            io.dx[(row + t) * sh.D + c] = to_io<T>(fmaf(d[p], qv, Dc * ds[p]));
+            io.ddt[(row + t) * sh.D + c] = to_io<T>(ddt);
+          }
+        }
+        // the wave's sums over channels: the lower half of the wave gets the pair's
+        // first token, even rows states 0 and 1 of the four, odd rows 2 and 3
+        auto channels = [&](const float (&v)[8], int which) {
+          float w[4], o[2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = halves_fold(v[i], v[4 + i]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            o[i] = rows_fold(w[i], w[i + 2]);
+            if constexpr (RN <= 8) o[i] += dpp_move<0x128>(o[i]);   // row_ror:8
+            if constexpr (RN <= 4) o[i] += dpp_move<0x124>(o[i]);   // row_ror:4
+          }
+          const int tok = 2 * p + (lane >> 5);
+          if ((lane & 15) < RN) {
+            float* q = slot + (tok * 2 + which) * NP + n0 + ((lane >> 4) & 1) * 2;
+            q[0] = o[0];
+            q[1] = o[1];
+          }
+        };
+        channels(vB, 0);
+        channels(vC, 1);
+      }
+    }
+
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t lc = base + dl * 2 + j;
+      if (lc >= sh.Dg) continue;
+      const int64_t cj = g * sh.Dg + lc;
+      *reinterpret_cast<floatx4*>(io.dApart + ((b * sh.K + k) * sh.D + cj) * NP + n0) =
+          floatx4{dA[j][0], dA[j][1], dA[j][2], dA[j][3]};
+      if (k == 0 && io.dinit)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n0 + i < sh.N) io.dinit[(b * sh.D + cj) * sh.N + n0 + i] = gr[j][i];
+    }
+    dD += dpp_move<0x4E>(dD);         // both tokens of the pairs
+    dbias += dpp_move<0x4E>(dbias);
+    if (mine && par == 0) {
+      io.dDpart[(b * sh.K + k) * sh.D + c] = dD;
+      io.dbpart[(b * sh.K + k) * sh.D + c] = dbias;
+    }
+  }
+  __syncthreads();
+  // the workgroup's sums of dB and dC: live waves in order
+  const int64_t left = sh.Dg - (tile % sh.tiles) * kBwdWaves * CW;
+  const int waves = left >= kBwdWaves * CW ? kBwdWaves : (int)((left + CW - 1) / CW);
+  for (int i = tid; i < (int)(t1 - t0) * 2 * NP; i += kBwdThreads) {
+    const int tok = i / (2 * NP), e = i % (2 * NP);
+    const float* q = smem + 2 * TB * NP + (tok / kSub) * SLOT + (tok % kSub) * 2 * NP + e;
+    float v = 0.0f;
+    for (int w = 0; w < waves; ++w) v += q[w * SUBS * SLOT];
+    io.bcpart[(((b * sh.L + t0 + tok) * sh.G + g) * sh.tiles + tile % sh.tiles) * 2 * NP + e] = v;
+  }
+}
+
+// dB and dC [batch, L, G, N] from the workgroups' sums, `tiles` for each (b, t, g).
+template <typename T>
+__global__ void __launch_bounds__(256)
+selscan_reduce_bc_kernel(const float* __restrict__ part, T* __restrict__ dB, T* __restrict__ dC,
+                         int64_t rows, int64_t tiles, int NP, int64_t N) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t r = i / (2 * NP);
+  const int e = (int)(i % (2 * NP)), n = e % NP;
+  if (r >= rows || n >= N) return;
+  float v = 0.0f;
+  for (int64_t t = 0; t < tiles; ++t) v += part[(r * tiles + t) * 2 * NP + e];
+  (e < NP ? dB : dC)[r * N + n] = to_io<T>(v);
+}
+
+// dA [D, N], dD [D] and the bias gradient [D] from `n` (batch x chunks) rows of sums.
+__global__ void __launch_bounds__(256)
+selscan_reduce_a_kernel(const float* __restrict__ dAp, const float* __restrict__ dDp,
+                        const float* __restrict__ dbp, int64_t n, int64_t D, int64_t N, int NP,
+                        float* __restrict__ dA, float* __restrict__ dD, float* __restrict__ db) {
+  __shared__ double sums[4][64];
+  const int64_t per = D * NP, cols = per + 2 * D;
+  const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x % 64;
+  double s = 0.0;
+  if (i < cols) {
+    const float* p = i < per ? dAp + i : i < per + D ? dDp + (i - per) : dbp + (i - per - D);
+    const int64_t ld = i < per ? per : D;
+    for (int64_t r = threadIdx.x / 64; r < n; r += 4) s += (double)p[r * ld];
+  }
+  sums[threadIdx.x / 64][threadIdx.x % 64] = s;
+  __syncthreads();
+  if (threadIdx.x >= 64 || i >= cols) return;
+  const float v = (float)((sums[0][threadIdx.x] + sums[1][threadIdx.x]) +
+                          (sums[2][threadIdx.x] + sums[3][threadIdx.x]));
+  if (i < per) {
+    if (i % NP < N) dA[i / NP * N + i % NP] = v;
+  } else if (i < per + D) {
+    if (dD) dD[i - per] = v;
+  } else if (db) {
+    db[i - per - D] = v;
+  }
+}
+
+// ---- host ----
+
+static ScanShape bwd_shape(int64_t L, int64_t D, int64_t N, int64_t G) {
+  ScanShape s;
+  const int rn = selscan_rn(N);
+  const int64_t per = 128 / rn * kBwdWaves;
+  s.L = L; s.D = D; s.N = N; s.G = G; s.Dg = D / G;
+  s.T = bwd_tokens(rn);
+  s.K = (L + s.T - 1) / s.T;
+  s.tiles = (s.Dg + per - 1) / per;
+  return s;
+}
+static size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
+
+struct ScanBwdLayout {
+  size_t h, r, sum, dd, db, bc, bytes;
+};
+static ScanBwdLayout bwd_layout(int64_t batch, const ScanShape& s) {
+  ScanBwdLayout w;
+  const size_t st = selscan_state_bytes(batch, s), sm = selscan_sum_bytes(batch, s);
+  w.h = 0;
+  w.r = st;
+  w.sum = 2 * st;
+  w.dd = w.sum + sm;
+  w.db = w.dd + sm;
+  w.bc = w.db + sm;
+  w.bytes = w.bc + up256(size_t(batch) * s.L * s.G * s.tiles * 8 * selscan_rn(s.N) * sizeof(float));
+  return w;
+}
+
+size_t selscan_bwd_workspace(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
+  return bwd_layout(batch, bwd_shape(L, D, N, G)).bytes;
+}
+
+// Whether every launch of the scan stays within a grid: workgroups along x
+// (channels x chunks, rows of the reductions), batches along y.
+int selscan_grid_ok(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
+  const ScanShape s = bwd_shape(L, D, N, G);
+  const __int128 most = (1 << 24) - 1;   // of 256 threads each: a launch has fewer than 2^32
+  const int np = 4 * selscan_rn(N);
+  return batch <= 65535 && (__int128)s.tiles * G * s.K <= most &&
+         (__int128)batch * L * G * 2 * np / 256 < most &&
+         (__int128)batch * D * np / 64 < most;
+}
+
+// The forward kernels tile channels more widely than the backward one.
+static ScanShape fwd_tiles(ScanShape s) {
+  const int64_t per = 256 / selscan_rn(s.N) * 4;
+  s.tiles = (s.Dg + per - 1) / per;
+  return s;
+}
+
+template <typename T, int RN, bool GATE>
+static hipError_t bwd_g(const ScanArgs& a, hipStream_t stream) {
+  const ScanShape s = bwd_shape(a.L, a.D, a.N, a.G);
+  const ScanBwdLayout w = bwd_layout(a.batch, s);
+  char* ws = static_cast<char*>(a.workspace);
+  float* H = reinterpret_cast<float*>(ws + w.h);
+  float* R = reinterpret_cast<float*>(ws + w.r);
+  hipError_t e = launch_selscan_both(a, fwd_tiles(s), H, R, reinterpret_cast<float*>(ws + w.sum), stream);
+  if (e != hipSuccess) return e;
+  ScanBwdIo<T> io{};
+  io.x = static_cast<const T*>(a.x);
+  io.dt = static_cast<const T*>(a.dt);
+  io.A = a.A;
+  io.B = static_cast<const T*>(a.B);
+  io.bs = {a.bs[0], a.bs[1]};
+  io.C = static_cast<const T*>(a.C);
+  io.cs = {a.cs[0], a.cs[1]};
+  io.Dv = a.Dv;
+  io.z = static_cast<const T*>(a.z);
+  io.zs = {a.zs[0], a.zs[1]};
+  io.dy = static_cast<const T*>(a.dy);
+  io.init = a.init;
+  io.H = H;
+  io.R = R;
+  io.dApart = H;
+  io.dDpart = reinterpret_cast<float*>(ws + w.dd);
+  io.dbpart = reinterpret_cast<float*>(ws + w.db);
+  io.bcpart = reinterpret_cast<float*>(ws + w.bc);
+  io.dx = static_cast<T*>(a.dx);
+  io.ddt = static_cast<T*>(a.ddt);
+  io.dz = static_cast<T*>(a.dz);
+  io.dzs = {a.dzs[0], a.dzs[1]};
+  io.dinit = a.dinit;
+  io.xf = a.xf ? *a.xf : DtXform{nullptr, 0, -INFINITY, INFINITY};
+  constexpr int smem = bwd_smem_floats(RN) * (int)sizeof(float);
+  e = ensure_dyn_lds<selscan_bwd_kernel<T, RN, GATE>>(smem);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((selscan_bwd_kernel<T, RN, GATE>),
+                     dim3((unsigned)(s.tiles * s.G * s.K), (unsigned)a.batch), dim3(kBwdThreads), smem,
+                     stream, io, s);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t rows = a.batch * a.L * a.G;
+  const int np = 4 * RN;
+  hipLaunchKernelGGL(selscan_reduce_bc_kernel<T>, dim3((unsigned)((rows * 2 * np + 255) / 256)), dim3(256),
+                     0, stream, io.bcpart, static_cast<T*>(a.dB), static_cast<T*>(a.dC), rows, s.tiles,
+                     np, a.N);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(selscan_reduce_a_kernel, dim3((unsigned)((a.D * (np + 2) + 63) / 64)), dim3(256), 0,
+                     stream, io.dApart, io.dDpart, io.dbpart, a.batch * s.K, a.D, a.N, np, a.dA, a.dD,
+                     a.dbias);
+  return hipGetLastError();
+}
+
+template <typename T, int RN>
+static hipError_t bwd_rn(const ScanArgs& a, hipStream_t stream) {
+  return a.z ? bwd_g<T, RN, true>(a, stream) : bwd_g<T, RN, false>(a, stream);
+}
+template <typename T>
+static hipError_t bwd_t(const ScanArgs& a, hipStream_t stream) {
+  const int rn = selscan_rn(a.N);
+  if (rn == 4) return bwd_rn<T, 4>(a, stream);
+  if (rn == 8) return bwd_rn<T, 8>(a, stream);
+  return bwd_rn<T, 16>(a, stream);
+}
+
+hipError_t launch_selscan_bwd(const ScanArgs& a, hipStream_t stream) {
+  return a.bf16 ? bwd_t<bf16>(a, stream) : bwd_t<float>(a, stream);
+}
+
+}  // namespace ssd

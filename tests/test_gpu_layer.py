@@ -1,0 +1,501 @@
+"""The operators around the scan against their fp64 references (oracle/layer.py), with
+the bounds derived in layer_util.py, and how they are used: together, token by
+token, on other streams, in captured graphs."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import state_space_sequence_03_amd as lib
+from layer_util import IO, Draw, cat, within
+from oracle import layer as ref
+
+pytestmark = pytest.mark.gpu
+f = ref.f64
+PLAIN = dict(memory_format=torch.contiguous_format)   # a copy of its own, at an aligned address
+
+
+@pytest.fixture(autouse=True)
+def need_gpu(gpu_available):
+    if not gpu_available:
+        pytest.skip("needs a GPU")
+
+
+# ---- convolution ----
+
+# batch, tokens, split, width, pad of the projection, io, state given, activation
+CONV = [
+    (1, 1, (8,), 4, 0, "bf16", False, True),
+    (1, 1, (8,), 4, 0, "fp32", True, True),
+    (2, 2, (16, 8, 8), 4, 8, "bf16", True, True),      # fewer tokens than the window
+    (2, 3, (5,), 4, 0, "bf16", True, True),            # no vector fits
+    (3, 37, (24, 16), 3, 3, "bf16", True, False),      # rows at odd offsets
+    (2, 130, (64, 32, 32), 4, 16, "bf16", False, True),
+    (1, 1030, (1,), 2, 0, "fp32", True, True),         # a single channel
+    (2, 517, (37,), 3, 1, "fp32", False, True),
+    (1, 260, (520,), 4, 0, "fp32", True, True),        # more channels than one workgroup's lanes
+    (5, 33, (528, 8, 8), 2, 24, "bf16", True, True),
+]
+
+
+def conv_case(case, seed=0):
+    Bz, L, split, W, pad, io, state, act = case
+    d, C = Draw(seed), sum(split)
+    x = d.rows(Bz, L, C, pad=pad, dtype=IO[io])
+    w, bias = d.normal(C, W, std=0.5), d.normal(C, std=0.3)
+    init = d.normal(Bz, W - 1, C, dtype=IO[io]) if state else None
+    return d, x, w, bias, init, (None if len(split) == 1 else split), "silu" if act else None
+
+
+@pytest.mark.parametrize("case", CONV, ids=str)
+def test_conv_fwd(case):
+    d, x, w, bias, init, split, act = conv_case(case)
+    y, fin = lib.ssd_conv_fwd(x, w, bias, init, split=split, activation=act, want_final_state=True)
+    yr, fr, _ = ref.conv(x, w, bias, init, act is not None)
+    mag, _, _ = ref.conv(f(x).__abs__(), f(w).__abs__(), f(bias).__abs__(),
+                         None if init is None else f(init).__abs__(), False)
+    within(cat(y), yr, 40, mag, "y")
+    assert np.array_equal(f(fin), fr)
+    y0, _ = lib.ssd_conv_fwd(x, w, None, None, split=split, activation=act)   # neither bias nor state
+    within(cat(y0), ref.conv(x, w, None, None, act is not None)[0], 40, mag, "y without bias")
+
+
+@pytest.mark.parametrize("case", CONV, ids=str)
+def test_conv_step_is_the_prompt_token_by_token(case):
+    d, x, w, bias, init, split, act = conv_case(case)
+    x = x[:, :40]
+    want, fin = lib.ssd_conv_fwd(x, w, bias, init, split=split, activation=act, want_final_state=True)
+    state = torch.zeros_like(fin) if init is None else init.clone()
+    got, t = [], 0
+    for n in (1, 1, 3, 2, 1, 64):      # tokens per call
+        if t < x.shape[1]:
+            got.append(cat(lib.ssd_conv_step(state, x[:, t:t + n], w, bias, split=split, activation=act)))
+        t += n
+    assert torch.equal(torch.cat(got, 1), cat(want)) and torch.equal(state, fin)
+
+
+@pytest.mark.parametrize("case", CONV, ids=str)
+def test_conv_bwd(case):
+    d, x, w, bias, init, split, act = conv_case(case)
+    dy = [d.normal(x.shape[0], x.shape[1], n, dtype=x.dtype) for n in case[2]]
+    dfin = d.normal(x.shape[0], w.shape[1] - 1, x.shape[2], dtype=x.dtype)
+    got = lib.ssd_conv_bwd(x, w, bias, init, dy if split else dy[0], dfin, activation=act, want_dinit=True)
+    dyc = cat(dy)
+    want = ref.conv_bwd(x, w, bias, init, dyc, dfin, act is not None)
+    a = lambda t: None if t is None else np.abs(f(t))
+    u, _, _ = ref.conv(a(x), a(w), a(bias), a(init), False)
+    mag = ref.conv_bwd(a(x), a(w), a(bias), a(init), a(dyc) * (1.1 + u), a(dfin), False)
+    for k, count in (("dx", 64), ("dinit", 64), ("dweight", 400), ("dbias", 400)):
+        within(got[k], want[k], count, mag[k], k)
+    again = lib.ssd_conv_bwd(x, w, bias, init, dy if split else dy[0], dfin, activation=act, want_dinit=True)
+    assert all(torch.equal(got[k], again[k]) for k in got)
+    bare = lib.ssd_conv_bwd(x, w, None, None, dy if split else dy[0], activation=act)
+    want = ref.conv_bwd(x, w, None, None, dyc, None, act is not None)
+    assert bare["dbias"] is None and bare["dinit"] is None
+    within(bare["dx"], want["dx"], 64, mag["dx"], "dx without bias and state")
+    within(bare["dweight"], want["dweight"], 400, mag["dweight"], "dweight without bias and state")
+
+
+# ---- selective scan ----
+
+# batch, tokens, channels, states, groups, io, gate, state given, D given, step size
+SCAN = [
+    (1, 1, 1, 1, 1, "fp32", False, False, False, "given"),
+    (1, 1, 64, 16, 1, "bf16", True, True, True, "softplus"),
+    (2, 7, 66, 16, 2, "fp32", True, True, True, "softplus"),
+    (1, 33, 40, 5, 1, "bf16", False, True, True, "clamped"),
+    (2, 129, 24, 16, 1, "fp32", True, False, True, "softplus"),     # two chunks, one of one token
+    (1, 700, 130, 16, 1, "bf16", True, True, True, "softplus"),
+    (1, 321, 34, 19, 2, "fp32", False, True, False, "given"),
+    (3, 200, 9, 32, 3, "fp32", True, True, True, "softplus"),
+    (1, 150, 20, 33, 1, "fp32", True, True, True, "softplus"),
+    (2, 140, 6, 64, 2, "bf16", True, False, True, "clamped"),
+    (1, 260, 1000, 8, 1, "fp32", False, True, True, "softplus"),    # several workgroups of channels
+    (40, 70, 1030, 4, 1, "bf16", True, False, True, "softplus"),    # one chunk, many batches
+]
+
+
+def scan_case(case, seed=0):
+    Bz, L, D, N, G, io, gate, state, skip, step = case
+    d = Draw(seed)
+    s = dict(x=d.normal(Bz, L, D, dtype=IO[io]), A=-d.uniform(0.3, 1.0 + N, D, N),
+             B=d.rows(Bz, L, G, N, pad=3, dtype=IO[io], std=N ** -0.5),
+             C=d.rows(Bz, L, G, N, pad=8, dtype=IO[io], std=N ** -0.5),
+             D=d.normal(D) if skip else None, z=d.rows(Bz, L, D, pad=D, dtype=IO[io]) if gate else None)
+    opt = {}
+    if step == "given":
+        s["dt"] = d.uniform(0.001, 0.3, Bz, L, D, dtype=IO[io])
+    elif step == "softplus":
+        s["dt"] = d.normal(Bz, L, D, dtype=IO[io], std=0.7)
+        opt = dict(dt_bias=d.uniform(-6.0, -1.0, D), dt_softplus=True)
+    else:
+        s["dt"] = d.uniform(0.0, 0.4, Bz, L, D, dtype=IO[io])
+        opt = dict(dt_limit=(0.05, 0.25))
+    init = d.normal(Bz, D, N) if state else None
+    return d, s, init, opt, dict(bias=opt.get("dt_bias"), softplus=opt.get("dt_softplus", False),
+                                 limit=opt.get("dt_limit"))
+
+
+def scan_mag(s):
+    m = {k: None if v is None else np.abs(f(v)) for k, v in s.items()}
+    m["dt"], m["A"], m["z"] = f(s["dt"]), f(s["A"]), None
+    return m
+
+
+@pytest.mark.parametrize("case", SCAN, ids=str)
+def test_scan_fwd(case):
+    d, s, init, opt, ropt = scan_case(case)
+    y, fin = lib.ssd_selscan_fwd(s["x"], s["dt"], s["A"], s["B"], s["C"], s["D"], s["z"], init, **opt)
+    yr, hr, _, _ = ref.selscan(**s, init=init, **ropt)
+    m = scan_mag(s)
+    ym, hm, _, _ = ref.selscan(**m, init=None if init is None else np.abs(f(init)), **ropt)
+    if s["z"] is not None:
+        ym = ym * np.abs(ref.silu(f(s["z"])))
+    count = 400 + 4 * case[1]
+    within(y, yr, count, ym, "y")
+    within(fin, hr, count, hm, "final state")
+    again, _ = lib.ssd_selscan_fwd(s["x"], s["dt"], s["A"], s["B"], s["C"], s["D"], s["z"], init,
+                                   want_final_state=False, **opt)
+    assert torch.equal(again, y)
+
+
+@pytest.mark.parametrize("case", SCAN, ids=str)
+def test_scan_step(case):
+    d, s, init, opt, ropt = scan_case(case)
+    L = min(case[1], 12)
+    s = {k: v[:, :L] if k in ("x", "dt", "B", "C", "z") and v is not None else v for k, v in s.items()}
+    state = torch.zeros(case[0], case[2], case[3], device="cuda") if init is None else init.clone()
+    got, t = [], 0
+    while t < L:      # calls of one, two, ... tokens
+        n = min(len(got) + 1, L - t)
+        cut = {k: v[:, t:t + n] if k in ("x", "dt", "B", "C", "z") and v is not None else v for k, v in s.items()}
+        got.append(lib.ssd_selscan_step(state, cut["x"].clone(**PLAIN),
+                                        cut["dt"].clone(**PLAIN), cut["A"], cut["B"],
+                                        cut["C"], cut["D"], cut["z"], **opt))
+        t += n
+    yr, hr, _, _ = ref.selscan(**s, init=init, **ropt)
+    ym, hm, _, _ = ref.selscan(**scan_mag(s), init=None if init is None else np.abs(f(init)), **ropt)
+    if s["z"] is not None:
+        ym = ym * np.abs(ref.silu(f(s["z"])))
+    within(torch.cat(got, 1), yr, 400 + 4 * L, ym, "y")
+    within(state, hr, 400 + 4 * L, hm, "state")
+
+
+@pytest.mark.parametrize("case", SCAN, ids=str)
+def test_scan_bwd(case):
+    d, s, init, opt, ropt = scan_case(case)
+    dy = d.normal(*s["x"].shape, dtype=s["x"].dtype)
+    dfin = d.normal(case[0], case[2], case[3]) if init is not None else None
+    call = lambda: lib.ssd_selscan_bwd(s["x"], s["dt"], s["A"], s["B"], s["C"], s["D"], s["z"], init, dy, dfin,
+                                       want_dinit=True, want_ddt_bias=True, **opt)
+    got = call()
+    want = ref.selscan_bwd(**s, init=init, dy=dy, dfinal=dfin, **ropt)
+    m = scan_mag(s)
+    m["z"] = f(s["z"])
+    a = lambda t: None if t is None else np.abs(f(t))
+    mag = ref.selscan_bwd(**m, init=a(init), dy=a(dy), dfinal=a(dfin), mag=True, **ropt)
+    if s["D"] is None:
+        assert got["dD"] is None
+    count = 800 + 8 * case[1]
+    for k, v in got.items():
+        if v is not None:
+            within(v, want[k], count, mag[k], k)
+    assert (got["dz"] is None) == (s["z"] is None)
+    again = call()
+    assert all(v is None or torch.equal(v, again[k]) for k, v in got.items())
+
+
+# ---- gated norm ----
+
+# batch, tokens, channels, groups, io, gate, pad, norm first
+NORM = [
+    (1, 1, 8, 1, "bf16", True, 0, False),
+    (1, 1, 5, 5, "fp32", True, 0, False),           # groups of one channel
+    (2, 3, 14, 2, "bf16", True, 1, True),           # nothing aligned
+    (2, 5, 48, 3, "bf16", True, 8, False),          # two pieces a group
+    (1, 17, 512, 8, "fp32", True, 4, False),
+    (3, 7, 1000, 1, "bf16", True, 16, False),
+    (1, 9, 1023, 1, "fp32", True, 0, True),
+    (2, 40, 1536, 1, "bf16", False, 0, False),
+    (1, 3, 5120, 1, "bf16", True, 48, False),
+    (1, 5, 16384, 2, "bf16", True, 0, True),        # the largest groups
+    (1, 3, 8192, 1, "fp32", True, 0, False),
+    (1, 3, 8191, 1, "bf16", True, 0, False),
+    (3, 700, 64, 1, "bf16", True, 0, False),
+    (1, 2100, 4096, 8, "bf16", True, 0, False),     # more rows than workgroups
+]
+
+
+def norm_case(case):
+    Bz, L, D, G, io, gate, pad, before = case
+    d = Draw(1)
+    x = d.normal(Bz, L, D, dtype=IO[io])
+    x[0, 0] = 0          # a row that only eps keeps from dividing by zero
+    return d, x, d.rows(Bz, L, D, pad=pad, dtype=IO[io]) if gate else None, d.uniform(0.5, 1.5, D), \
+        dict(ngroups=G, norm_before_gate=before), dict(groups=G, before=before)
+
+
+@pytest.mark.parametrize("case", NORM, ids=str)
+def test_norm_fwd(case):
+    d, x, z, w, opt, ropt = norm_case(case)
+    y = lib.ssd_gated_norm_fwd(x, z, w, **opt)
+    want = ref.gated_norm(x, z, w, **ropt)
+    within(y, want, 100, np.abs(want), "y")
+    want = ref.gated_norm(x, z, w, eps=0.5, **ropt)
+    within(lib.ssd_gated_norm_fwd(x, z, w, eps=0.5, **opt), want, 100, np.abs(want), "y with eps 0.5")
+
+
+@pytest.mark.parametrize("case", NORM, ids=str)
+def test_norm_bwd(case):
+    d, x, z, w, opt, ropt = norm_case(case)
+    dy = d.normal(*x.shape, dtype=x.dtype)
+    got = lib.ssd_gated_norm_bwd(x, z, w, dy, **opt)
+    want = ref.gated_norm_bwd(x, z, w, dy, **ropt)
+    # magnitudes: r |t| + |u| r^3 mean |t u|, times what du is multiplied by
+    xs, zs, ws, ds = f(x), f(z), f(w), f(dy)
+    gate, slope = (1.0, 0.0) if z is None else (np.abs(ref.silu(zs)), np.abs(ref.silu_slope(zs)))
+    u = np.abs(xs) if ropt["before"] else np.abs(xs) * gate
+    g = lambda v: v.reshape(v.shape[:2] + (ropt["groups"], -1))
+    r = 1.0 / np.sqrt((g(u) ** 2).mean(-1, keepdims=True) + 1e-5)
+    dn = np.abs(ds) * gate if ropt["before"] else np.abs(ds)
+    t = g(dn * ws)
+    du = (r * t + g(u) * r ** 3 * (t * g(u)).mean(-1, keepdims=True)).reshape(u.shape)
+    n = (g(u) * r).reshape(u.shape)
+    within(got["dx"], want["dx"], 200, du if ropt["before"] else du * gate, "dx")
+    within(got["dweight"], want["dweight"], 400, (dn * n).sum((0, 1)), "dweight")
+    if z is None:
+        assert got["dz"] is None
+    else:
+        mag = np.abs(ds) * ws * n * (slope + E_SLOPE) if ropt["before"] else du * np.abs(xs) * (slope + E_SLOPE)
+        within(got["dz"], want["dz"], 200, mag, "dz")
+    again = lib.ssd_gated_norm_bwd(x, z, w, dy, **opt)
+    assert all(v is None or torch.equal(v, again[k]) for k, v in got.items())
+
+
+E_SLOPE = 1.1   # the slope of SiLU is a difference of terms of up to 1.1
+
+
+# ---- as a layer uses them ----
+
+def layer_inputs(io="fp32", Bz=2, L=70, H=4, P=16, N=16, G=2):
+    d = Draw(11)
+    inner, side = H * P, G * N
+    proj = d.normal(Bz, L, 2 * inner + 2 * side + H, dtype=IO[io])
+    z, xbc = proj[..., :inner], proj[..., inner:2 * inner + 2 * side]
+    p = dict(w=d.normal(inner + 2 * side, 4, std=0.5), bias=d.normal(inner + 2 * side, std=0.2),
+             A=-d.uniform(0.5, 4.0, H), D=d.normal(H), norm=d.uniform(0.5, 1.5, inner),
+             dt=d.uniform(0.01, 0.3, Bz, L, H))
+    return d, proj, z, xbc, p, (inner, side, side), (Bz, L, H, P, N, G)
+
+
+def test_second_generation_layer_prompt_then_tokens():
+    d, proj, z, xbc, p, split, (Bz, L, H, P, N, G) = layer_inputs()
+
+    def mix(x, z, dt, scan):
+        y = scan(x[0].view(Bz, -1, H, P), dt, x[1].view(Bz, -1, G, N), x[2].view(Bz, -1, G, N))
+        return lib.ssd_gated_norm_fwd(y.view(Bz, -1, H * P), z, p["norm"], ngroups=G)
+
+    parts, conv_state = lib.ssd_conv_fwd(xbc, p["w"], p["bias"], split=split, want_final_state=True)
+    fin = {}
+
+    def prompt(x, dt, B, C):
+        y, fin["h"] = lib.ssd_fwd(x, dt, p["A"], B, C, p["D"], 32)
+        return y
+    whole = mix(parts, z, p["dt"], prompt)
+    # the same: a prompt of 50 tokens, then single ones
+    cut = 50
+    parts, cs = lib.ssd_conv_fwd(xbc[:, :cut], p["w"], p["bias"], split=split, want_final_state=True)
+    first = mix(parts, z[:, :cut], p["dt"][:, :cut].clone(**PLAIN), prompt)
+    h = fin["h"]
+    rest = []
+    for t in range(cut, L):
+        x1 = lib.ssd_conv_step(cs, xbc[:, t:t + 1], p["w"], p["bias"], split=split)
+        rest.append(mix(x1, z[:, t:t + 1], p["dt"][:, t:t + 1].clone(**PLAIN),
+                        lambda x, dt, B, C: lib.ssd_step(h, x, dt, p["A"], B, C, p["D"])))
+    got = torch.cat([first] + rest, 1)
+    # against the fp64 chain
+    xr, _, _ = ref.conv(xbc, p["w"], p["bias"], None)
+    r32 = lambda v, *s: torch.from_numpy(v.reshape(s)).float()
+    i, s = split[0], split[1]
+    yr, _, _ = oracle.recurrence(r32(xr[..., :i], Bz, L, H, P), p["dt"].cpu(), p["A"].cpu(),
+                                 r32(xr[..., i:i + s], Bz, L, G, N), r32(xr[..., i + s:], Bz, L, G, N),
+                                 p["D"].cpu(), None)
+    want = ref.gated_norm(yr.reshape(Bz, L, i), z, p["norm"], G)
+    for name, v in (("prompt", whole), ("tokens", got)):
+        err = np.abs(f(v) - want).max() / np.abs(want).max()
+        assert err < 1e-4, (name, err)      # fp32 io through ssd_fwd: its own bound, max-abs 1e-4
+    assert torch.equal(cs, conv_state)
+
+
+def test_second_generation_layer_gradients():
+    d, proj, z, xbc, p, split, (Bz, L, H, P, N, G) = layer_inputs()
+    i, s = split[0], split[1]
+    dout = d.normal(Bz, L, i)
+    (x, B, C), _ = lib.ssd_conv_fwd(xbc, p["w"], p["bias"], split=split)
+    xh, Bh, Ch = x.view(Bz, L, H, P), B.view(Bz, L, G, N), C.view(Bz, L, G, N)
+    y, _ = lib.ssd_fwd(xh, p["dt"], p["A"], Bh, Ch, p["D"], 32)
+    dproj = torch.zeros_like(proj)
+    n = lib.ssd_gated_norm_bwd(y.view(Bz, L, i), z, p["norm"], dout, ngroups=G, dz_out=dproj[..., :i])
+    g = lib.ssd_bwd(xh, p["dt"], p["A"], Bh, Ch, p["D"], 32, None, n["dx"].view(Bz, L, H, P))
+    c = lib.ssd_conv_bwd(xbc, p["w"], p["bias"], None,
+                         (g["dx"].view(Bz, L, i), g["dB"].view(Bz, L, s), g["dC"].view(Bz, L, s)),
+                         dx_out=dproj[..., i:2 * i + 2 * s])
+    assert not dproj[..., 2 * i + 2 * s:].any()      # the rest of the projection's gradient is untouched
+    # the fp64 chain, step by step
+    xr, _, _ = ref.conv(xbc, p["w"], p["bias"], None)
+    t = lambda v, *sh: torch.from_numpy(np.ascontiguousarray(v).reshape(sh)).float()
+    xo, Bo, Co = t(xr[..., :i], Bz, L, H, P), t(xr[..., i:i + s], Bz, L, G, N), t(xr[..., i + s:], Bz, L, G, N)
+    cpu = {k: v.cpu() for k, v in p.items()}
+    yr, _, _ = oracle.recurrence(xo, cpu["dt"], cpu["A"], Bo, Co, cpu["D"], None)
+    nr = ref.gated_norm_bwd(yr.reshape(Bz, L, i), z, p["norm"], dout, G)
+    gr = oracle.recurrence_bwd(xo, cpu["dt"], cpu["A"], Bo, Co, cpu["D"], None,
+                               t(nr["dx"], Bz, L, H, P), None)
+    cr = ref.conv_bwd(xbc, p["w"], p["bias"], None, np.concatenate(
+        [f(gr["dx"]).reshape(Bz, L, i), f(gr["dB"]).reshape(Bz, L, s), f(gr["dC"]).reshape(Bz, L, s)], 2))
+    pairs = [("dz", dproj[..., :i], nr["dz"]), ("dxbc", dproj[..., i:2 * i + 2 * s], cr["dx"]),
+             ("dnorm", n["dweight"], nr["dweight"]), ("dw", c["dweight"], cr["dweight"]),
+             ("dbias", c["dbias"], cr["dbias"]), ("dA", g["dA"], gr["dA"]), ("ddt", g["ddt"], gr["ddt"])]
+    for name, v, want in pairs:
+        assert v.stride() is not None
+        err = np.abs(f(v) - want).max() / np.abs(want).max()
+        assert err < 1e-4, (name, err)      # ssd_bwd's bound for fp32 io, max-abs 1e-4
+
+
+def test_first_generation_layer_prompt_then_tokens():
+    d = Draw(12)
+    Bz, L, D, N = 2, 200, 48, 16
+    proj = d.normal(Bz, L, 2 * D)
+    w, bias, A, Dv = d.normal(D, 4, std=0.5), d.normal(D, std=0.2), -d.uniform(0.3, 16, D, N), d.normal(D)
+    dt, dtb = d.normal(Bz, L, D, std=0.5), d.uniform(-5, -1, D)
+    bc = d.normal(Bz, L, 2 * N)
+    B, C = bc[..., :N].unflatten(2, (1, N)), bc[..., N:].unflatten(2, (1, N))
+    opt = dict(dt_bias=dtb, dt_softplus=True)
+    x, cs = lib.ssd_conv_fwd(proj[..., :D], w, bias, want_final_state=True)
+    whole, h = lib.ssd_selscan_fwd(x, dt, A, B, C, Dv, proj[..., D:], **opt)
+    xr, _, _ = ref.conv(proj[..., :D], w, bias)
+    want, hr, _, _ = ref.selscan(xr, dt, A, B, C, Dv, proj[..., D:], bias=dtb, softplus=True)
+    cs2 = torch.zeros_like(cs)
+    h2 = torch.zeros_like(h)
+    out = []
+    for t in range(L):
+        x1 = lib.ssd_conv_step(cs2, proj[:, t:t + 1, :D], w, bias)
+        out.append(lib.ssd_selscan_step(h2, x1, dt[:, t:t + 1].clone(**PLAIN), A, B[:, t:t + 1], C[:, t:t + 1], Dv,
+                                        proj[:, t:t + 1, D:], **opt))
+    assert torch.equal(cs, cs2)
+    for name, v, r in (("prompt", whole, want), ("tokens", torch.cat(out, 1), want), ("state", h, hr),
+                       ("state of tokens", h2, hr)):
+        err = np.abs(f(v) - r).max() / np.abs(r).max()
+        assert err < 3e-5, (name, err)       # (400 + 4 L) e = 7e-5 of the terms' magnitude, of which |ref| is a part
+
+
+# ---- streams, graphs, memory ----
+
+def all_calls(d, io="bf16"):
+    """Every entry point on small inputs: name -> call without arguments, and inputs to refresh."""
+    conv = conv_case((2, 130, (64, 32, 32), 4, 16, io, True, True))
+    _, s, init, opt, _ = scan_case((1, 700, 130, 16, 1, io, True, True, True, "softplus"))
+    _, x, z, w, nopt, _ = norm_case((2, 40, 1536, 1, io, True, 0, False))
+    _, cx, cw, cb, ci, split, act = conv
+    dys = [d.normal(2, 130, n, dtype=IO[io]) for n in split]
+    dy, ndy = d.normal(*s["x"].shape, dtype=IO[io]), d.normal(*x.shape, dtype=IO[io])
+    scan = [s[k] for k in ("x", "dt", "A", "B", "C", "D", "z")]
+    flat = lambda v: [t for t in (v.values() if isinstance(v, dict) else v) if t is not None]
+
+    def step(fn, state, *args, **kw):
+        state = state.clone()
+        y = fn(state, *args, **kw)
+        return (list(y) if isinstance(y, (list, tuple)) else [y]) + [state]
+    first = lambda v: v[:, :1].clone(**PLAIN)
+    return {
+        "conv_fwd": lambda: [t for t in lib.ssd_conv_fwd(cx, cw, cb, ci, split=split)[0]],
+        "conv_step": lambda: step(lib.ssd_conv_step, ci, cx[:, :1], cw, cb, split=split),
+        "conv_bwd": lambda: flat(lib.ssd_conv_bwd(cx, cw, cb, ci, dys, want_dinit=True)),
+        "scan_fwd": lambda: list(lib.ssd_selscan_fwd(*scan, init, **opt)),
+        "scan_step": lambda: step(lib.ssd_selscan_step, init, first(scan[0]), first(scan[1]), scan[2], scan[3][:, :1],
+                                  scan[4][:, :1], scan[5], scan[6][:, :1], **opt),
+        "scan_bwd": lambda: flat(lib.ssd_selscan_bwd(*scan, init, dy, init, want_dinit=True, want_ddt_bias=True, **opt)),
+        "norm_fwd": lambda: [lib.ssd_gated_norm_fwd(x, z, w, **nopt)],
+        "norm_bwd": lambda: flat(lib.ssd_gated_norm_bwd(x, z, w, ndy, **nopt)),
+    }, [cx, s["x"], x]
+
+
+@pytest.mark.parametrize("name", ["conv_fwd", "conv_step", "conv_bwd", "scan_fwd", "scan_step", "scan_bwd",
+                                  "norm_fwd", "norm_bwd"])
+def test_captured_graph_and_other_stream(name):
+    calls, inputs = all_calls(Draw(21))
+    call = calls[name]
+    want = call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = call()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, other))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        held = call()
+    for turn in range(4):      # new inputs, the program's own eager call, and a replay each time
+        for t in inputs:
+            t.mul_(-0.75)
+        want = call()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, held)), turn
+
+
+def test_two_graphs_side_by_side():
+    calls, _ = all_calls(Draw(22))
+    names = ("scan_bwd", "conv_bwd")
+    want, graphs, held = {}, {}, {}
+    for n in names:
+        want[n] = calls[n]()
+        graphs[n] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[n]):
+            held[n] = calls[n]()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for n, s in zip(names, streams):
+            with torch.cuda.stream(s):
+                graphs[n].replay()
+        torch.cuda.synchronize()
+        for n in names:
+            assert all(torch.equal(a, b) for a, b in zip(want[n], held[n])), n
+
+
+def test_rows_beside_strided_outputs_stay():
+    d = Draw(31)
+    Bz, L, D = 2, 9, 40
+    x, z, w, dy = (d.normal(Bz, L, D, dtype=torch.bfloat16) for _ in range(4))
+    wide = torch.full((Bz + 1, L + 2, D + 24), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = wide[1:, 1:L + 1, 8:8 + D]
+    lib.ssd_gated_norm_bwd(x, z, d.uniform(0.5, 1.5, D), dy, dz_out=out)
+    a = out.clone()
+    lib.ssd_conv_bwd(x, d.normal(D, 4), None, None, dy, dx_out=out)
+    A, B, dt = -d.uniform(0.5, 2, D, 4), d.normal(Bz, L, 1, 4, dtype=torch.bfloat16), d.uniform(0.1, 0.2, Bz, L, D, dtype=torch.bfloat16)
+    lib.ssd_selscan_bwd(x, dt, A, B, B, None, z, None, dy, dz_out=out)
+    assert not torch.equal(a, out)
+    out.fill_(7.0)
+    assert torch.equal(wide, torch.full_like(wide, 7.0))
+
+
+def test_offsets_past_32_bits():
+    # rows more than 2^31 elements apart: the second batch of a huge buffer
+    far = 2 ** 31 + 8 * 1000
+    store = torch.empty(far + 64 * 128, dtype=torch.bfloat16, device="cuda")
+    d = Draw(41)
+    Bz, L, D = 2, 40, 64
+    near = d.normal(Bz, L, D, dtype=torch.bfloat16)
+    x = store.as_strided((Bz, L, D), (far, 128, 1))
+    x.copy_(near)
+    w, dy = d.normal(D, 4), d.normal(Bz, L, D, dtype=torch.bfloat16)
+    assert torch.equal(lib.ssd_conv_fwd(x, w)[0], lib.ssd_conv_fwd(near, w)[0])
+    nw = d.uniform(0.5, 1.5, D)
+    assert torch.equal(lib.ssd_gated_norm_fwd(dy, x, nw), lib.ssd_gated_norm_fwd(dy, near, nw))
+    A, dt = -d.uniform(0.5, 2, D, 16), d.uniform(0.1, 0.2, Bz, L, D, dtype=torch.bfloat16)
+    B = x[..., :16].unflatten(2, (1, 16))
+    Bn = near[..., :16].unflatten(2, (1, 16))
+    a, b = (lib.ssd_selscan_fwd(dy, dt, A, q, q, None, v) for q, v in ((B, x), (Bn, near)))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    g = lib.ssd_conv_bwd(near, w, None, None, dy)["dx"]
+    lib.ssd_conv_bwd(near, w, None, None, dy, dx_out=x)
+    assert torch.equal(x, g)

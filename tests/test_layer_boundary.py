@@ -1,0 +1,257 @@
+"""Refusals of the operators around the scan (ssd_layer.h): host checks in the documented
+order, none of which reaches a kernel launch, so they run without a GPU."""
+import ctypes
+import os
+import re
+import subprocess
+
+import pytest
+import torch
+
+import state_space_sequence_03_amd as lib
+from state_space_sequence_03_amd import layer
+from test_host_asan import CLANG_RT, HIPCC, _instrumented, _run_child
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "ssd_layer.h")
+OK, NULLP, SHAPE, DTYPE, MISAL, WS, UNSUP, BADVAL = 0, 1, 2, 4, 5, 6, 7, 10
+PTR = 1 << 20      # 16-byte aligned, never dereferenced: a check fails first
+ODD = PTR + 2
+
+
+@pytest.fixture(scope="module", autouse=True)
+def so():
+    if not os.path.exists(lib.lib_path()):
+        from state_space_sequence_03_amd import build
+        build.build()
+    return lib.load_library()
+
+
+def test_exports_every_declared_symbol(so):
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = set(re.findall(r"\b(ssd_[a-z_]+)\s*\(", text))
+    assert names == {"ssd_layer_abi_version", "ssd_conv_fwd", "ssd_conv_step", "ssd_conv_bwd",
+                     "ssd_conv_bwd_workspace_size", "ssd_selscan_fwd", "ssd_selscan_step", "ssd_selscan_bwd",
+                     "ssd_selscan_fwd_workspace_size", "ssd_selscan_bwd_workspace_size", "ssd_gated_norm_fwd",
+                     "ssd_gated_norm_bwd", "ssd_gated_norm_bwd_workspace_size"}
+    for n in names:
+        assert hasattr(so, n) and n in lib.__all__ and hasattr(lib, n), n
+    assert lib.ssd_layer_abi_version() == 1
+
+
+def p(v):
+    return ctypes.c_void_p(v) if v else None
+
+
+def st(batch, token):
+    return ctypes.byref(layer.ssd_strides(batch, token))
+
+
+# ---- convolution ----
+
+def CP(batch=2, seqlen=10, channels=64, width=4, split=(32, 16, 16), io=1, act=1, reserved=0, nsplit=None):
+    prob = layer.ssd_conv_problem(batch, seqlen, channels, width, len(split) if nsplit is None else nsplit,
+                                  (ctypes.c_int64 * 3)(*(list(split) + [0] * (3 - len(split)))), io, act, reserved)
+    return prob
+
+
+def outs(*v):
+    return (ctypes.c_void_p * 3)(*v)
+
+
+def conv_fwd(prob, x=PTR, xs=None, w=PTR, bias=PTR, init=PTR, y=(PTR, PTR, PTR), fin=PTR):
+    return lib.load_library().ssd_conv_fwd(None if prob is None else ctypes.byref(prob), p(x), xs, p(w), p(bias),
+                                           p(init), None if y is None else outs(*y), p(fin), None)
+
+
+def conv_step(prob, state=PTR, x=PTR, y=(PTR, PTR, PTR)):
+    return lib.load_library().ssd_conv_step(ctypes.byref(prob), p(state), p(x), None, p(PTR), None, outs(*y), None)
+
+
+def conv_bwd(prob, x=PTR, dy=(PTR, PTR, PTR), dx=PTR, dxs=None, dw=PTR, ws=PTR, n=0, dinit=PTR):
+    return lib.load_library().ssd_conv_bwd(ctypes.byref(prob), p(x), None, p(PTR), None, None, outs(*dy), None, p(dx),
+                                           dxs, p(dw), None, p(dinit), p(ws), n, None)
+
+
+BAD_CONV = [(dict(batch=0), SHAPE), (dict(seqlen=0), SHAPE), (dict(channels=-1), SHAPE), (dict(width=0), SHAPE),
+            (dict(split=(32, 16)), SHAPE), (dict(split=(64, 16, -16)), SHAPE), (dict(split=(64, 0)), SHAPE),
+            (dict(nsplit=0), SHAPE), (dict(nsplit=4), SHAPE),
+            (dict(channels=2 ** 40, split=(2 ** 40,), seqlen=2 ** 40), SHAPE),
+            (dict(io=2), DTYPE), (dict(reserved=1), DTYPE), (dict(act=2), BADVAL), (dict(act=-1), BADVAL)]
+LATE_CONV = [(dict(width=1), UNSUP), (dict(width=5), UNSUP), (dict(batch=65536), UNSUP),
+             (dict(channels=2 ** 25, split=(2 ** 25,)), UNSUP), (dict(seqlen=2 ** 40), UNSUP)]
+
+
+@pytest.mark.parametrize("kw,code", BAD_CONV + LATE_CONV)
+def test_conv_bad_problem(kw, code):
+    assert conv_fwd(CP(**kw)) == code and lib.ssd_last_error_message()
+    assert conv_step(CP(**kw)) == code
+    assert conv_bwd(CP(**kw), n=2 ** 60) == code
+    n = ctypes.c_size_t(7)
+    assert lib.load_library().ssd_conv_bwd_workspace_size(ctypes.byref(CP(**kw)), ctypes.byref(n)) == code
+    assert n.value == 7
+
+
+def test_conv_pointers_and_strides():
+    assert conv_fwd(None) == NULLP and conv_fwd(CP(), y=None) == NULLP
+    for kw in (dict(x=0), dict(w=0), dict(y=(PTR, 0, PTR))):
+        assert conv_fwd(CP(), **kw) == NULLP, kw
+    assert conv_step(CP(), state=0) == NULLP and conv_bwd(CP(), ws=0) == NULLP
+    assert conv_bwd(CP(), dy=(PTR, PTR, 0)) == NULLP
+    assert conv_fwd(CP(batch=0), y=(0, 0, 0)) == SHAPE          # the shape says how many outputs there are
+    for kw in (dict(w=ODD), dict(bias=ODD), dict(init=ODD), dict(fin=ODD), dict(y=(PTR, ODD, PTR)), dict(x=PTR + 1)):
+        assert conv_fwd(CP(), **kw) == MISAL, kw
+    assert conv_fwd(CP(), xs=st(-1, 64)) == BADVAL and conv_fwd(CP(), xs=st(640, -64)) == BADVAL
+    assert conv_fwd(CP(), xs=st(2 ** 62, 64)) == SHAPE
+    assert conv_fwd(CP(), x=PTR + 1, xs=st(-1, 64)) == BADVAL   # strides before alignment
+    # rows of an output that overlap: tokens, batches
+    for s in (st(640, 63), st(639, 64), st(0, 64), st(0, 0)):
+        assert conv_bwd(CP(), dxs=s, n=2 ** 60) == BADVAL
+    assert conv_bwd(CP(), dxs=st(640, 64), n=0) == WS
+    assert conv_bwd(CP(), dxs=st(64, 128), n=0) == WS           # batches inside tokens are apart
+    assert conv_bwd(CP(batch=1, seqlen=1), dxs=st(0, 0), n=0) == WS
+    n = ctypes.c_size_t(0)
+    assert lib.load_library().ssd_conv_bwd_workspace_size(ctypes.byref(CP()), ctypes.byref(n)) == OK and n.value > 0
+    assert conv_bwd(CP(), n=n.value - 1) == WS
+
+
+# ---- selective scan ----
+
+def SP(batch=2, seqlen=300, channels=64, dstate=16, ngroups=2, io=1, reserved=0):
+    return layer.ssd_selscan_problem(batch, seqlen, channels, dstate, ngroups, io, reserved)
+
+
+def XF(bias=0, softplus=1, reserved=0, lo=0.0, hi=float("inf")):
+    return lib.ssd_dt_transform(bias or None, softplus, reserved, lo, hi)
+
+
+def scan_fwd(prob, xf=None, x=PTR, dt=PTR, A=PTR, B=PTR, bs=None, C=PTR, cs=None, D=PTR, z=PTR, zs=None, init=PTR,
+             y=PTR, fin=PTR, ws=PTR, n=2 ** 60):
+    return lib.load_library().ssd_selscan_fwd(ctypes.byref(prob), None if xf is None else ctypes.byref(xf), p(x), p(dt),
+                                              p(A), p(B), bs, p(C), cs, p(D), p(z), zs, p(init), p(y), p(fin), p(ws),
+                                              n, None)
+
+
+def scan_step(prob, state=PTR, x=PTR, z=PTR, zs=None, y=PTR, xf=None):
+    return lib.load_library().ssd_selscan_step(ctypes.byref(prob), None if xf is None else ctypes.byref(xf), p(state),
+                                               p(x), p(PTR), p(PTR), p(PTR), None, p(PTR), None, None, p(z), zs, p(y),
+                                               None)
+
+
+def scan_bwd(prob, x=PTR, z=PTR, dy=PTR, dx=PTR, dz=PTR, dzs=None, dB=PTR, ws=PTR, n=2 ** 60, xf=None):
+    return lib.load_library().ssd_selscan_bwd(ctypes.byref(prob), None if xf is None else ctypes.byref(xf), p(x), p(PTR),
+                                              p(PTR), p(PTR), None, p(PTR), None, p(PTR), p(z), None, None, p(dy), None,
+                                              p(dx), p(PTR), p(PTR), p(dB), p(PTR), p(PTR), p(dz), dzs, None, None,
+                                              p(ws), n, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=0), SHAPE), (dict(seqlen=0), SHAPE), (dict(channels=0), SHAPE), (dict(dstate=0), SHAPE),
+    (dict(ngroups=0), SHAPE), (dict(ngroups=3), SHAPE), (dict(seqlen=2 ** 58), SHAPE),
+    (dict(io=5), DTYPE), (dict(reserved=2), DTYPE), (dict(dstate=65), UNSUP), (dict(batch=65536), UNSUP),
+    (dict(seqlen=2 ** 36), UNSUP)])
+def test_scan_bad_problem(kw, code):
+    assert scan_fwd(SP(**kw)) == code and lib.ssd_last_error_message()
+    assert scan_step(SP(**kw)) == code and scan_bwd(SP(**kw)) == code
+    n = ctypes.c_size_t(7)
+    for f in (lib.load_library().ssd_selscan_fwd_workspace_size, lib.load_library().ssd_selscan_bwd_workspace_size):
+        assert f(ctypes.byref(SP(**kw)), ctypes.byref(n)) == code and n.value == 7
+
+
+@pytest.mark.parametrize("xf", [XF(softplus=2), XF(reserved=1), XF(lo=float("nan")), XF(hi=float("nan")),
+                                XF(lo=1.0, hi=0.5)])
+def test_scan_bad_transform(xf):
+    assert scan_fwd(SP(), xf) == BADVAL and scan_step(SP(), xf=xf) == BADVAL and scan_bwd(SP(), xf=xf) == BADVAL
+    assert scan_fwd(SP(), xf, x=ODD) == BADVAL      # before alignment
+
+
+def test_scan_pointers_and_strides():
+    for k in ("x", "dt", "A", "B", "C", "y"):
+        assert scan_fwd(SP(), **{k: 0}) == NULLP, k
+    for k in ("x", "dt", "A", "D", "init", "y", "fin", "ws"):
+        assert scan_fwd(SP(), **{k: ODD}) == MISAL, k
+    for k in ("B", "C", "z"):
+        assert scan_fwd(SP(), **{k: PTR + 1}) == MISAL, k
+    for k in ("bs", "cs", "zs"):
+        assert scan_fwd(SP(), **{k: st(-8, 32)}) == BADVAL, k
+        assert scan_fwd(SP(), **{k: st(2 ** 62, 32)}) == SHAPE, k
+    assert scan_fwd(SP(), z=0, zs=st(-8, 32), n=0) == WS        # strides of an absent z are not looked at
+    assert scan_fwd(SP(), XF(bias=ODD)) == MISAL
+    assert scan_step(SP(), state=0) == NULLP and scan_step(SP(), state=ODD) == MISAL
+    assert scan_bwd(SP(), dz=0) == NULLP and scan_bwd(SP(), z=0, dz=0, n=0) == WS
+    assert scan_bwd(SP(), dB=ODD) == MISAL and scan_bwd(SP(), ws=0) == NULLP
+    assert scan_bwd(SP(), dzs=st(0, 64)) == BADVAL and scan_bwd(SP(), n=0) == WS
+    assert scan_fwd(SP(), ws=0) == WS                           # this one needs a workspace
+    n = ctypes.c_size_t(0)
+    f = lib.load_library().ssd_selscan_fwd_workspace_size
+    assert f(ctypes.byref(SP()), ctypes.byref(n)) == OK and n.value > 0
+    assert scan_fwd(SP(), n=n.value - 1) == WS
+    assert f(ctypes.byref(SP(seqlen=1)), ctypes.byref(n)) == OK and n.value == 0
+
+
+# ---- gated norm ----
+
+def NP(batch=2, seqlen=5, channels=64, ngroups=2, eps=1e-5, before=0, io=1, reserved=0):
+    return layer.ssd_gated_norm_problem(batch, seqlen, channels, ngroups, eps, before, io, reserved)
+
+
+def norm_fwd(prob, x=PTR, z=PTR, zs=None, w=PTR, y=PTR):
+    return lib.load_library().ssd_gated_norm_fwd(ctypes.byref(prob), p(x), p(z), zs, p(w), p(y), None)
+
+
+def norm_bwd(prob, x=PTR, z=PTR, dy=PTR, dx=PTR, dz=PTR, dzs=None, dw=PTR, ws=PTR, n=2 ** 60):
+    return lib.load_library().ssd_gated_norm_bwd(ctypes.byref(prob), p(x), p(z), None, p(PTR), p(dy), p(dx), p(dz), dzs,
+                                                 p(dw), p(ws), n, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=0), SHAPE), (dict(seqlen=-3), SHAPE), (dict(channels=0), SHAPE), (dict(ngroups=5), SHAPE),
+    (dict(batch=2 ** 31, seqlen=2 ** 31), SHAPE), (dict(io=-1), DTYPE), (dict(reserved=1), DTYPE),
+    (dict(eps=-1e-9), BADVAL), (dict(eps=float("nan")), BADVAL), (dict(eps=float("inf")), BADVAL),
+    (dict(before=2), BADVAL), (dict(channels=16386), UNSUP), (dict(seqlen=2 ** 33), UNSUP)])
+def test_norm_bad_problem(kw, code):
+    assert norm_fwd(NP(**kw)) == code and lib.ssd_last_error_message()
+    assert norm_bwd(NP(**kw)) == code
+    n = ctypes.c_size_t(7)
+    assert lib.load_library().ssd_gated_norm_bwd_workspace_size(ctypes.byref(NP(**kw)), ctypes.byref(n)) == code
+
+
+def test_norm_pointers_and_strides():
+    for k in ("x", "w", "y"):
+        assert norm_fwd(NP(), **{k: 0}) == NULLP and norm_fwd(NP(), **{k: ODD}) == MISAL, k
+    assert norm_fwd(NP(), z=PTR + 1) == MISAL and norm_fwd(NP(), zs=st(-1, 0)) == BADVAL
+    assert norm_bwd(NP(), dz=0) == NULLP and norm_bwd(NP(), z=0, dz=0, n=0) == WS
+    assert norm_bwd(NP(), dzs=st(64, 64)) == BADVAL and norm_bwd(NP(), dz=PTR + 1) == MISAL
+    assert norm_bwd(NP(), n=4) == WS and norm_bwd(NP(), dw=ODD) == MISAL
+
+
+# ---- the Python binding ----
+
+def test_binding_rejects_cpu_tensors():
+    x, w = torch.zeros(1, 2, 8), torch.zeros(8, 4)
+    for call in (lambda: lib.ssd_conv_fwd(x, w), lambda: lib.ssd_conv_bwd(x, w, None, None, x),
+                 lambda: lib.ssd_selscan_fwd(x, x, torch.zeros(8, 4), x, x),
+                 lambda: lib.ssd_gated_norm_fwd(x, None, w[:, 0])):
+        with pytest.raises(lib.SsdArgumentError):
+            call()
+
+
+@pytest.mark.skipif(not CLANG_RT or not os.path.exists(HIPCC), reason="ROCm clang ASan runtime missing")
+@pytest.mark.skipif("SSD_LIBRARY" in os.environ, reason="this is the instrumented run")
+def test_host_code_under_asan(tmp_path):
+    from state_space_sequence_03_amd import build as b
+    objs = {os.path.splitext(s)[0]: os.path.join(b.BUILD_DIR, os.path.splitext(s)[0] + ".o") for s in b.SOURCES}
+    if not all(os.path.exists(o) for o in objs.values()):
+        b.build()
+    asan = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fno-omit-frame-pointer"]
+    for src in ("ssd_api.cpp", "layer_api.cpp"):
+        obj = str(tmp_path / (os.path.splitext(src)[0] + ".o"))
+        subprocess.run([HIPCC] + b.COMMON_FLAGS + asan + ["-x", "hip", "-c", os.path.join(b.CSRC, src), "-o", obj],
+                       check=True, capture_output=True, text=True)
+        objs[os.path.splitext(src)[0]] = obj
+    so = str(tmp_path / "libssd_asan.so")
+    subprocess.run([HIPCC, "--offload-arch=" + b.ARCH, "-shared", "-fPIC", "-shared-libasan",
+                    "-Xarch_host", "-fsanitize=address", "-o", so] + list(objs.values()), check=True,
+                   capture_output=True, text=True)
+    assert _instrumented(so)
+    _run_child(["tests/test_layer_boundary.py"], {"LD_PRELOAD": CLANG_RT[-1], "SSD_LIBRARY": so})
