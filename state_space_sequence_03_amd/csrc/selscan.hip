@@ -53,41 +53,47 @@ struct ScanIo {
   DtXform xf;
 };
 
-template <typename T, int RN, int MODE, bool GATE>
-__global__ void __launch_bounds__(kScanThreads)
+template <typename T, int NP, int MODE, bool GATE>
+__global__ void __launch_bounds__(kScanThreads, 2)
 selscan_kernel(ScanIo<T> io, ScanShape sh) {
-  constexpr int NP = 4 * RN, CW = 256 / RN;   // padded states, channels per wave
+  constexpr int RN = NP / 8, CW = 128 / RN;   // lanes per channel, channels per wave
   constexpr int PER = kScanTile * NP / kScanThreads;
+  constexpr int U = kScanAhead;
   __shared__ float sB[2][kScanTile][NP];
   __shared__ float sC[MODE == kStates ? 1 : 2][kScanTile][NP];
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-  const int64_t tile = blockIdx.x % (sh.tiles * sh.G);
-  const int64_t k = blockIdx.x / (sh.tiles * sh.G);
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int tiles = (int)sh.tiles, groups = (int)sh.G;
+  const int tile = blockIdx.x % (tiles * groups);
+  const int k = blockIdx.x / (tiles * groups);
   const int64_t b = blockIdx.y;
-  const int64_t g = tile / sh.tiles;
-  const int64_t base = ((tile % sh.tiles) * (kScanThreads / kWave) + wave) * CW;
-  const bool live = base < sh.Dg;             // whole waves past the group only stage
+  const int g = tile / tiles;
+  const int base = ((tile % tiles) * (kScanThreads / kWave) + wave) * CW;
+  const int Dg = (int)sh.Dg, N = (int)sh.N;
+  const bool live = base < Dg;             // whole waves past the group only stage
   const int nl = lane % RN, dl = lane / RN;
-  const int n0 = 4 * nl;
-  const int64_t own = base + dl * 4 + (lane & 3);   // the channel this lane prepares
-  const int64_t c = g * sh.Dg + (own < sh.Dg ? own : sh.Dg - 1);
-  const bool mine = own < sh.Dg && nl < 4;
-  const int64_t t0 = k * sh.T, t1 = t0 + sh.T < sh.L ? t0 + sh.T : sh.L;
+  const int n0 = 8 * nl;
+  const int own = base + dl * 2 + (lane & 1);   // the channel this lane prepares
+  const int c = g * Dg + (own < Dg ? own : Dg - 1);
+  const unsigned at = (unsigned)c * sizeof(T);
+  const bool mine = own < Dg && nl < 2;
+  const int64_t t0 = k * sh.T;
+  const int len = (int)(t0 + sh.T < sh.L ? sh.T : sh.L - t0);   // tokens of this chunk
 
-  float A2[4][4], h[4][4], P[4][4], R[4][4];
+  float A2[2][8], h[2][8], P[2][8], R[2][8];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t lc = base + dl * 4 + j;
-    const int64_t cj = g * sh.Dg + (lc < sh.Dg ? lc : sh.Dg - 1);
+  for (int j = 0; j < 2; ++j) {
+    const int lc = base + dl * 2 + j;
+    const int64_t cj = g * Dg + (lc < Dg ? lc : Dg - 1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const int n = n0 + i;
-      A2[j][i] = n < sh.N ? io.A[cj * sh.N + n] * kLog2e : 0.0f;
+      A2[j][i] = n < N ? io.A[cj * N + n] * kLog2e : 0.0f;
       h[j][i] = 0.0f;
       P[j][i] = 1.0f;
       R[j][i] = 0.0f;
       if (k == 0) {
-        if (io.init && n < sh.N) h[j][i] = io.init[(b * sh.D + cj) * sh.N + n];
+        if (io.init && n < N) h[j][i] = io.init[(b * sh.D + cj) * N + n];
       } else if (MODE == kOut) {
         h[j][i] = io.H[((b * sh.K + k) * sh.D + cj) * NP + n];
       }
@@ -97,22 +103,24 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
   const float Dc = MODE == kOut && io.Dv ? io.Dv[c] : 0.0f;
   float sum = 0.0f;
 
-  const T* xp = io.x + b * sh.L * sh.D + c;
-  const T* dp = io.dt + b * sh.L * sh.D + c;
-  const T* gp = MODE == kBoth ? io.dy + b * sh.L * sh.D + c : nullptr;
-  const T* zp = GATE ? io.z + b * io.zs.batch + c : nullptr;
-  const T* Bp = io.B + b * io.bs.batch + g * sh.N;
-  const T* Cp = MODE == kStates ? nullptr : io.C + b * io.cs.batch + g * sh.N;
+  // rows: a uniform pointer to the chunk's first token, the lane's channel as offset
+  const int64_t row = (b * sh.L + t0) * sh.D;
+  const T* const xp = io.x + row;
+  const T* const dp = io.dt + row;
+  const T* const gp = MODE == kBoth ? io.dy + row : nullptr;
+  T* const yp0 = MODE == kOut ? io.y + row : nullptr;
+  const T* const zp = GATE ? io.z + b * io.zs.batch + t0 * io.zs.token : nullptr;
+  const T* const Bp = io.B + b * io.bs.batch + t0 * io.bs.token + g * N;
+  const T* const Cp = MODE == kStates ? nullptr : io.C + b * io.cs.batch + t0 * io.cs.token + g * N;
 
   // B and C of one tile, held in registers from their load to their place in LDS
   float rb[PER], rc[MODE == kStates ? 1 : PER];
-  auto fetch = [&](int64_t t) {
+  auto fetch = [&](int t) {
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       const int i = q * kScanThreads + tid;
-      const int64_t tok = t + i / NP;
-      const int n = i % NP;
-      const bool in = tok < t1 && n < sh.N;
+      const int tok = t + i / NP, n = i % NP;
+      const bool in = tok < len && n < N;
       rb[q] = in ? to_f32(Bp[tok * io.bs.token + n]) : 0.0f;
       if constexpr (MODE != kStates) rc[q] = in ? to_f32(Cp[tok * io.cs.token + n]) : 0.0f;
     }
@@ -126,61 +134,68 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
     }
   };
 
-  T xr[kScanAhead], dr[kScanAhead], zr[kScanAhead], gr[kScanAhead];
-  auto load = [&](int64_t t) {
+  T xr[U], dr[U], zr[U], gr[U];
+  auto load = [&](int t) {
+    const unsigned o = here_offset(at);
 #pragma unroll
-    for (int u = 0; u < kScanAhead; ++u) {
-      const int64_t tok = t + u < t1 ? t + u : t1 - 1;
-      xr[u] = xp[tok * sh.D];
-      dr[u] = dp[tok * sh.D];
-      if constexpr (GATE && MODE != kStates) zr[u] = zp[tok * io.zs.token];
-      if constexpr (MODE == kBoth) gr[u] = gp[tok * sh.D];
+    for (int u = 0; u < U; ++u) {
+      const int64_t tok = t + u < len ? t + u : len - 1;
+      xr[u] = row_load(xp + tok * sh.D, o);
+      dr[u] = row_load(dp + tok * sh.D, o);
+      if constexpr (GATE && MODE != kStates) zr[u] = row_load(zp + tok * io.zs.token, o);
+      if constexpr (MODE == kBoth) gr[u] = row_load(gp + tok * sh.D, o);
     }
   };
 
-  fetch(t0);
-  load(t0);
+  fetch(0);
+  load(0);
   place(0);
   __syncthreads();
   int buf = 0;
-  for (int64_t tt = t0; tt < t1; tt += kScanTile, buf ^= 1) {
-    const bool more = tt + kScanTile < t1;
+  for (int tt = 0; tt < len; tt += kScanTile, buf ^= 1) {
+    const bool more = tt + kScanTile < len;
     if (more) fetch(tt + kScanTile);
     if (live) {
-      for (int s = 0; s < kScanTile && tt + s < t1; s += kScanAhead) {
-        const int64_t ts = tt + s;
-        float xv[kScanAhead], dv[kScanAhead], zv[kScanAhead], gv[kScanAhead];
+      for (int s = 0; s < kScanTile && tt + s < len; s += U) {
+        const int ts = tt + s;
+        // the lane's own channel at U tokens
+        float d[U], dx[U], xv[U], gate[U], ds[U], none[1];
 #pragma unroll
-        for (int u = 0; u < kScanAhead; ++u) {
+        for (int u = 0; u < U; ++u) {
           xv[u] = to_f32(xr[u]);
-          dv[u] = to_f32(dr[u]);
-          zv[u] = GATE && MODE != kStates ? to_f32(zr[u]) : 0.0f;
-          gv[u] = MODE == kBoth ? to_f32(gr[u]) : 0.0f;
+          d[u] = to_f32(dr[u]);
+          gate[u] = GATE && MODE != kStates ? to_f32(zr[u]) : 1.0f;
+          ds[u] = MODE == kBoth ? to_f32(gr[u]) : 0.0f;
         }
-        if (ts + kScanAhead < t1) load(ts + kScanAhead);
+        if (ts + U < len) load(ts + U);
+        dt_values<U, false>(f, d, none);
+        const unsigned o_at = here_offset(at);
 #pragma unroll
-        for (int u = 0; u < kScanAhead; ++u) {
-          const bool in = ts + u < t1;
-          const float d = in ? dt_value(f, dv[u]) : 0.0f;
-          const float dx = in ? d * xv[u] : 0.0f;
-          float gate = 1.0f;
-          if constexpr (GATE && MODE != kStates) gate = zv[u] * sigmoid_f32(zv[u]);
-          const float ds = MODE == kBoth && in ? gv[u] * gate : 0.0f;
-          if constexpr (MODE != kOut) sum += d;
-          const floatx4 Bv = *reinterpret_cast<const floatx4*>(&sB[buf][s + u][n0]);
-          floatx4 Cv = {0.0f, 0.0f, 0.0f, 0.0f};
-          if constexpr (MODE != kStates) Cv = *reinterpret_cast<const floatx4*>(&sC[buf][s + u][n0]);
-          float yp[4];
+        for (int u = 0; u < U; ++u) {
+          if (ts + u >= len) d[u] = xv[u] = ds[u] = 0.0f;
+          dx[u] = d[u] * xv[u];
+          if constexpr (GATE && MODE != kStates) gate[u] *= sigmoid_f32(gate[u]);
+          if constexpr (MODE == kBoth) ds[u] *= gate[u];
+          if constexpr (MODE != kOut) sum += d[u];
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float Bv[8], Cv[8], part[2];
+#pragma unroll
+          for (int q = 0; q < 8; q += 4) {
+            load_v<4>(&sB[buf][s + u][n0 + q], Bv + q);
+            if constexpr (MODE != kStates) load_v<4>(&sC[buf][s + u][n0 + q], Cv + q);
+          }
           auto channel = [&](auto J) {
             constexpr int j = decltype(J)::value;
-            const float dj = quad_bcast<j>(d), xj = quad_bcast<j>(dx);
-            const float sj = MODE == kBoth ? quad_bcast<j>(ds) : 0.0f;
-            yp[j] = 0.0f;
+            const float dj = pair_bcast<j>(d[u]), xj = pair_bcast<j>(dx[u]);
+            const float sj = MODE == kBoth ? pair_bcast<j>(ds[u]) : 0.0f;
+            part[j] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
               const float a = fast_exp2(dj * A2[j][i]);
               h[j][i] = fmaf(a, h[j][i], xj * Bv[i]);
-              if constexpr (MODE == kOut) yp[j] = fmaf(Cv[i], h[j][i], yp[j]);
+              if constexpr (MODE == kOut) part[j] = fmaf(Cv[i], h[j][i], part[j]);
               if constexpr (MODE == kBoth) {
                 P[j][i] *= a;
                 R[j][i] = fmaf(P[j][i], sj * Cv[i], R[j][i]);
@@ -189,12 +204,10 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
           };
           channel(std::integral_constant<int, 0>{});
           channel(std::integral_constant<int, 1>{});
-          channel(std::integral_constant<int, 2>{});
-          channel(std::integral_constant<int, 3>{});
           if constexpr (MODE == kOut) {
-            float o = quads_sum<RN>(quad_fold(yp, lane));
-            o = fmaf(Dc, xv[u], o) * gate;
-            if (in && mine) io.y[(b * sh.L + ts + u) * sh.D + c] = to_io<T>(o);
+            const float o = pairs_sum<RN>(pair_fold(part[0], part[1], lane));
+            if (mine && ts + u < len)
+              row_store(yp0 + (int64_t)(ts + u) * sh.D, o_at, to_io<T>(fmaf(Dc, xv[u], o) * gate[u]));
           }
         }
       }
@@ -205,23 +218,25 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
   if (!live) return;
   const bool last = k == sh.K - 1;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t lc = base + dl * 4 + j;
-    if (lc >= sh.Dg) continue;
-    const int64_t cj = g * sh.Dg + lc;
+  for (int j = 0; j < 2; ++j) {
+    const int lc = base + dl * 2 + j;
+    if (lc >= Dg) continue;
+    const int64_t cj = g * Dg + lc;
     if constexpr (MODE == kOut) {
       if (last && io.fin)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n0 + i < sh.N) io.fin[(b * sh.D + cj) * sh.N + n0 + i] = h[j][i];
+        for (int i = 0; i < 8; ++i)
+          if (n0 + i < N) io.fin[(b * sh.D + cj) * N + n0 + i] = h[j][i];
     } else {
       if (!last)
-        *reinterpret_cast<floatx4*>(io.H + ((b * sh.K + k + 1) * sh.D + cj) * NP + n0) =
-            floatx4{h[j][0], h[j][1], h[j][2], h[j][3]};
+#pragma unroll
+        for (int q = 0; q < 8; q += 4)
+          store_v<4>(io.H + ((b * sh.K + k + 1) * sh.D + cj) * NP + n0 + q, h[j] + q);
       if constexpr (MODE == kBoth)
         if (k > 0)
-          *reinterpret_cast<floatx4*>(io.R + ((b * sh.K + k - 1) * sh.D + cj) * NP + n0) =
-              floatx4{R[j][0], R[j][1], R[j][2], R[j][3]};
+#pragma unroll
+          for (int q = 0; q < 8; q += 4)
+            store_v<4>(io.R + ((b * sh.K + k - 1) * sh.D + cj) * NP + n0 + q, R[j] + q);
     }
   }
   if constexpr (MODE != kOut)
@@ -240,20 +255,29 @@ selscan_pass_kernel(float* __restrict__ H, const float* __restrict__ A,
   if (i >= batch * D * NP) return;
   const int64_t n = i % NP, c = i / NP % D, b = i / NP / D;
   const float a2 = n < N ? A[c * N + n] * kLog2e : 0.0f;
-  float* p = H + (b * K * D + c) * NP + n;
-  const float* sp = sumdt + b * K * D + c;
-  if (!reverse) {
-    float run = p[D * NP];
-    for (int64_t k = 2; k < K; ++k) {
-      run = fmaf(fast_exp2(a2 * sp[(k - 1) * D]), run, p[k * D * NP]);
-      p[k * D * NP] = run;
+  float* const p = H + (b * K * D + c) * NP + n;
+  const float* const sp = sumdt + b * K * D + c;
+  const int64_t step = D * NP;
+  // slots `at` from `first` on, `dir` apart, the decay of slot k being chunk
+  // k - dir's; eight slots are loaded before the first of them is used
+  float run = reverse ? (last && n < N ? last[(b * D + c) * N + n] : 0.0f) : p[step];
+  if (reverse) p[(K - 1) * step] = run;
+  const int64_t first = reverse ? K - 2 : 2, count = reverse ? K - 1 : K - 2, dir = reverse ? -1 : 1;
+  constexpr int M = 8;
+  for (int64_t q = 0; q < count; q += M) {
+    float v[M], s[M];
+#pragma unroll
+    for (int u = 0; u < M; ++u) {
+      const int64_t k = first + dir * (q + u < count ? q + u : count - 1);
+      v[u] = p[k * step];
+      s[u] = sp[(k - dir) * D];
     }
-  } else {
-    float run = last && n < N ? last[(b * D + c) * N + n] : 0.0f;
-    p[(K - 1) * D * NP] = run;
-    for (int64_t k = K - 2; k >= 0; --k) {
-      run = fmaf(fast_exp2(a2 * sp[(k + 1) * D]), run, p[k * D * NP]);
-      p[k * D * NP] = run;
+#pragma unroll
+    for (int u = 0; u < M; ++u) {
+      if (q + u < count) {
+        run = fmaf(fast_exp2(a2 * s[u]), run, v[u]);
+        p[(first + dir * (q + u)) * step] = run;
+      }
     }
   }
 }
@@ -300,8 +324,9 @@ selscan_step_kernel(float* __restrict__ state, const T* __restrict__ x, const T*
   for (int64_t t = 0; t < L; ++t) {
     const int64_t at = (b * L + t) * D + c;
     const float xv = to_f32(x[at]);
-    const float d = dt_value(f, to_f32(dt[at]));
-    const float dx = d * xv;
+    float dv[1] = {to_f32(dt[at])}, none[1];
+    dt_values<1, false>(f, dv, none);
+    const float d = dv[0], dx = d * xv;
     float part = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -336,8 +361,7 @@ selscan_step_kernel(float* __restrict__ state, const T* __restrict__ x, const T*
 // otherwise as many as give about three waves per SIMD, of at least 64 tokens.
 ScanShape selscan_fwd_shape(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
   ScanShape s;
-  const int rn = selscan_rn(N);
-  const int64_t cw = 256 / rn, per = cw * (kScanThreads / kWave);
+  const int64_t cw = 1024 / selscan_np(N), per = cw * (kScanThreads / kWave);
   s.L = L; s.D = D; s.N = N; s.G = G; s.Dg = D / G;
   s.tiles = (s.Dg + per - 1) / per;
   const int64_t waves = batch * G * ((s.Dg + cw - 1) / cw);
@@ -354,7 +378,7 @@ ScanShape selscan_fwd_shape(int64_t batch, int64_t L, int64_t D, int64_t N, int6
 
 static size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 size_t selscan_state_bytes(int64_t batch, const ScanShape& s) {
-  return up256(size_t(batch) * s.K * s.D * 4 * selscan_rn(s.N) * sizeof(float));
+  return up256(size_t(batch) * s.K * s.D * selscan_np(s.N) * sizeof(float));
 }
 size_t selscan_sum_bytes(int64_t batch, const ScanShape& s) {
   return up256(size_t(batch) * s.K * s.D * sizeof(float));
@@ -386,34 +410,34 @@ static ScanIo<T> scan_io(const ScanArgs& a) {
   return io;
 }
 
-template <typename T, int RN, int MODE>
+template <typename T, int NP, int MODE>
 static void launch_scan(const ScanIo<T>& io, const ScanShape& s, int64_t batch, int64_t chunks,
                         hipStream_t stream) {
   const dim3 grid((unsigned)(s.tiles * s.G * chunks), (unsigned)batch);
   if constexpr (MODE != kStates) {
     if (io.z) {
-      hipLaunchKernelGGL((selscan_kernel<T, RN, MODE, true>), grid, dim3(kScanThreads), 0, stream, io, s);
+      hipLaunchKernelGGL((selscan_kernel<T, NP, MODE, true>), grid, dim3(kScanThreads), 0, stream, io, s);
       return;
     }
   }
-  hipLaunchKernelGGL((selscan_kernel<T, RN, MODE, false>), grid, dim3(kScanThreads), 0, stream, io, s);
+  hipLaunchKernelGGL((selscan_kernel<T, NP, MODE, false>), grid, dim3(kScanThreads), 0, stream, io, s);
 }
 
 void launch_selscan_pass(float* H, const float* A, const float* sumdt, const float* last,
                          int64_t batch, const ScanShape& s, int reverse, hipStream_t stream) {
-  const int np = 4 * selscan_rn(s.N);
+  const int np = selscan_np(s.N);
   hipLaunchKernelGGL(selscan_pass_kernel, dim3((unsigned)((batch * s.D * np + 255) / 256)), dim3(256), 0,
                      stream, H, A, sumdt, last, batch, s.K, s.D, s.N, np, reverse);
 }
 
-template <typename T, int RN>
-static hipError_t fwd_rn(const ScanArgs& a, hipStream_t stream) {
+template <typename T, int NP>
+static hipError_t fwd_np(const ScanArgs& a, hipStream_t stream) {
   const ScanShape s = selscan_fwd_shape(a.batch, a.L, a.D, a.N, a.G);
   ScanIo<T> io = scan_io<T>(a);
   if (s.K > 1) {
     io.H = static_cast<float*>(a.workspace);
     io.sumdt = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + selscan_state_bytes(a.batch, s));
-    launch_scan<T, RN, kStates>(io, s, a.batch, s.K - 1, stream);
+    launch_scan<T, NP, kStates>(io, s, a.batch, s.K - 1, stream);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (s.K > 2) {
@@ -422,16 +446,16 @@ static hipError_t fwd_rn(const ScanArgs& a, hipStream_t stream) {
       if (e != hipSuccess) return e;
     }
   }
-  launch_scan<T, RN, kOut>(io, s, a.batch, s.K, stream);
+  launch_scan<T, NP, kOut>(io, s, a.batch, s.K, stream);
   return hipGetLastError();
 }
 
 template <typename T>
 static hipError_t fwd_t(const ScanArgs& a, hipStream_t stream) {
-  const int rn = selscan_rn(a.N);
-  if (rn == 4) return fwd_rn<T, 4>(a, stream);
-  if (rn == 8) return fwd_rn<T, 8>(a, stream);
-  return fwd_rn<T, 16>(a, stream);
+  const int np = selscan_np(a.N);
+  if (np == 16) return fwd_np<T, 16>(a, stream);
+  if (np == 32) return fwd_np<T, 32>(a, stream);
+  return fwd_np<T, 64>(a, stream);
 }
 
 hipError_t launch_selscan_fwd(const ScanArgs& a, hipStream_t stream) {
@@ -440,15 +464,15 @@ hipError_t launch_selscan_fwd(const ScanArgs& a, hipStream_t stream) {
 
 // First stage of the backward pass: every chunk's end state and the gradient it sends
 // to its start, then both chains.
-template <typename T, int RN>
-static hipError_t both_rn(const ScanArgs& a, const ScanShape& s, float* H, float* R, float* sumdt,
+template <typename T, int NP>
+static hipError_t both_np(const ScanArgs& a, const ScanShape& s, float* H, float* R, float* sumdt,
                           hipStream_t stream) {
   ScanIo<T> io = scan_io<T>(a);
   io.H = H;
   io.R = R;
   io.sumdt = sumdt;
   if (s.K > 1) {
-    launch_scan<T, RN, kBoth>(io, s, a.batch, s.K, stream);
+    launch_scan<T, NP, kBoth>(io, s, a.batch, s.K, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -458,14 +482,14 @@ static hipError_t both_rn(const ScanArgs& a, const ScanShape& s, float* H, float
 }
 hipError_t launch_selscan_both(const ScanArgs& a, const ScanShape& s, float* H, float* R,
                                float* sumdt, hipStream_t stream) {
-  const int rn = selscan_rn(a.N);
+  const int np = selscan_np(a.N);
   if (a.bf16)
-    return rn == 4 ? both_rn<bf16, 4>(a, s, H, R, sumdt, stream)
-           : rn == 8 ? both_rn<bf16, 8>(a, s, H, R, sumdt, stream)
-                     : both_rn<bf16, 16>(a, s, H, R, sumdt, stream);
-  return rn == 4 ? both_rn<float, 4>(a, s, H, R, sumdt, stream)
-         : rn == 8 ? both_rn<float, 8>(a, s, H, R, sumdt, stream)
-                   : both_rn<float, 16>(a, s, H, R, sumdt, stream);
+    return np == 16 ? both_np<bf16, 16>(a, s, H, R, sumdt, stream)
+           : np == 32 ? both_np<bf16, 32>(a, s, H, R, sumdt, stream)
+                      : both_np<bf16, 64>(a, s, H, R, sumdt, stream);
+  return np == 16 ? both_np<float, 16>(a, s, H, R, sumdt, stream)
+         : np == 32 ? both_np<float, 32>(a, s, H, R, sumdt, stream)
+                    : both_np<float, 64>(a, s, H, R, sumdt, stream);
 }
 
 template <typename T, int RN, bool GATE>
@@ -487,7 +511,7 @@ static hipError_t step_g(const ScanArgs& a, hipStream_t stream) {
 }
 template <typename T>
 static hipError_t step_t(const ScanArgs& a, hipStream_t stream) {
-  const int rn = selscan_rn(a.N);
+  const int rn = selscan_np(a.N) / 4;
   if (rn == 4) return a.z ? step_g<T, 4, true>(a, stream) : step_g<T, 4, false>(a, stream);
   if (rn == 8) return a.z ? step_g<T, 8, true>(a, stream) : step_g<T, 8, false>(a, stream);
   return a.z ? step_g<T, 16, true>(a, stream) : step_g<T, 16, false>(a, stream);

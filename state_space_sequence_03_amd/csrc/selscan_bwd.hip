@@ -74,28 +74,30 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
   extern __shared__ float smem[];
   float* const sB = smem;                 // [TB][NP]
   float* const sC = smem + TB * NP;       // [TB][NP]
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   float* const slots = smem + 2 * TB * NP + wave * SUBS * SLOT;   // [SUBS][SLOT], this wave's
-  const int64_t tile = blockIdx.x % (sh.tiles * sh.G);
-  const int64_t k = blockIdx.x / (sh.tiles * sh.G);
+  const int tiles = (int)sh.tiles, groups = (int)sh.G, Dg = (int)sh.Dg, N = (int)sh.N;
+  const int tile = blockIdx.x % (tiles * groups);
+  const int64_t k = blockIdx.x / (tiles * groups);
   const int64_t b = blockIdx.y;
-  const int64_t g = tile / sh.tiles;
-  const int64_t base = ((tile % sh.tiles) * kBwdWaves + wave) * CW;
-  const bool live = base < sh.Dg;
+  const int g = tile / tiles;
+  const int base = ((tile % tiles) * kBwdWaves + wave) * CW;
+  const bool live = base < Dg;
   const int nl = lane % RN, dl = lane / RN, n0 = 4 * nl;
   const int par = (lane >> 1) & 1;                   // which token of a pair this lane prepares
-  const int64_t own = base + dl * 2 + (lane & 1);    // and which channel
-  const int64_t c = g * sh.Dg + (own < sh.Dg ? own : sh.Dg - 1);
-  const bool mine = own < sh.Dg && nl < 4;
-  const int64_t t0 = k * TB, t1 = t0 + TB < sh.L ? t0 + TB : sh.L;
+  const int own = base + dl * 2 + (lane & 1);        // and which channel
+  const int c = g * Dg + (own < Dg ? own : Dg - 1);
+  const bool mine = own < Dg && nl < 4;
+  const int64_t t0 = k * TB;
+  const int len = (int)(t0 + TB < sh.L ? TB : sh.L - t0);   // tokens of this chunk
 
   {
-    const T* Bp = io.B + b * io.bs.batch + g * sh.N;
-    const T* Cp = io.C + b * io.cs.batch + g * sh.N;
+    const T* Bp = io.B + b * io.bs.batch + t0 * io.bs.token + g * N;
+    const T* Cp = io.C + b * io.cs.batch + t0 * io.cs.token + g * N;
     for (int i = tid; i < TB * NP; i += kBwdThreads) {
-      const int64_t tok = t0 + i / NP;
-      const int n = i % NP;
-      const bool in = tok < t1 && n < sh.N;
+      const int tok = i / NP, n = i % NP;
+      const bool in = tok < len && n < N;
       sB[i] = in ? to_f32(Bp[tok * io.bs.token + n]) : 0.0f;
       sC[i] = in ? to_f32(Cp[tok * io.cs.token + n]) : 0.0f;
     }
@@ -106,15 +108,15 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
     float A2[2][4], h[2][4], gr[2][4], dA[2][4];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int64_t lc = base + dl * 2 + j;
-      const int64_t cj = g * sh.Dg + (lc < sh.Dg ? lc : sh.Dg - 1);
+      const int lc = base + dl * 2 + j;
+      const int64_t cj = g * Dg + (lc < Dg ? lc : Dg - 1);
       const int64_t at = ((b * sh.K + k) * sh.D + cj) * NP + n0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int n = n0 + i;
-        A2[j][i] = n < sh.N ? io.A[cj * sh.N + n] * kLog2e : 0.0f;
+        A2[j][i] = n < N ? io.A[cj * N + n] * kLog2e : 0.0f;
         h[j][i] = k > 0 ? io.H[at + i]
-                        : io.init && n < sh.N ? io.init[(b * sh.D + cj) * sh.N + n] : 0.0f;
+                        : io.init && n < N ? io.init[(b * sh.D + cj) * N + n] : 0.0f;
         gr[j][i] = io.R[at + i];
         dA[j][i] = 0.0f;
       }
@@ -122,25 +124,35 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
     const DtLane f = dt_lane(io.xf, c);
     const float Dc = io.Dv ? io.Dv[c] : 0.0f;
     float dD = 0.0f, dbias = 0.0f;
-    const int64_t row = b * sh.L;
-    const T* xp = io.x + row * sh.D + c;
-    const T* dp = io.dt + row * sh.D + c;
-    const T* gp = io.dy + row * sh.D + c;
-    const T* zp = GATE ? io.z + b * io.zs.batch + c : nullptr;
-    const int subs = (int)((t1 - t0 + kSub - 1) / kSub);
+    // this chunk's rows: the lane's channel, and its token of each pair
+    const int64_t row = (b * sh.L + t0) * sh.D;
+    const T* const xp = io.x + row;
+    const T* const dp = io.dt + row;
+    const T* const gp = io.dy + row;
+    const T* const zp = GATE ? io.z + b * io.zs.batch + t0 * io.zs.token : nullptr;
+    T* const zo = GATE ? io.dz + b * io.dzs.batch + t0 * io.dzs.token : nullptr;
+    const int subs = (len + kSub - 1) / kSub;
+    // byte offsets from a pair's first row: the lane's channel, in its own token's row
+    // where that is inside the chunk (a pair's rows are less than 4 GiB apart)
+    const unsigned here = (unsigned)c * sizeof(T);
+    const unsigned od = here + par * (unsigned)(sh.D * sizeof(T));
+    const unsigned oz = GATE ? here + par * (unsigned)(io.zs.token * sizeof(T)) : 0;
+    const unsigned ozo = GATE ? here + par * (unsigned)(io.dzs.token * sizeof(T)) : 0;
 
     // forwards, one checkpoint per 8 tokens
     T xr[kPairs], dr[kPairs], zr[kPairs], yr[kPairs];
     auto load = [&](int s, bool all) {
+      const unsigned o_here = here_offset(here), o_d = here_offset(od), o_z = here_offset(oz);
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) {
-        const int64_t t = t0 + s * kSub + 2 * p + par;
-        const int64_t tok = t < t1 ? t : t1 - 1;
-        xr[p] = xp[tok * sh.D];
-        dr[p] = dp[tok * sh.D];
+        const int t = s * kSub + 2 * p;
+        const int64_t first = t < len ? t : 0;       // uniform: the pair's first row, or any row inside
+        const bool both = t + 1 < len;
+        xr[p] = row_load(xp + first * sh.D, both ? o_d : o_here);
+        dr[p] = row_load(dp + first * sh.D, both ? o_d : o_here);
         if (all) {
-          yr[p] = gp[tok * sh.D];
-          if constexpr (GATE) zr[p] = zp[tok * io.zs.token];
+          yr[p] = row_load(gp + first * sh.D, both ? o_d : o_here);
+          if constexpr (GATE) zr[p] = row_load(zp + first * io.zs.token, both ? o_z : o_here);
         }
       }
     };
@@ -151,12 +163,15 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
         *reinterpret_cast<floatx4*>(slots + s * SLOT + (j * kWave + lane) * 4) =
             floatx4{h[j][0], h[j][1], h[j][2], h[j][3]};
       if (s + 1 == subs) break;
-      float d[kPairs], dx[kPairs];
+      float d[kPairs], dx[kPairs], none[1];
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) {   // only the last 8 tokens can lie past the end
-        d[p] = dt_value(f, to_f32(dr[p]));
-        dx[p] = d[p] * to_f32(xr[p]);
+        d[p] = to_f32(dr[p]);
+        dx[p] = to_f32(xr[p]);
       }
+      dt_values<kPairs, false>(f, d, none);
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) dx[p] *= d[p];
       if (s + 2 < subs) load(s + 1, false);
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) {
@@ -188,16 +203,18 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
         for (int i = 0; i < 4; ++i) h0[j][i] = v[i];
       }
       wave_sync();   // other lanes' sums will be written over this checkpoint
-      float d[kPairs], dx[kPairs], ds[kPairs], xv[kPairs], raw[kPairs], yv[kPairs], zv[kPairs];
+      float d[kPairs], dx[kPairs], ds[kPairs], xv[kPairs], slope[kPairs], yv[kPairs], zv[kPairs];
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) d[p] = to_f32(dr[p]);
+      dt_values<kPairs, true>(f, d, slope);
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) {
         // past the last token and past the group's last channel nothing is added
-        const bool in = t0 + s * kSub + 2 * p + par < t1 && own < sh.Dg;
+        const bool in = s * kSub + 2 * p + par < len && own < Dg;
         xv[p] = to_f32(xr[p]);
-        raw[p] = to_f32(dr[p]);
         yv[p] = in ? to_f32(yr[p]) : 0.0f;
         zv[p] = GATE ? to_f32(zr[p]) : 0.0f;
-        d[p] = in ? dt_value(f, raw[p]) : 0.0f;
+        d[p] = in ? d[p] : 0.0f;
         dx[p] = in ? d[p] * xv[p] : 0.0f;
         ds[p] = GATE ? yv[p] * (zv[p] * sigmoid_f32(zv[p])) : yv[p];
       }
@@ -228,10 +245,11 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
         token(std::integral_constant<int, 1>{});
         if constexpr (GATE) {
           const float o = fmaf(Dc, xv[p], quads_sum<RN>(quad_fold(yp, lane)));
-          const int64_t t = t0 + s * kSub + 2 * p + par;
+          const int t = s * kSub + 2 * p + par;
           const float sg = sigmoid_f32(zv[p]);
-          if (mine && t < t1)
-            io.dz[b * io.dzs.batch + t * io.dzs.token + c] = to_io<T>(yv[p] * o * silu_slope(zv[p], sg));
+          if (mine && t < len)
+            row_store(zo + (int64_t)(s * kSub + 2 * p) * io.dzs.token, ozo,
+                      to_io<T>(yv[p] * o * silu_slope(zv[p], sg)));
         }
       }
 #pragma unroll
@@ -270,14 +288,15 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
         token(std::integral_constant<int, 0>{});
         const float qv = quads_sum<RN>(quad_fold(vq, lane));
         const float rv = quads_sum<RN>(quad_fold(vr, lane)) * 0.6931471805599453f;   // A2 = A log2 e
-        const int64_t t = t0 + s * kSub + 2 * p + par;
-        if (t < t1) {
-          const float ddt = fmaf(xv[p], qv, rv) * dt_slope(f, raw[p]);
+        const int t = s * kSub + 2 * p + par;
+        if (t < len) {
+          const float ddt = fmaf(xv[p], qv, rv) * slope[p];
           dbias += ddt;
           dD = fmaf(ds[p], xv[p], dD);
           if (mine) {
-            io.dx[(row + t) * sh.D + c] = to_io<T>(fmaf(d[p], qv, Dc * ds[p]));
-            io.ddt[(row + t) * sh.D + c] = to_io<T>(ddt);
+            const int64_t first = row + (int64_t)(s * kSub + 2 * p) * sh.D;
+            row_store(io.dx + first, od, to_io<T>(fmaf(d[p], qv, Dc * ds[p])));
+            row_store(io.ddt + first, od, to_io<T>(ddt));
           }
         }
         // the wave's sums over channels: the lower half of the wave gets the pair's
@@ -306,15 +325,15 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
 
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int64_t lc = base + dl * 2 + j;
-      if (lc >= sh.Dg) continue;
-      const int64_t cj = g * sh.Dg + lc;
+      const int lc = base + dl * 2 + j;
+      if (lc >= Dg) continue;
+      const int64_t cj = g * Dg + lc;
       *reinterpret_cast<floatx4*>(io.dApart + ((b * sh.K + k) * sh.D + cj) * NP + n0) =
           floatx4{dA[j][0], dA[j][1], dA[j][2], dA[j][3]};
       if (k == 0 && io.dinit)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (n0 + i < sh.N) io.dinit[(b * sh.D + cj) * sh.N + n0 + i] = gr[j][i];
+          if (n0 + i < N) io.dinit[(b * sh.D + cj) * N + n0 + i] = gr[j][i];
     }
     dD += dpp_move<0x4E>(dD);         // both tokens of the pairs
     dbias += dpp_move<0x4E>(dbias);
@@ -325,14 +344,14 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
   }
   __syncthreads();
   // the workgroup's sums of dB and dC: live waves in order
-  const int64_t left = sh.Dg - (tile % sh.tiles) * kBwdWaves * CW;
-  const int waves = left >= kBwdWaves * CW ? kBwdWaves : (int)((left + CW - 1) / CW);
-  for (int i = tid; i < (int)(t1 - t0) * 2 * NP; i += kBwdThreads) {
+  const int left = Dg - (tile % tiles) * kBwdWaves * CW;
+  const int waves = left >= kBwdWaves * CW ? kBwdWaves : (left + CW - 1) / CW;
+  for (int i = tid; i < len * 2 * NP; i += kBwdThreads) {
     const int tok = i / (2 * NP), e = i % (2 * NP);
     const float* q = smem + 2 * TB * NP + (tok / kSub) * SLOT + (tok % kSub) * 2 * NP + e;
     float v = 0.0f;
     for (int w = 0; w < waves; ++w) v += q[w * SUBS * SLOT];
-    io.bcpart[(((b * sh.L + t0 + tok) * sh.G + g) * sh.tiles + tile % sh.tiles) * 2 * NP + e] = v;
+    io.bcpart[(((b * sh.L + t0 + tok) * groups + g) * tiles + tile % tiles) * 2 * NP + e] = v;
   }
 }
 
@@ -382,7 +401,7 @@ selscan_reduce_a_kernel(const float* __restrict__ dAp, const float* __restrict__
 
 static ScanShape bwd_shape(int64_t L, int64_t D, int64_t N, int64_t G) {
   ScanShape s;
-  const int rn = selscan_rn(N);
+  const int rn = selscan_np(N) / 4;
   const int64_t per = 128 / rn * kBwdWaves;
   s.L = L; s.D = D; s.N = N; s.G = G; s.Dg = D / G;
   s.T = bwd_tokens(rn);
@@ -404,7 +423,7 @@ static ScanBwdLayout bwd_layout(int64_t batch, const ScanShape& s) {
   w.dd = w.sum + sm;
   w.db = w.dd + sm;
   w.bc = w.db + sm;
-  w.bytes = w.bc + up256(size_t(batch) * s.L * s.G * s.tiles * 8 * selscan_rn(s.N) * sizeof(float));
+  w.bytes = w.bc + up256(size_t(batch) * s.L * s.G * s.tiles * 2 * selscan_np(s.N) * sizeof(float));
   return w;
 }
 
@@ -417,7 +436,7 @@ size_t selscan_bwd_workspace(int64_t batch, int64_t L, int64_t D, int64_t N, int
 int selscan_grid_ok(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
   const ScanShape s = bwd_shape(L, D, N, G);
   const __int128 most = (1 << 24) - 1;   // of 256 threads each: a launch has fewer than 2^32
-  const int np = 4 * selscan_rn(N);
+  const int np = selscan_np(N);
   return batch <= 65535 && (__int128)s.tiles * G * s.K <= most &&
          (__int128)batch * L * G * 2 * np / 256 < most &&
          (__int128)batch * D * np / 64 < most;
@@ -425,7 +444,7 @@ int selscan_grid_ok(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
 
 // The forward kernels tile channels more widely than the backward one.
 static ScanShape fwd_tiles(ScanShape s) {
-  const int64_t per = 256 / selscan_rn(s.N) * 4;
+  const int64_t per = 1024 / selscan_np(s.N) * 4;
   s.tiles = (s.Dg + per - 1) / per;
   return s;
 }
@@ -491,7 +510,7 @@ static hipError_t bwd_rn(const ScanArgs& a, hipStream_t stream) {
 }
 template <typename T>
 static hipError_t bwd_t(const ScanArgs& a, hipStream_t stream) {
-  const int rn = selscan_rn(a.N);
+  const int rn = selscan_np(a.N) / 4;
   if (rn == 4) return bwd_rn<T, 4>(a, stream);
   if (rn == 8) return bwd_rn<T, 8>(a, stream);
   return bwd_rn<T, 16>(a, stream);
