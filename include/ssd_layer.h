@@ -150,8 +150,8 @@ ssd_status ssd_selscan_fwd_workspace_size(const ssd_selscan_problem* prob, size_
  *   init_state, final_state : [batch, channels, dstate] fp32, or NULL.
  *   workspace   : ssd_selscan_fwd_workspace_size bytes (which may be 0: then it
  *                 may be NULL).
- * Errors: UNSUPPORTED for dstate > 64, batch > 65535, or sizes past a
- * launch's 2^32 threads. */
+ * Errors: UNSUPPORTED for dstate > 64, batch > 65535, tokens of z 2^28 bytes or
+ * more apart, or sizes past a launch's 2^32 threads. */
 ssd_status ssd_selscan_fwd(const ssd_selscan_problem* prob, const ssd_dt_transform* dtx,
                            const void* x, const void* dt, const float* A, const void* B,
                            const ssd_strides* b_strides, const void* C,

@@ -192,8 +192,15 @@ ssd_status scan_shape(const ssd_selscan_problem& p) {
 ssd_status scan_supported(const ssd_selscan_problem& p) {
   if (p.dstate > 64)
     return fail(SSD_ERR_UNSUPPORTED, "dstate must be at most 64 (got %lld)", (long long)p.dstate);
-  if (!ssd::selscan_grid_ok(p.batch, p.seqlen, p.channels, p.dstate, p.ngroups))
+  if (p.channels > (1 << 24) || !ssd::selscan_grid_ok(p.batch, p.seqlen, p.channels, p.dstate, p.ngroups))
     return fail(SSD_ERR_UNSUPPORTED, "grid too large for this build");
+  return SSD_OK;
+}
+// The kernels reach eight rows of z and dz by 32-bit byte offsets.
+ssd_status scan_rows(const ssd_selscan_problem& p, const ssd::ScanArgs& a) {
+  const int64_t most = (int64_t(1) << 28) / (int64_t)element(p.io_dtype);
+  if ((a.z && a.zs[1] > most) || (a.dz && a.dzs[1] > most))
+    return fail(SSD_ERR_UNSUPPORTED, "tokens of z and dz must be less than 2^28 bytes apart");
   return SSD_OK;
 }
 ssd_status scan_transform(const ssd_dt_transform* dtx, ssd::DtXform* xf) {
@@ -408,6 +415,7 @@ ssd_status ssd_selscan_fwd(const ssd_selscan_problem* prob, const ssd_dt_transfo
     st = scan_alignment(*prob, a, dtx);
     if (st != SSD_OK) return st;
     st = scan_supported(*prob);
+    if (st == SSD_OK) st = scan_rows(*prob, a);
     if (st != SSD_OK) return st;
     const size_t need = ssd::selscan_fwd_workspace(a.batch, a.L, a.D, a.N, a.G);
     if (need > 0 && (!workspace || workspace_bytes < need))
@@ -490,6 +498,7 @@ ssd_status ssd_selscan_bwd(const ssd_selscan_problem* prob, const ssd_dt_transfo
     st = scan_alignment(*prob, a, dtx);
     if (st != SSD_OK) return st;
     st = scan_supported(*prob);
+    if (st == SSD_OK) st = scan_rows(*prob, a);
     if (st != SSD_OK) return st;
     const size_t need = ssd::selscan_bwd_workspace(a.batch, a.L, a.D, a.N, a.G);
     if (workspace_bytes < need)

@@ -75,8 +75,15 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
   const int n0 = 8 * nl;
   const int own = base + dl * 2 + (lane & 1);   // the channel this lane prepares
   const int c = g * Dg + (own < Dg ? own : Dg - 1);
-  const unsigned at = (unsigned)c * sizeof(T);
   const bool mine = own < Dg && nl < 2;
+  // byte offsets of the lane's channel in U rows of x, dt, dy and y, and of z; lanes
+  // that share a channel store the same value
+  unsigned ox[U], oz[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    ox[u] = own < Dg ? (unsigned)(u * sh.D + c) * (unsigned)sizeof(T) : kOutside;
+    oz[u] = GATE && own < Dg ? (unsigned)(u * io.zs.token + c) * (unsigned)sizeof(T) : kOutside;
+  }
   const int64_t t0 = k * sh.T;
   const int len = (int)(t0 + sh.T < sh.L ? sh.T : sh.L - t0);   // tokens of this chunk
 
@@ -94,8 +101,37 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
       R[j][i] = 0.0f;
       if (k == 0) {
         if (io.init && n < N) h[j][i] = io.init[(b * sh.D + cj) * N + n];
-      } else if (MODE == kOut) {
-        h[j][i] = io.H[((b * sh.K + k) * sh.D + cj) * NP + n];
+      }
+    }
+  }
+  if constexpr (MODE == kOut) {
+    // the start state: the chunks before this one, chained.  Slot m of H holds chunk
+    // m - 1's end state from a zero start, chunk 0's from the caller's
+    if (k > 0) {
+      constexpr int M = 4;   // chunks loaded at a time
+      for (int m0 = 1; m0 <= k; m0 += M) {
+        float s[M][2], v[M][2][8];
+#pragma unroll
+        for (int u = 0; u < M; ++u) {
+          const int m = m0 + u <= k ? m0 + u : k;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int lc = base + dl * 2 + j;
+            const int64_t at = (b * sh.K + m) * sh.D + g * Dg + (lc < Dg ? lc : Dg - 1);
+            s[u][j] = io.sumdt[at - sh.D];
+#pragma unroll
+            for (int q = 0; q < 8; q += 4) load_v<4>(io.H + at * NP + n0 + q, v[u][j] + q);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < M; ++u)
+          if (m0 + u <= k)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                h[j][i] = m0 + u == 1 ? v[u][j][i]
+                                      : fmaf(fast_exp2(A2[j][i] * s[u][j]), h[j][i], v[u][j][i]);
       }
     }
   }
@@ -136,14 +172,23 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
 
   T xr[U], dr[U], zr[U], gr[U];
   auto load = [&](int t) {
-    const unsigned o = here_offset(at);
+    const int valid = t + U <= len ? U : len - t;
+    const Rows rx = rows_at(xp + t * sh.D, valid, sh.D, sh.D);
+    const Rows rd = rows_at(dp + t * sh.D, valid, sh.D, sh.D);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t tok = t + u < len ? t + u : len - 1;
-      xr[u] = row_load(xp + tok * sh.D, o);
-      dr[u] = row_load(dp + tok * sh.D, o);
-      if constexpr (GATE && MODE != kStates) zr[u] = row_load(zp + tok * io.zs.token, o);
-      if constexpr (MODE == kBoth) gr[u] = row_load(gp + tok * sh.D, o);
+      xr[u] = row_load<T>(rx, ox[u]);
+      dr[u] = row_load<T>(rd, ox[u]);
+    }
+    if constexpr (GATE && MODE != kStates) {
+      const Rows rz = rows_at(zp + t * io.zs.token, valid, io.zs.token, sh.D);
+#pragma unroll
+      for (int u = 0; u < U; ++u) zr[u] = row_load<T>(rz, oz[u]);
+    }
+    if constexpr (MODE == kBoth) {
+      const Rows rg = rows_at(gp + t * sh.D, valid, sh.D, sh.D);
+#pragma unroll
+      for (int u = 0; u < U; ++u) gr[u] = row_load<T>(rg, ox[u]);
     }
   };
 
@@ -169,10 +214,15 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
         }
         if (ts + U < len) load(ts + U);
         dt_values<U, false>(f, d, none);
-        const unsigned o_at = here_offset(at);
+        if (ts + U > len) {   // past the last token x and dy are zero; the decays have to be one
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (ts + u >= len) d[u] = 0.0f;
+        }
+        const Rows ry = rows_at(MODE == kOut ? yp0 + ts * sh.D : nullptr, ts + U <= len ? U : len - ts,
+                                sh.D, sh.D);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          if (ts + u >= len) d[u] = xv[u] = ds[u] = 0.0f;
           dx[u] = d[u] * xv[u];
           if constexpr (GATE && MODE != kStates) gate[u] *= sigmoid_f32(gate[u]);
           if constexpr (MODE == kBoth) ds[u] *= gate[u];
@@ -206,8 +256,7 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
           channel(std::integral_constant<int, 1>{});
           if constexpr (MODE == kOut) {
             const float o = pairs_sum<RN>(pair_fold(part[0], part[1], lane));
-            if (mine && ts + u < len)
-              row_store(yp0 + (int64_t)(ts + u) * sh.D, o_at, to_io<T>(fmaf(Dc, xv[u], o) * gate[u]));
+            row_store<T>(ry, ox[u], to_io<T>(fmaf(Dc, xv[u], o) * gate[u]));
           }
         }
       }
@@ -368,9 +417,11 @@ ScanShape selscan_fwd_shape(int64_t batch, int64_t L, int64_t D, int64_t N, int6
   s.K = 1;
   s.T = L;
   if (waves < 640 && L > 128) {
-    int64_t k = (3072 + waves - 1) / waves;
-    if (k > L / 64) k = L / 64;
-    s.T = ((L + k - 1) / k + kScanTile - 1) / kScanTile * kScanTile;
+    int64_t k = 2000 / waves;
+    if (k > L / 32) k = L / 32;
+    if (k > 64) k = 64;
+    if (k < 1) k = 1;
+    s.T = ((L + k - 1) / k + 7) / 8 * 8;
     s.K = (L + s.T - 1) / s.T;
   }
   return s;
@@ -438,13 +489,8 @@ static hipError_t fwd_np(const ScanArgs& a, hipStream_t stream) {
     io.H = static_cast<float*>(a.workspace);
     io.sumdt = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + selscan_state_bytes(a.batch, s));
     launch_scan<T, NP, kStates>(io, s, a.batch, s.K - 1, stream);
-    hipError_t e = hipGetLastError();
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (s.K > 2) {
-      launch_selscan_pass(io.H, a.A, io.sumdt, nullptr, a.batch, s, 0, stream);
-      e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
   }
   launch_scan<T, NP, kOut>(io, s, a.batch, s.K, stream);
   return hipGetLastError();

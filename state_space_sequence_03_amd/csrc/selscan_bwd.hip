@@ -132,27 +132,37 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
     const T* const zp = GATE ? io.z + b * io.zs.batch + t0 * io.zs.token : nullptr;
     T* const zo = GATE ? io.dz + b * io.dzs.batch + t0 * io.dzs.token : nullptr;
     const int subs = (len + kSub - 1) / kSub;
-    // byte offsets from a pair's first row: the lane's channel, in its own token's row
-    // where that is inside the chunk (a pair's rows are less than 4 GiB apart)
-    const unsigned here = (unsigned)c * sizeof(T);
-    const unsigned od = here + par * (unsigned)(sh.D * sizeof(T));
-    const unsigned oz = GATE ? here + par * (unsigned)(io.zs.token * sizeof(T)) : 0;
-    const unsigned ozo = GATE ? here + par * (unsigned)(io.dzs.token * sizeof(T)) : 0;
+    // byte offsets of the lane's channel and token in 8 rows; lanes that share both
+    // store the same values
+    unsigned ox[kPairs], oz[kPairs], ozo[kPairs];
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) {
+      const int u = 2 * p + par;
+      ox[p] = own < Dg ? (unsigned)(u * sh.D + c) * (unsigned)sizeof(T) : kOutside;
+      oz[p] = GATE && own < Dg ? (unsigned)(u * io.zs.token + c) * (unsigned)sizeof(T) : kOutside;
+      ozo[p] = GATE && own < Dg ? (unsigned)(u * io.dzs.token + c) * (unsigned)sizeof(T) : kOutside;
+    }
 
     // forwards, one checkpoint per 8 tokens
     T xr[kPairs], dr[kPairs], zr[kPairs], yr[kPairs];
     auto load = [&](int s, bool all) {
-      const unsigned o_here = here_offset(here), o_d = here_offset(od), o_z = here_offset(oz);
+      const int64_t t = s * kSub;
+      const int valid = s * kSub + kSub <= len ? kSub : len - s * kSub;
+      const Rows rx = rows_at(xp + t * sh.D, valid, sh.D, sh.D);
+      const Rows rd = rows_at(dp + t * sh.D, valid, sh.D, sh.D);
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) {
-        const int t = s * kSub + 2 * p;
-        const int64_t first = t < len ? t : 0;       // uniform: the pair's first row, or any row inside
-        const bool both = t + 1 < len;
-        xr[p] = row_load(xp + first * sh.D, both ? o_d : o_here);
-        dr[p] = row_load(dp + first * sh.D, both ? o_d : o_here);
-        if (all) {
-          yr[p] = row_load(gp + first * sh.D, both ? o_d : o_here);
-          if constexpr (GATE) zr[p] = row_load(zp + first * io.zs.token, both ? o_z : o_here);
+        xr[p] = row_load<T>(rx, ox[p]);
+        dr[p] = row_load<T>(rd, ox[p]);
+      }
+      if (all) {
+        const Rows rg = rows_at(gp + t * sh.D, valid, sh.D, sh.D);
+#pragma unroll
+        for (int p = 0; p < kPairs; ++p) yr[p] = row_load<T>(rg, ox[p]);
+        if constexpr (GATE) {
+          const Rows rz = rows_at(zp + t * io.zs.token, valid, io.zs.token, sh.D);
+#pragma unroll
+          for (int p = 0; p < kPairs; ++p) zr[p] = row_load<T>(rz, oz[p]);
         }
       }
     };
@@ -209,16 +219,19 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
       dt_values<kPairs, true>(f, d, slope);
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) {
-        // past the last token and past the group's last channel nothing is added
-        const bool in = s * kSub + 2 * p + par < len && own < Dg;
         xv[p] = to_f32(xr[p]);
-        yv[p] = in ? to_f32(yr[p]) : 0.0f;
+        yv[p] = to_f32(yr[p]);   // x and dy are zero past the last token and the last channel
         zv[p] = GATE ? to_f32(zr[p]) : 0.0f;
-        d[p] = in ? d[p] : 0.0f;
-        dx[p] = in ? d[p] * xv[p] : 0.0f;
+        if (s * kSub + 2 * p + par >= len) d[p] = slope[p] = 0.0f;
+        dx[p] = d[p] * xv[p];
         ds[p] = GATE ? yv[p] * (zv[p] * sigmoid_f32(zv[p])) : yv[p];
       }
       if (s > 0) load(s - 1, true);
+      const int valid = s * kSub + kSub <= len ? kSub : len - s * kSub;
+      const Rows wx = rows_at(io.dx + row + (int64_t)s * kSub * sh.D, valid, sh.D, sh.D);
+      const Rows wd = rows_at(io.ddt + row + (int64_t)s * kSub * sh.D, valid, sh.D, sh.D);
+      const Rows wz = rows_at(GATE ? zo + (int64_t)s * kSub * io.dzs.token : nullptr, valid,
+                              GATE ? io.dzs.token : 0, sh.D);
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) {
         float yp[4];
@@ -245,11 +258,7 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
         token(std::integral_constant<int, 1>{});
         if constexpr (GATE) {
           const float o = fmaf(Dc, xv[p], quads_sum<RN>(quad_fold(yp, lane)));
-          const int t = s * kSub + 2 * p + par;
-          const float sg = sigmoid_f32(zv[p]);
-          if (mine && t < len)
-            row_store(zo + (int64_t)(s * kSub + 2 * p) * io.dzs.token, ozo,
-                      to_io<T>(yv[p] * o * silu_slope(zv[p], sg)));
+          row_store<T>(wz, ozo[p], to_io<T>(yv[p] * o * silu_slope(zv[p], sigmoid_f32(zv[p]))));
         }
       }
 #pragma unroll
@@ -288,17 +297,11 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
         token(std::integral_constant<int, 0>{});
         const float qv = quads_sum<RN>(quad_fold(vq, lane));
         const float rv = quads_sum<RN>(quad_fold(vr, lane)) * 0.6931471805599453f;   // A2 = A log2 e
-        const int t = s * kSub + 2 * p + par;
-        if (t < len) {
-          const float ddt = fmaf(xv[p], qv, rv) * slope[p];
-          dbias += ddt;
-          dD = fmaf(ds[p], xv[p], dD);
-          if (mine) {
-            const int64_t first = row + (int64_t)(s * kSub + 2 * p) * sh.D;
-            row_store(io.dx + first, od, to_io<T>(fmaf(d[p], qv, Dc * ds[p])));
-            row_store(io.ddt + first, od, to_io<T>(ddt));
-          }
-        }
+        const float ddt = fmaf(xv[p], qv, rv) * slope[p];   // (past the end x, ds and slope are zero)
+        dbias += ddt;
+        dD = fmaf(ds[p], xv[p], dD);
+        row_store<T>(wx, ox[p], to_io<T>(fmaf(d[p], qv, Dc * ds[p])));
+        row_store<T>(wd, ox[p], to_io<T>(ddt));
         // the wave's sums over channels: the lower half of the wave gets the pair's
         // first token, even rows states 0 and 1 of the four, odd rows 2 and 3
         auto channels = [&](const float (&v)[8], int which) {

@@ -34,29 +34,29 @@ template <int J> __device__ __forceinline__ float pair_bcast(float v) {
   return r;
 }
 
-// An element of a row: the row's pointer is uniform (a pair of scalar registers),
-// the lane's place in it a 32-bit byte offset, so that no lane adds 64-bit
-// addresses.  The empty statement keeps the compiler from adding the offset first.
-template <typename T> struct GlobalPtr {
-  typedef __attribute__((address_space(1))) T* type;
-};
-__device__ __forceinline__ unsigned here_offset(unsigned bytes) {
-  __asm__("" : "+v"(bytes));   // the same for the offset: its widening stays beside the accesses
-  return bytes;
+// A few rows of a [token][channel] operand through a buffer resource: a lane's
+// byte offsets from the first row stay in registers, moving on by some rows costs
+// scalar work only, and the resource ends after the last valid row, so that loads
+// past it give zero and stores past it are dropped, as at kOutside for lanes
+// without a channel.
+typedef __amdgpu_buffer_rsrc_t Rows;
+constexpr unsigned kOutside = 0xffffff00u;
+template <typename T>
+__device__ __forceinline__ Rows rows_at(const T* first, int valid, int64_t stride, int64_t width) {
+  const unsigned bytes = (unsigned)(valid - 1) * (unsigned)(stride * sizeof(T)) + (unsigned)(width * sizeof(T));
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(first), (short)0, (int)bytes, 0x00020000);
 }
-template <typename T> __device__ __forceinline__ T row_load(const T* row, unsigned bytes) {
-  uint64_t base = reinterpret_cast<uint64_t>(row);
-  __asm__("" : "+s"(base));
-  typedef typename GlobalPtr<const T>::type Ptr;
-  typedef typename GlobalPtr<const char>::type Bytes;
-  return *reinterpret_cast<Ptr>(reinterpret_cast<Bytes>(base) + bytes);
+template <typename T> __device__ __forceinline__ T row_load(Rows r, unsigned bytes) {
+  if constexpr (sizeof(T) == 2)
+    return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, (int)bytes, 0, 0));
+  else
+    return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, (int)bytes, 0, 0));
 }
-template <typename T> __device__ __forceinline__ void row_store(T* row, unsigned bytes, T v) {
-  uint64_t base = reinterpret_cast<uint64_t>(row);
-  __asm__("" : "+s"(base));
-  typedef typename GlobalPtr<T>::type Ptr;
-  typedef typename GlobalPtr<char>::type Bytes;
-  *reinterpret_cast<Ptr>(reinterpret_cast<Bytes>(base) + bytes) = v;
+template <typename T> __device__ __forceinline__ void row_store(Rows r, unsigned bytes, T v) {
+  if constexpr (sizeof(T) == 2)
+    __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(unsigned short, v), r, (int)bytes, 0, 0);
+  else
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned, v), r, (int)bytes, 0, 0);
 }
 
 // Two values summed over pairs of lanes: even lanes get v0's sums, odd lanes v1's.
@@ -106,6 +106,11 @@ __device__ __forceinline__ float rows_fold(float v0, float v1) {
 // where softplus is on, zero where the clamp holds (its ends pass the
 // gradient).  The uniform branch is taken once for all M, whose independent
 // chains of exp2, log and reciprocal then overlap.
+//
+// softplus(v) = max(v, 0) + log1p(w) with w = e^-|v| <= 1.  For u = 1 + w as
+// rounded, c = w - (u - 1) is exact and log1p(w) = log(u) + log(1 + c / u); c is at
+// most half a step of u, so c for the second term is off by less than 2^-24
+// (u - 1) < 1.5 2^-24 log(u).  The logistic is 1 / u or w / u.
 struct DtLane {
   float bias, lo, hi;
   int softplus;
@@ -120,8 +125,11 @@ __device__ __forceinline__ void dt_values(const DtLane& f, float (&v)[M], float 
   if (f.softplus) {
 #pragma unroll
     for (int u = 0; u < M; ++u) {
-      if constexpr (SLOPE) slope[u] = sigmoid_f32(v[u]);
-      v[u] = softplus_f32(v[u]);
+      const float w = fast_exp2(-fabsf(v[u]) * kLog2e);
+      const float s = 1.0f + w;
+      if constexpr (SLOPE) slope[u] = (v[u] >= 0.0f ? 1.0f : w) * __builtin_amdgcn_rcpf(s);
+      const float c = w - (s - 1.0f);
+      v[u] = fmaxf(v[u], 0.0f) + fmaf(__builtin_amdgcn_logf(s), 0.6931471805599453f, c);
     }
   } else if constexpr (SLOPE) {
 #pragma unroll
@@ -131,7 +139,7 @@ __device__ __forceinline__ void dt_values(const DtLane& f, float (&v)[M], float 
   for (int u = 0; u < M; ++u) {
     if constexpr (SLOPE)
       if (!(v[u] >= f.lo && v[u] <= f.hi)) slope[u] = 0.0f;
-    v[u] = fminf(fmaxf(v[u], f.lo), f.hi);
+    v[u] = __builtin_amdgcn_fmed3f(v[u], f.lo, f.hi);
   }
 }
 
