@@ -10,8 +10,8 @@ stride.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 from typing import Optional, Sequence, Tuple, Union
 
 import torch
@@ -74,76 +74,107 @@ def declare(lib, dt_transform) -> None:
 
 
 # The helpers of the binding's other half (tensor checks, errors, streams).
-from . import (SsdArgumentError, _check, _dev, _dt_transform, _io_code, _stream,  # noqa: E402
-               load_library)
+from . import SsdArgumentError, _check, _dt_transform, _io_code, load_library  # noqa: E402
+
+_F32 = torch.float32
 
 
 def ssd_layer_abi_version() -> int:
     return int(load_library().ssd_layer_abi_version())
 
 
-def _on(device: torch.device):
-    """A context in which `device` is the current one: launches go to streams of
-    the current device."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+# A call's cost is its arguments' marshalling for single tokens, so the checks
+# below take one pass over a tensor's properties and say what was wrong only
+# after one failed, and what depends on shapes alone (problem structs, strides,
+# workspace sizes) is made once per shape.
 
-
-def _same_device(x, *tensors):
-    for t in tensors:
-        if t is not None and t.device != x.device:
-            raise SsdArgumentError(1, "every tensor must be on the device of x (%s), got %s"
-                                   % (x.device, t.device))
-
-
-def _rows(t: Optional[torch.Tensor], name: str, dtype, shape):
-    """(pointer, ssd_strides reference) of a strided operand."""
+def _plain(t: Optional[torch.Tensor], name: str, dtype, shape, dev: int):
+    """Pointer of a contiguous operand of the given type, shape and device (None for None)."""
     if t is None:
-        return None, None
+        return None
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape, dev)
+    raise SsdArgumentError(2, "%s must be contiguous" % name)
+
+
+def _refuse(t, name, dtype, shape, dev):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise SsdArgumentError(1, "%s must be a GPU tensor" % name)
     if tuple(t.shape) != tuple(shape):
         raise SsdArgumentError(2, "%s must be %s, got %s" % (name, list(shape), list(t.shape)))
     if t.dtype != dtype:
         raise SsdArgumentError(4, "%s must be %s, got %s" % (name, dtype, t.dtype))
-    inner = 1
-    for i in range(t.dim() - 1, 1, -1):
-        if t.shape[i] != 1 and t.stride(i) != inner:
-            raise SsdArgumentError(2, "%s must be contiguous beyond its first two axes" % name)
-        inner *= t.shape[i]
-    return t.data_ptr(), ctypes.byref(ssd_strides(t.stride(0), t.stride(1)))
+    if t.get_device() != dev:
+        raise SsdArgumentError(1, "%s must be on the device of x (cuda:%d), got %s" % (name, dev, t.device))
 
 
-def _plain(t: Optional[torch.Tensor], name: str, dtype, shape):
-    """Pointer of a contiguous operand of the given shape."""
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise SsdArgumentError(2, "%s must be %s, got %s" % (name, list(shape), list(t.shape)))
-    return _dev(t, name, dtype)
+@functools.lru_cache(maxsize=1024)
+def _strides(batch: int, token: int):
+    return ctypes.byref(ssd_strides(batch, token))
 
 
-def _f32(x, *shape):
-    return torch.empty(shape, dtype=torch.float32, device=x.device)
+def _rows(t: Optional[torch.Tensor], name: str, dtype, shape, dev: int):
+    """(pointer, ssd_strides reference) of a strided operand."""
+    if t is None:
+        return None, None
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
+            s = t.stride()
+            inner = 1
+            for i in range(len(s) - 1, 1, -1):
+                if shape[i] != 1 and s[i] != inner:
+                    raise SsdArgumentError(2, "%s must be contiguous beyond its first two axes" % name)
+                inner *= shape[i]
+            return t.data_ptr(), _strides(s[0], s[1])
+    except AttributeError:
+        pass
+    _refuse(t, name, dtype, shape, dev)
+    raise SsdArgumentError(2, "%s must be %s" % (name, list(shape)))
+
+
+def _three(x, name="x"):
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise SsdArgumentError(1, "%s must be a GPU tensor" % name)
+    shape = x.shape
+    if len(shape) != 3:
+        raise SsdArgumentError(2, "%s must be [batch, seqlen, channels]" % name)
+    return tuple(shape)
+
+
+def _scratch(x, workspace, need: int, dev: int):
+    """(pointer, bytes) of the caller's workspace or of a new one."""
+    if workspace is None:
+        if not need:
+            return None, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev:
+        raise SsdArgumentError(1, "workspace must be a GPU tensor on the device of x")
+    elif not workspace.is_contiguous():
+        raise SsdArgumentError(2, "workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _launch(fn, dev: int, *args) -> None:
+    """Call an entry point on the current stream of device `dev`, with that device
+    current: launches go to streams of the current device."""
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, stream)
+    if st:
+        _check(st)
 
 
 def _size(fn, prob) -> int:
     n = ctypes.c_size_t(0)
     _check(fn(ctypes.byref(prob), ctypes.byref(n)))
     return int(n.value)
-
-
-def _scratch(x, workspace, need):
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
-    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
-
-
-def _three(x, name="x"):
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
-        raise SsdArgumentError(1, "%s must be a GPU tensor" % name)
-    if x.dim() != 3:
-        raise SsdArgumentError(2, "%s must be [batch, seqlen, channels]" % name)
-    return x.shape
 
 
 # ---------------------------------------------------------------- convolution
@@ -160,31 +191,42 @@ def make_conv_problem(batch, seqlen, channels, width, split, io_dtype, activatio
                             int(activation), 0)
 
 
+@functools.lru_cache(maxsize=1024)
+def _conv_problem(*args):
+    return ctypes.byref(make_conv_problem(*args))
+
+
+@functools.lru_cache(maxsize=1024)
+def _conv_bwd_bytes(*args):
+    return _size(load_library().ssd_conv_bwd_workspace_size, make_conv_problem(*args))
+
+
 def _conv(x, weight, bias, activation, split):
-    bsz, L, C = _three(x)
+    """(device, shape of x, width, sizes of the split, problem arguments, pointers)."""
+    shape = _three(x)
+    dev = x.get_device()
     if activation not in _ACTIVATIONS:
         raise SsdArgumentError(10, "activation must be None or 'silu', got %r" % (activation,))
-    if weight.dim() != 2 or weight.shape[0] != C:
+    wshape = tuple(weight.shape)
+    if len(wshape) != 2 or wshape[0] != shape[2]:
         raise SsdArgumentError(2, "weight must be [channels, width]")
-    prob = make_conv_problem(bsz, L, C, weight.shape[1], (C,) if split is None else split, _io_code(x),
-                             _ACTIVATIONS[activation])
-    return prob, _rows(x, "x", x.dtype, x.shape), _plain(weight, "weight", torch.float32, weight.shape), \
-        _plain(bias, "bias", torch.float32, (C,))
+    sizes = (shape[2],) if split is None else tuple(split)
+    key = shape + (wshape[1], sizes, _io_code(x), _ACTIVATIONS[activation])
+    ptrs = _rows(x, "x", x.dtype, shape, dev) + (_plain(weight, "weight", _F32, wshape, dev),
+                                                 _plain(bias, "bias", _F32, (shape[2],), dev))
+    return dev, shape, wshape[1], sizes, key, ptrs
 
 
-def _conv_outputs(x, split, out):
+def _conv_outputs(x, shape, sizes, split, out):
     if out is None:
-        sizes = (x.shape[2],) if split is None else split
-        return [torch.empty((x.shape[0], x.shape[1], int(c)), dtype=x.dtype, device=x.device) for c in sizes]
+        return [x.new_empty((shape[0], shape[1], c)) for c in sizes]
     return [out] if split is None else list(out)
 
 
-def _conv_parts(ts, x, split, name):
-    sizes = (x.shape[2],) if split is None else split
+def _conv_parts(ts, x, shape, sizes, name, dev):
     if len(ts) != len(sizes):
         raise SsdArgumentError(2, "%s must have one tensor per part of the split" % name)
-    _same_device(x, *ts)
-    return (ctypes.c_void_p * 3)(*[_plain(t, name, x.dtype, (x.shape[0], x.shape[1], int(c)))
+    return (ctypes.c_void_p * 3)(*[_plain(t, name, x.dtype, (shape[0], shape[1], c), dev)
                                    for t, c in zip(ts, sizes)])
 
 
@@ -200,17 +242,15 @@ def ssd_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Ten
     of them, each contiguous (what ssd_fwd takes as x, B and C after a view).
     final_state, where wanted, holds the last width - 1 inputs."""
     lib = load_library()
-    prob, (xp, xs), wp, bp = _conv(x, weight, bias, activation, split)
-    state = (x.shape[0], weight.shape[1] - 1, x.shape[2])
-    ys = _conv_outputs(x, split, out)
+    dev, shape, width, sizes, key, ptrs = _conv(x, weight, bias, activation, split)
+    state = (shape[0], width - 1, shape[2])
+    ys = _conv_outputs(x, shape, sizes, split, out)
     fin = None
     if want_final_state:
-        fin = final_out if final_out is not None else torch.empty(state, dtype=x.dtype, device=x.device)
-    _same_device(x, weight, bias, init_state, fin)
-    args = (xp, xs, wp, bp, _plain(init_state, "init_state", x.dtype, state),
-            _conv_parts(ys, x, split, "out"), _plain(fin, "final_out", x.dtype, state))
-    with _on(x.device):
-        _check(lib.ssd_conv_fwd(ctypes.byref(prob), *args, _stream(x.device)))
+        fin = final_out if final_out is not None else x.new_empty(state)
+    _launch(lib.ssd_conv_fwd, dev, _conv_problem(*key), *ptrs,
+            _plain(init_state, "init_state", x.dtype, state, dev),
+            _conv_parts(ys, x, shape, sizes, "out", dev), _plain(fin, "final_out", x.dtype, state, dev))
     return (ys[0] if split is None else ys), fin
 
 
@@ -220,13 +260,11 @@ def ssd_conv_step(state: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     """Advance ``state`` [batch, width - 1, channels] (io dtype, in place) through the
     seqlen tokens of x.  Returns y as ssd_conv_fwd does."""
     lib = load_library()
-    prob, (xp, xs), wp, bp = _conv(x, weight, bias, activation, split)
-    ys = _conv_outputs(x, split, out)
-    _same_device(x, weight, bias, state)
-    sp = _plain(state, "state", x.dtype, (x.shape[0], weight.shape[1] - 1, x.shape[2]))
-    parts = _conv_parts(ys, x, split, "out")
-    with _on(x.device):
-        _check(lib.ssd_conv_step(ctypes.byref(prob), sp, xp, xs, wp, bp, parts, _stream(x.device)))
+    dev, shape, width, sizes, key, ptrs = _conv(x, weight, bias, activation, split)
+    ys = _conv_outputs(x, shape, sizes, split, out)
+    _launch(lib.ssd_conv_step, dev, _conv_problem(*key),
+            _plain(state, "state", x.dtype, (shape[0], width - 1, shape[2]), dev), *ptrs,
+            _conv_parts(ys, x, shape, sizes, "out", dev))
     return ys[0] if split is None else ys
 
 
@@ -246,25 +284,20 @@ def ssd_conv_bwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Ten
     lib = load_library()
     one = isinstance(dy, torch.Tensor)
     dys = [dy] if one else list(dy)
-    for t in dys:
-        _three(t, "dy")
-    split = None if one else [t.shape[2] for t in dys]
-    prob, (xp, xs), wp, bp = _conv(x, weight, bias, activation, split)
-    state = (x.shape[0], weight.shape[1] - 1, x.shape[2])
-    parts = _conv_parts(dys, x, split, "dy")
-    dx = dx_out if dx_out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    dw = _f32(x, *weight.shape)
-    db = _f32(x, x.shape[2]) if bias is not None else None
-    dinit = torch.empty(state, dtype=x.dtype, device=x.device) if want_dinit else None
-    _same_device(x, weight, bias, init_state, dfinal, dx, workspace)
-    dxp, dxs = _rows(dx, "dx_out", x.dtype, x.shape)
-    ws, ws_bytes = _scratch(x, workspace, _size(lib.ssd_conv_bwd_workspace_size, prob)
-                            if workspace is None else 0)
-    args = (xp, xs, wp, bp, _plain(init_state, "init_state", x.dtype, state), parts,
-            _plain(dfinal, "dfinal", x.dtype, state), dxp, dxs, _dev(dw, "dweight"), _dev(db, "dbias"),
-            _dev(dinit, "dinit"), ws, ws_bytes)
-    with _on(x.device):
-        _check(lib.ssd_conv_bwd(ctypes.byref(prob), *args, _stream(x.device)))
+    split = None if one else [_three(t, "dy")[2] for t in dys]
+    dev, shape, width, sizes, key, ptrs = _conv(x, weight, bias, activation, split)
+    state = (shape[0], width - 1, shape[2])
+    parts = _conv_parts(dys, x, shape, sizes, "dy", dev)
+    dx = dx_out if dx_out is not None else x.new_empty(shape)
+    dw = weight.new_empty((shape[2], width))
+    db = weight.new_empty((shape[2],)) if bias is not None else None
+    dinit = x.new_empty(state) if want_dinit else None
+    ws, ws_bytes, held = _scratch(x, workspace, _conv_bwd_bytes(*key) if workspace is None else 0, dev)
+    _launch(lib.ssd_conv_bwd, dev, _conv_problem(*key), *ptrs,
+            _plain(init_state, "init_state", x.dtype, state, dev), parts,
+            _plain(dfinal, "dfinal", x.dtype, state, dev), *_rows(dx, "dx_out", x.dtype, shape, dev),
+            dw.data_ptr(), None if db is None else db.data_ptr(),
+            None if dinit is None else dinit.data_ptr(), ws, ws_bytes)
     return {"dx": dx, "dweight": dw, "dbias": db, "dinit": dinit}
 
 
@@ -275,21 +308,35 @@ def make_selscan_problem(batch, seqlen, channels, dstate, ngroups, io_dtype) -> 
                                int(io_dtype), 0)
 
 
+@functools.lru_cache(maxsize=1024)
+def _scan_problem(*args):
+    return ctypes.byref(make_selscan_problem(*args))
+
+
+@functools.lru_cache(maxsize=1024)
+def _scan_bytes(backward, *args):
+    lib = load_library()
+    return _size(lib.ssd_selscan_bwd_workspace_size if backward else lib.ssd_selscan_fwd_workspace_size,
+                 make_selscan_problem(*args))
+
+
 def _selscan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit):
-    bsz, L, ch = _three(x)
+    """(device, problem arguments, (transform, its reference), pointers, state's shape)."""
+    shape = _three(x)
+    dev, io = x.get_device(), x.dtype
     if not isinstance(B, torch.Tensor) or B.dim() != 4:
         raise SsdArgumentError(2, "B and C must be [batch, seqlen, ngroups, dstate]")
     G, N = B.shape[2], B.shape[3]
-    prob = make_selscan_problem(bsz, L, ch, N, G, _io_code(x))
-    _same_device(x, dt, A, B, C, D, z, dt_bias)
-    if dt_bias is not None and tuple(dt_bias.shape) != (ch,):
-        raise SsdArgumentError(2, "dt_bias must be [channels]")
-    xf, xfp = _dt_transform(ch, dt_bias, dt_softplus, dt_limit)
-    args = (_plain(x, "x", x.dtype, x.shape), _plain(dt, "dt", x.dtype, x.shape),
-            _plain(A, "A", torch.float32, (ch, N)), *_rows(B, "B", x.dtype, (bsz, L, G, N)),
-            *_rows(C, "C", x.dtype, (bsz, L, G, N)), _plain(D, "D", torch.float32, (ch,)),
-            *_rows(z, "z", x.dtype, x.shape))
-    return prob, (xf, xfp), args, (bsz, ch, N)
+    key = shape + (N, G, _io_code(x))
+    ch = (shape[2],)
+    if dt_bias is not None:
+        _plain(dt_bias, "dt_bias", _F32, ch, dev)
+    xf = _dt_transform(shape[2], dt_bias, dt_softplus, dt_limit)
+    bc = (shape[0], shape[1], G, N)
+    ptrs = (_plain(x, "x", io, shape, dev), _plain(dt, "dt", io, shape, dev),
+            _plain(A, "A", _F32, (shape[2], N), dev)) + _rows(B, "B", io, bc, dev) + \
+        _rows(C, "C", io, bc, dev) + (_plain(D, "D", _F32, ch, dev),) + _rows(z, "z", io, shape, dev)
+    return dev, key, xf, ptrs, (shape[0], shape[2], N)
 
 
 def ssd_selscan_fwd_workspace_size(prob: ssd_selscan_problem) -> int:
@@ -312,21 +359,15 @@ def ssd_selscan_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch
     y is multiplied by z sigmoid(z); init_state [batch, channels, dstate] fp32.
     dt_bias [channels], dt_softplus, dt_limit: raw step size, as in ssd_fwd."""
     lib = load_library()
-    prob, (xf, xfp), args, state = _selscan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit)
-    y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dev, key, (xf, xfp), ptrs, state = _selscan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit)
+    y = out if out is not None else torch.empty_like(x)
     fin = None
     if want_final_state:
-        fin = final_out if final_out is not None else _f32(x, *state)
-    _same_device(x, init_state, y, fin, workspace)
-    if workspace is None:
-        need = _size(lib.ssd_selscan_fwd_workspace_size, prob)
-        ws, ws_bytes = _scratch(x, None, need) if need else (None, 0)
-    else:
-        ws, ws_bytes = _scratch(x, workspace, 0)
-    more = (_plain(init_state, "init_state", torch.float32, state), _plain(y, "out", x.dtype, x.shape),
-            _plain(fin, "final_out", torch.float32, state), ws, ws_bytes)
-    with _on(x.device):
-        _check(lib.ssd_selscan_fwd(ctypes.byref(prob), xfp, *args, *more, _stream(x.device)))
+        fin = final_out if final_out is not None else A.new_empty(state)
+    ws, ws_bytes, held = _scratch(x, workspace, _scan_bytes(False, *key) if workspace is None else 0, dev)
+    _launch(lib.ssd_selscan_fwd, dev, _scan_problem(*key), xfp, *ptrs,
+            _plain(init_state, "init_state", _F32, state, dev), _plain(y, "out", x.dtype, x.shape, dev),
+            _plain(fin, "final_out", _F32, state, dev), ws, ws_bytes)
     return y, fin
 
 
@@ -338,12 +379,10 @@ def ssd_selscan_step(state: torch.Tensor, x: torch.Tensor, dt: torch.Tensor, A: 
     """Advance ``state`` [batch, channels, dstate] (fp32, in place) through the seqlen
     tokens of x one at a time.  Arguments as for ssd_selscan_fwd; returns y."""
     lib = load_library()
-    prob, (xf, xfp), args, shape = _selscan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit)
-    y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _same_device(x, state, y)
-    sp, yp = _plain(state, "state", torch.float32, shape), _plain(y, "out", x.dtype, x.shape)
-    with _on(x.device):
-        _check(lib.ssd_selscan_step(ctypes.byref(prob), xfp, sp, *args, yp, _stream(x.device)))
+    dev, key, (xf, xfp), ptrs, shape = _selscan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit)
+    y = out if out is not None else torch.empty_like(x)
+    _launch(lib.ssd_selscan_step, dev, _scan_problem(*key), xfp, _plain(state, "state", _F32, shape, dev),
+            *ptrs, _plain(y, "out", x.dtype, x.shape, dev))
     return y
 
 
@@ -364,25 +403,21 @@ def ssd_selscan_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch
     dinit and ddt_bias (None otherwise).  dz_out (strided) may be a slice of the
     projection's gradient."""
     lib = load_library()
-    prob, (xf, xfp), args, state = _selscan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit)
-    like = dict(dtype=x.dtype, device=x.device)
-    got = {"dx": torch.empty(x.shape, **like), "ddt": torch.empty(x.shape, **like),
-           "dA": _f32(x, *A.shape), "dB": torch.empty(B.shape, **like),
-           "dC": torch.empty(B.shape, **like), "dD": _f32(x, x.shape[2]) if D is not None else None,
-           "dz": None, "dinit": _f32(x, *state) if want_dinit else None,
-           "ddt_bias": _f32(x, x.shape[2]) if want_ddt_bias else None}
+    dev, key, (xf, xfp), ptrs, state = _selscan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit)
+    bc = tuple(B.shape)
+    got = {"dx": torch.empty_like(x), "ddt": torch.empty_like(x), "dA": torch.empty_like(A),
+           "dB": x.new_empty(bc), "dC": x.new_empty(bc), "dD": torch.empty_like(D) if D is not None else None,
+           "dz": None, "dinit": A.new_empty(state) if want_dinit else None,
+           "ddt_bias": A.new_empty((state[1],)) if want_ddt_bias else None}
     if z is not None:
-        got["dz"] = dz_out if dz_out is not None else torch.empty(x.shape, **like)
-    _same_device(x, init_state, dy, dfinal, got["dz"], workspace)
-    ws, ws_bytes = _scratch(x, workspace, _size(lib.ssd_selscan_bwd_workspace_size, prob)
-                            if workspace is None else 0)
-    more = (_plain(init_state, "init_state", torch.float32, state), _plain(dy, "dy", x.dtype, x.shape),
-            _plain(dfinal, "dfinal", torch.float32, state),
-            *[_dev(got[k], k) for k in ("dx", "ddt", "dA", "dB", "dC", "dD")],
-            *_rows(got["dz"], "dz_out", x.dtype, x.shape), _dev(got["dinit"], "dinit"),
-            _dev(got["ddt_bias"], "ddt_bias"), ws, ws_bytes)
-    with _on(x.device):
-        _check(lib.ssd_selscan_bwd(ctypes.byref(prob), xfp, *args, *more, _stream(x.device)))
+        got["dz"] = dz_out if dz_out is not None else torch.empty_like(x)
+    ws, ws_bytes, held = _scratch(x, workspace, _scan_bytes(True, *key) if workspace is None else 0, dev)
+    ptr = lambda k: None if got[k] is None else got[k].data_ptr()
+    _launch(lib.ssd_selscan_bwd, dev, _scan_problem(*key), xfp, *ptrs,
+            _plain(init_state, "init_state", _F32, state, dev), _plain(dy, "dy", x.dtype, x.shape, dev),
+            _plain(dfinal, "dfinal", _F32, state, dev), ptr("dx"), ptr("ddt"), ptr("dA"), ptr("dB"), ptr("dC"),
+            ptr("dD"), *_rows(got["dz"], "dz_out", x.dtype, x.shape, dev), ptr("dinit"), ptr("ddt_bias"), ws,
+            ws_bytes)
     return got
 
 
@@ -394,12 +429,22 @@ def make_gated_norm_problem(batch, seqlen, channels, ngroups, eps, norm_before_g
                                   int(bool(norm_before_gate)), int(io_dtype), 0)
 
 
+@functools.lru_cache(maxsize=1024)
+def _norm_problem(*args):
+    return ctypes.byref(make_gated_norm_problem(*args))
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_bwd_bytes(*args):
+    return _size(load_library().ssd_gated_norm_bwd_workspace_size, make_gated_norm_problem(*args))
+
+
 def _gated_norm(x, z, weight, ngroups, eps, norm_before_gate):
-    bsz, L, ch = _three(x)
-    prob = make_gated_norm_problem(bsz, L, ch, ngroups, eps, norm_before_gate, _io_code(x))
-    _same_device(x, z, weight)
-    return prob, (_plain(x, "x", x.dtype, x.shape), *_rows(z, "z", x.dtype, x.shape),
-                  _plain(weight, "weight", torch.float32, (ch,)))
+    shape = _three(x)
+    dev = x.get_device()
+    key = shape + (ngroups, eps, norm_before_gate, _io_code(x))
+    return dev, shape, key, (_plain(x, "x", x.dtype, shape, dev),) + _rows(z, "z", x.dtype, shape, dev) + \
+        (_plain(weight, "weight", _F32, (shape[2],), dev),)
 
 
 def ssd_gated_norm_fwd(x: torch.Tensor, z: Optional[torch.Tensor], weight: torch.Tensor, *,
@@ -409,12 +454,9 @@ def ssd_gated_norm_fwd(x: torch.Tensor, z: Optional[torch.Tensor], weight: torch
     same shape or None, weight [channels] fp32.  The gate is applied to x, or with
     norm_before_gate to the normalised output.  Returns y."""
     lib = load_library()
-    prob, args = _gated_norm(x, z, weight, ngroups, eps, norm_before_gate)
-    y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _same_device(x, y)
-    yp = _plain(y, "out", x.dtype, x.shape)
-    with _on(x.device):
-        _check(lib.ssd_gated_norm_fwd(ctypes.byref(prob), *args, yp, _stream(x.device)))
+    dev, shape, key, ptrs = _gated_norm(x, z, weight, ngroups, eps, norm_before_gate)
+    y = out if out is not None else torch.empty_like(x)
+    _launch(lib.ssd_gated_norm_fwd, dev, _norm_problem(*key), *ptrs, _plain(y, "out", x.dtype, shape, dev))
     return y
 
 
@@ -429,17 +471,13 @@ def ssd_gated_norm_bwd(x: torch.Tensor, z: Optional[torch.Tensor], weight: torch
     """Gradients of ssd_gated_norm_fwd: a dict with dx, dz (None without z; dz_out,
     strided, may be a slice of the projection's gradient) and dweight."""
     lib = load_library()
-    prob, args = _gated_norm(x, z, weight, ngroups, eps, norm_before_gate)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dev, shape, key, ptrs = _gated_norm(x, z, weight, ngroups, eps, norm_before_gate)
+    dx = torch.empty_like(x)
     dz = None
     if z is not None:
-        dz = dz_out if dz_out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    dw = _f32(x, x.shape[2])
-    _same_device(x, dy, dz, workspace)
-    ws, ws_bytes = _scratch(x, workspace, _size(lib.ssd_gated_norm_bwd_workspace_size, prob)
-                            if workspace is None else 0)
-    more = (_plain(dy, "dy", x.dtype, x.shape), _dev(dx, "dx"), *_rows(dz, "dz_out", x.dtype, x.shape),
-            _dev(dw, "dweight"), ws, ws_bytes)
-    with _on(x.device):
-        _check(lib.ssd_gated_norm_bwd(ctypes.byref(prob), *args, *more, _stream(x.device)))
+        dz = dz_out if dz_out is not None else torch.empty_like(x)
+    dw = torch.empty_like(weight)
+    ws, ws_bytes, held = _scratch(x, workspace, _norm_bwd_bytes(*key) if workspace is None else 0, dev)
+    _launch(lib.ssd_gated_norm_bwd, dev, _norm_problem(*key), *ptrs, _plain(dy, "dy", x.dtype, shape, dev),
+            dx.data_ptr(), *_rows(dz, "dz_out", x.dtype, shape, dev), dw.data_ptr(), ws, ws_bytes)
     return {"dx": dx, "dz": dz, "dweight": dw}
