@@ -41,7 +41,21 @@ __device__ __forceinline__ PartRow<T> part_of(const ConvParts& q, int64_t b, int
 }
 
 constexpr int kConvThreads = 256;
-constexpr int kConvAhead = 4;   // rows loaded ahead of the one in use
+constexpr int kFwdAhead = 4, kBwdAhead = 2;   // rows loaded ahead of those in use
+
+// Workgroup -> (channels, tokens).  Workgroups go to the 8 XCDs in turn; each XCD
+// takes a run of tokens, channels fastest, so that rows are read whole and the
+// W - 1 rows that neighbouring tiles share come from one L2.  The grid is rounded up to
+// a multiple of 8: tiles past the last are empty.
+struct ConvTiles {
+  int64_t bx, by;   // workgroups along the channels and the tokens
+};
+__device__ __forceinline__ bool conv_tile(const ConvTiles& n, int64_t* ix, int64_t* iy) {
+  const int64_t t = (int64_t)(blockIdx.x % 8) * (gridDim.x / 8) + blockIdx.x / 8;
+  *ix = t % n.bx;
+  *iy = t / n.bx;
+  return t < n.bx * n.by;
+}
 
 // Threads of a workgroup: lc lanes along the channels (a power of two up to
 // 64), kConvThreads / lc runs of tokens.
@@ -49,11 +63,13 @@ template <typename T, int V, int W>
 __global__ void __launch_bounds__(kConvThreads)
 conv_fwd_kernel(const T* __restrict__ x, Strides xs, const float* __restrict__ w,
                 const float* __restrict__ bias, const T* init, ConvParts y, T* fin, int silu,
-                int64_t L, int64_t C, int64_t bx, int lc_log, int64_t run) {
+                int64_t L, int64_t C, ConvTiles tiles, int lc_log, int64_t run) {
+  constexpr int M = kFwdAhead;
+  int64_t ix, iy;
+  if (!conv_tile(tiles, &ix, &iy)) return;
   const int lane = threadIdx.x & ((1 << lc_log) - 1);
-  const int64_t c = ((int64_t)(blockIdx.x % bx) * (1 << lc_log) + lane) * V;
-  const int64_t t0 =
-      ((int64_t)(blockIdx.x / bx) * (blockDim.x >> lc_log) + (threadIdx.x >> lc_log)) * run;
+  const int64_t c = (ix * (1 << lc_log) + lane) * V;
+  const int64_t t0 = (iy * (blockDim.x >> lc_log) + (threadIdx.x >> lc_log)) * run;
   const int64_t b = blockIdx.y;
   if (c >= C || t0 >= L) return;
   const int64_t t1 = t0 + run < L ? t0 + run : L;
@@ -78,19 +94,19 @@ conv_fwd_kernel(const T* __restrict__ x, Strides xs, const float* __restrict__ w
       win[k] = zero_raw<T, V>();
   }
   const PartRow<T> o = part_of<T>(y, b, L, c);
-  Raw next[kConvAhead];
+  Raw next[M];
 #pragma unroll
-  for (int a = 0; a < kConvAhead; ++a)
+  for (int a = 0; a < M; ++a)
     next[a] = t0 + a < t1 ? load_raw<T, V>(xp + (t0 + a) * xs.token) : zero_raw<T, V>();
-  for (int64_t t = t0; t < t1; t += kConvAhead) {
-    Raw cur[kConvAhead];
+  for (int64_t t = t0; t < t1; t += M) {
+    Raw cur[M];
 #pragma unroll
-    for (int a = 0; a < kConvAhead; ++a) cur[a] = next[a];
+    for (int a = 0; a < M; ++a) cur[a] = next[a];
 #pragma unroll
-    for (int a = 0; a < kConvAhead; ++a)
-      if (t + kConvAhead + a < t1) next[a] = load_raw<T, V>(xp + (t + kConvAhead + a) * xs.token);
+    for (int a = 0; a < M; ++a)
+      if (t + M + a < t1) next[a] = load_raw<T, V>(xp + (t + M + a) * xs.token);
 #pragma unroll
-    for (int a = 0; a < kConvAhead; ++a) {
+    for (int a = 0; a < M; ++a) {
       if (t + a >= t1) break;
       float u[V], r[V];
 #pragma unroll
@@ -132,16 +148,17 @@ __global__ void __launch_bounds__(kConvThreads)
 conv_bwd_kernel(const T* __restrict__ x, Strides xs, const float* __restrict__ w,
                 const float* __restrict__ bias, const T* __restrict__ init, ConvParts dy,
                 const T* __restrict__ dfin, T* __restrict__ dx, Strides dxs, T* __restrict__ dinit,
-                float* __restrict__ part, int silu, int64_t L, int64_t C, int64_t bx, int lc_log,
-                int64_t run) {
+                float* __restrict__ part, int silu, int64_t L, int64_t C, ConvTiles tiles,
+                int lc_log, int64_t run) {
   const int lanes = 1 << lc_log;
   const int lane = threadIdx.x & (lanes - 1);
   const int row = threadIdx.x >> lc_log;
   const int rows = blockDim.x >> lc_log;
-  const int64_t c0 = (int64_t)(blockIdx.x % bx) * lanes * V;   // the workgroup's first channel
+  int64_t ix, iy;
+  if (!conv_tile(tiles, &ix, &iy)) return;
+  const int64_t c0 = ix * lanes * V;   // the workgroup's first channel
   const int64_t c = c0 + lane * V;
-  const int64_t tile = blockIdx.x / bx;
-  const int64_t t0 = (tile * rows + row) * run;
+  const int64_t t0 = (iy * rows + row) * run;
   const int64_t b = blockIdx.y;
   typedef typename RawV<T, V>::type Raw;
   float dw[W][V], db[V];
@@ -177,73 +194,93 @@ conv_bwd_kernel(const T* __restrict__ x, Strides xs, const float* __restrict__ w
       for (int v = 0; v < V; ++v) gw[k][v] = 0.0f;
     }
     const int64_t first = t0 == 0 ? -(int64_t)(W - 1) : t0;   // first row of dx (or dinit) formed here
-    Raw xn = load_raw<T, V>(xp + t0 * xs.token), gn = load_raw<T, V>(g.p + t0 * g.ld);
-    for (int64_t t = t0; t < t1 + W - 1; ++t) {
-      const Raw xr = xn, gr = gn;
-      if (t + 1 < L && t + 1 < t1 + W - 1) {
-        xn = load_raw<T, V>(xp + (t + 1) * xs.token);
-        gn = load_raw<T, V>(g.p + (t + 1) * g.ld);
-      }
-      float xc[V], du[V];
+    const int64_t end = t1 + W - 1;                            // rows of x and dy looked at
+    constexpr int M = kBwdAhead;
+    Raw xn[M], gn[M];
+    auto load = [&](int64_t t) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) xc[v] = du[v] = 0.0f;
-      if (t < L) {
-        float gc[V];
-        widen<T, V>(xr, xc);
-        widen<T, V>(gr, gc);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float u = fmaf(wt[W - 1][v], xc[v], bs[v]);
-#pragma unroll
-          for (int k = 0; k < W - 1; ++k) u = fmaf(wt[k][v], xw[k][v], u);
-          du[v] = silu ? gc[v] * silu_slope(u, sigmoid_f32(u)) : gc[v];
+      for (int a = 0; a < M; ++a)
+        if (t + a < L && t + a < end) {
+          xn[a] = load_raw<T, V>(xp + (t + a) * xs.token);
+          gn[a] = load_raw<T, V>(g.p + (t + a) * g.ld);
         }
-        if (t < t1) {
+    };
+#pragma unroll
+    for (int a = 0; a < M; ++a) xn[a] = gn[a] = zero_raw<T, V>();
+    load(t0);
+    for (int64_t tt = t0; tt < end; tt += M) {
+      Raw xr[M], gr[M];
+#pragma unroll
+      for (int a = 0; a < M; ++a) {
+        xr[a] = xn[a];
+        gr[a] = gn[a];
+      }
+      load(tt + M);
+#pragma unroll
+      for (int a = 0; a < M; ++a) {
+        const int64_t t = tt + a;
+        if (t >= end) break;
+        float xc[V], du[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) xc[v] = du[v] = 0.0f;
+        if (t < L) {
+          float gc[V];
+          widen<T, V>(xr[a], xc);
+          widen<T, V>(gr[a], gc);
 #pragma unroll
           for (int v = 0; v < V; ++v) {
-            db[v] += du[v];
-            dw[W - 1][v] = fmaf(du[v], xc[v], dw[W - 1][v]);
+            float u = fmaf(wt[W - 1][v], xc[v], bs[v]);
 #pragma unroll
-            for (int k = 0; k < W - 1; ++k) dw[k][v] = fmaf(du[v], xw[k][v], dw[k][v]);
+            for (int k = 0; k < W - 1; ++k) u = fmaf(wt[k][v], xw[k][v], u);
+            du[v] = silu ? gc[v] * silu_slope(u, sigmoid_f32(u)) : gc[v];
+          }
+          if (t < t1) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+              db[v] += du[v];
+              dw[W - 1][v] = fmaf(du[v], xc[v], dw[W - 1][v]);
+#pragma unroll
+              for (int k = 0; k < W - 1; ++k) dw[k][v] = fmaf(du[v], xw[k][v], dw[k][v]);
+            }
           }
         }
-      }
-      // row s = t - (W - 1) of dx takes du[s .. s + W - 1] = gw[0 .. W - 2], du
-      const int64_t s = t - (W - 1);
-      if (s >= first && s < t1) {
-        float o[V];
+        // row s = t - (W - 1) of dx takes du[s .. s + W - 1] = gw[0 .. W - 2], du
+        const int64_t s = t - (W - 1);
+        if (s >= first && s < t1) {
+          float o[V];
+#pragma unroll
+          for (int v = 0; v < V; ++v) {
+            o[v] = wt[0][v] * du[v];
+#pragma unroll
+            for (int k = 0; k < W - 1; ++k) o[v] = fmaf(wt[W - 1 - k][v], gw[k][v], o[v]);
+          }
+          const int64_t f = s - (L - (W - 1));   // this input's row in the final state
+          if (dfin && f >= 0) {
+            float d[V];
+            load_v<V>(dfin + (b * (W - 1) + f) * C + c, d);
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[v] += d[v];
+          }
+          if (s >= 0)
+            store_v<V>(dxp + s * dxs.token, o);
+          else if (dinit)
+            store_v<V>(dinit + (b * (W - 1) + s + (W - 1)) * C + c, o);
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          o[v] = wt[0][v] * du[v];
 #pragma unroll
-          for (int k = 0; k < W - 1; ++k) o[v] = fmaf(wt[W - 1 - k][v], gw[k][v], o[v]);
+          for (int k = 0; k + 1 < W - 1; ++k) {
+            xw[k][v] = xw[k + 1][v];
+            gw[k][v] = gw[k + 1][v];
+          }
+          xw[W - 2][v] = xc[v];
+          gw[W - 2][v] = du[v];
         }
-        const int64_t f = s - (L - (W - 1));   // this input's row in the final state
-        if (dfin && f >= 0) {
-          float d[V];
-          load_v<V>(dfin + (b * (W - 1) + f) * C + c, d);
-#pragma unroll
-          for (int v = 0; v < V; ++v) o[v] += d[v];
-        }
-        if (s >= 0)
-          store_v<V>(dxp + s * dxs.token, o);
-        else if (dinit)
-          store_v<V>(dinit + (b * (W - 1) + s + (W - 1)) * C + c, o);
-      }
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-#pragma unroll
-        for (int k = 0; k + 1 < W - 1; ++k) {
-          xw[k][v] = xw[k + 1][v];
-          gw[k][v] = gw[k + 1][v];
-        }
-        xw[W - 2][v] = xc[v];
-        gw[W - 2][v] = du[v];
       }
     }
   }
   __shared__ float sums[kConvThreads][V];
-  float* out = part + (b * (gridDim.x / bx) + tile) * (W + 1) * C;
+  float* out = part + (b * tiles.by + iy) * (W + 1) * C;
 #pragma unroll
   for (int k = 0; k <= W; ++k) {
 #pragma unroll
@@ -261,28 +298,18 @@ conv_bwd_kernel(const T* __restrict__ x, Strides xs, const float* __restrict__ w
   }
 }
 
-// dweight [C, W] and dbias [C] from `n` rows of part sums [W + 1][C]: a
-// workgroup takes 64 of the (W + 1) C columns, four waves every fourth row.
+// dweight [C, W] and dbias [C] from `n` rows of part sums [W + 1][C].
 __global__ void __launch_bounds__(256)
 conv_reduce_kernel(const float* __restrict__ part, int64_t n, int64_t C, int W,
                    float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ double sums[4][64];
-  const int64_t cols = (W + 1) * C;
-  const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x % 64;
-  double s = 0.0;
-  if (i < cols)
-    for (int64_t r = threadIdx.x / 64; r < n; r += 4) s += (double)part[r * cols + i];
-  sums[threadIdx.x / 64][threadIdx.x % 64] = s;
-  __syncthreads();
-  if (threadIdx.x < 64 && i < cols) {
-    const double v = (sums[0][threadIdx.x] + sums[1][threadIdx.x]) +
-                     (sums[2][threadIdx.x] + sums[3][threadIdx.x]);
-    const int64_t k = i / C, c = i % C;
-    if (k < W)
-      dw[c * W + k] = (float)v;
-    else if (db)
-      db[c] = (float)v;
-  }
+  const int64_t cols = (W + 1) * C, i = (int64_t)blockIdx.x * 32 + threadIdx.x % 32;
+  const float v = column_sum(i < cols ? part + i : nullptr, n, cols);
+  if (threadIdx.x >= 32 || i >= cols) return;
+  const int64_t k = i / C, c = i % C;
+  if (k < W)
+    dw[c * W + k] = v;
+  else if (db)
+    db[c] = v;
 }
 
 // ---- host ----
@@ -313,17 +340,16 @@ ConvGrid conv_grid(int64_t batch, int64_t L, int64_t C, int V, int longest, int6
   g.by = (runs + g.rows - 1) / g.rows;
   return g;
 }
-constexpr int kConvBwdRun = 64;
 ConvGrid conv_bwd_grid(int64_t batch, int64_t L, int64_t C, int V) {
-  return conv_grid(batch, L, C, V, kConvBwdRun, 4096);
+  return conv_grid(batch, L, C, V, 64, 2048);
 }
 
 }  // namespace
 
-size_t conv_bwd_workspace(int64_t batch, int64_t L, int64_t C, int W, int io_bf16) {
+size_t conv_bwd_workspace(int64_t batch, int64_t L, int64_t C, int W) {
   // either vector width may be taken, by the call's pointers and strides
   size_t most = 0;
-  for (int V : {1, io_bf16 ? 8 : 4}) {
+  for (int V : {1, 4}) {
     const ConvGrid g = conv_bwd_grid(batch, L, C, V);
     const size_t n = size_t(batch) * g.by * (W + 1) * C * sizeof(float);
     if (n > most) most = n;
@@ -334,24 +360,24 @@ size_t conv_bwd_workspace(int64_t batch, int64_t L, int64_t C, int W, int io_bf1
 // Every launch has fewer than 2^32 threads along x (V = 1 has the most).
 int conv_grid_ok(int64_t batch, int64_t L, int64_t C) {
   if (batch > 65535 || C > (1 << 24) || L > (int64_t(1) << 32)) return 0;
-  const ConvGrid g = conv_grid(batch, L, C, 1, 32, 4096);
-  return (__int128)g.bx * g.by * kConvThreads < (int64_t(1) << 32);
+  const ConvGrid g = conv_grid(batch, L, C, 1, 16, 4096);
+  return ((__int128)g.bx * g.by + 7) * kConvThreads < (int64_t(1) << 32);
 }
 
 template <typename T, int V>
 static hipError_t conv_fwd_v(const ConvArgs& a, hipStream_t stream) {
-  ConvGrid g = conv_grid(a.batch, a.L, a.C, V, 32, 4096);
+  ConvGrid g = conv_grid(a.batch, a.L, a.C, V, 16, 4096);
   if (a.one_run) {   // the state is updated in place: one thread per (b, c) reads and writes it
     g.run = a.L;
     g.by = 1;
     g.rows = g.lc_log < 6 ? 64 >> g.lc_log : 1;
   }
   const ConvParts y{{a.y[0], a.y[1], a.y[2]}, {a.end[0], a.end[1], a.end[2]}};
-  const dim3 grid((unsigned)(g.bx * g.by), (unsigned)a.batch);
+  const dim3 grid((unsigned)((g.bx * g.by + 7) / 8 * 8), (unsigned)a.batch);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(g.threads()), 0, stream, static_cast<const T*>(a.x),
                        Strides{a.xs[0], a.xs[1]}, a.w, a.bias, static_cast<const T*>(a.init), y,
-                       static_cast<T*>(a.fin), a.silu, a.L, a.C, g.bx, g.lc_log, g.run);
+                       static_cast<T*>(a.fin), a.silu, a.L, a.C, ConvTiles{g.bx, g.by}, g.lc_log, g.run);
   };
   if (a.W == 2) go(conv_fwd_kernel<T, V, 2>);
   else if (a.W == 3) go(conv_fwd_kernel<T, V, 3>);
@@ -361,7 +387,7 @@ static hipError_t conv_fwd_v(const ConvArgs& a, hipStream_t stream) {
 
 hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t stream) {
   if (a.bf16)
-    return a.vec ? conv_fwd_v<bf16, 8>(a, stream) : conv_fwd_v<bf16, 1>(a, stream);
+    return a.vec ? conv_fwd_v<bf16, 4>(a, stream) : conv_fwd_v<bf16, 1>(a, stream);
   return a.vec ? conv_fwd_v<float, 4>(a, stream) : conv_fwd_v<float, 1>(a, stream);
 }
 
@@ -369,14 +395,14 @@ template <typename T, int V>
 static hipError_t conv_bwd_v(const ConvArgs& a, hipStream_t stream) {
   const ConvGrid g = conv_bwd_grid(a.batch, a.L, a.C, V);
   const ConvParts dy{{a.y[0], a.y[1], a.y[2]}, {a.end[0], a.end[1], a.end[2]}};
-  const dim3 grid((unsigned)(g.bx * g.by), (unsigned)a.batch);
+  const dim3 grid((unsigned)((g.bx * g.by + 7) / 8 * 8), (unsigned)a.batch);
   float* part = static_cast<float*>(a.workspace);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(g.threads()), 0, stream, static_cast<const T*>(a.x),
                        Strides{a.xs[0], a.xs[1]}, a.w, a.bias, static_cast<const T*>(a.init), dy,
                        static_cast<const T*>(a.dfin), static_cast<T*>(a.dx),
                        Strides{a.dxs[0], a.dxs[1]}, static_cast<T*>(a.dinit), part, a.silu, a.L,
-                       a.C, g.bx, g.lc_log, g.run);
+                       a.C, ConvTiles{g.bx, g.by}, g.lc_log, g.run);
   };
   if (a.W == 2) go(conv_bwd_kernel<T, V, 2>);
   else if (a.W == 3) go(conv_bwd_kernel<T, V, 3>);
@@ -384,14 +410,14 @@ static hipError_t conv_bwd_v(const ConvArgs& a, hipStream_t stream) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t cols = (a.W + 1) * a.C;
-  hipLaunchKernelGGL(conv_reduce_kernel, dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, stream,
+  hipLaunchKernelGGL(conv_reduce_kernel, dim3((unsigned)((cols + 31) / 32)), dim3(256), 0, stream,
                      part, a.batch * g.by, a.C, (int)a.W, a.dw, a.db);
   return hipGetLastError();
 }
 
 hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t stream) {
   if (a.bf16)
-    return a.vec ? conv_bwd_v<bf16, 8>(a, stream) : conv_bwd_v<bf16, 1>(a, stream);
+    return a.vec ? conv_bwd_v<bf16, 4>(a, stream) : conv_bwd_v<bf16, 1>(a, stream);
   return a.vec ? conv_bwd_v<float, 4>(a, stream) : conv_bwd_v<float, 1>(a, stream);
 }
 

@@ -131,24 +131,35 @@ norm_bwd_kernel(const T* __restrict__ x, const T* __restrict__ z, Strides zs,
       wt[i][v] = live && c < S ? w[c0 + c + v] : 0.0f;
       dw[i][v] = 0.0f;
     }
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+  typedef typename RawV<T, V>::type Raw;
+  Raw xn[NV], gn[NV], zn[GATE ? NV : 1];   // the next row, loaded while this one is worked on
+  auto load = [&](int64_t row) {
     const T* xp = x + row * D + c0;
     const T* gp = dy + row * D + c0;
     const T* zp = GATE ? z + (row / L) * zs.batch + (row % L) * zs.token + c0 : nullptr;
-    T* dzp = GATE ? dz + (row / L) * dzs.batch + (row % L) * dzs.token + c0 : nullptr;
-    typedef typename RawV<T, V>::type Raw;
-    Raw xr[NV], gr[NV], zr[GATE ? NV : 1];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tg + lane) * V;
-      xr[i] = gr[i] = zero_raw<T, V>();
-      if constexpr (GATE) zr[i] = zero_raw<T, V>();
+      xn[i] = gn[i] = zero_raw<T, V>();
+      if constexpr (GATE) zn[i] = zero_raw<T, V>();
       if (live && c < S) {
-        xr[i] = load_raw<T, V>(xp + c);
-        gr[i] = load_raw<T, V>(gp + c);
-        if constexpr (GATE) zr[i] = load_raw<T, V>(zp + c);
+        xn[i] = load_raw<T, V>(xp + c);
+        gn[i] = load_raw<T, V>(gp + c);
+        if constexpr (GATE) zn[i] = load_raw<T, V>(zp + c);
       }
     }
+  };
+  if (blockIdx.x < rows) load(blockIdx.x);
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    T* dzp = GATE ? dz + (row / L) * dzs.batch + (row % L) * dzs.token + c0 : nullptr;
+    Raw xr[NV], gr[NV], zr[GATE ? NV : 1];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      xr[i] = xn[i];
+      gr[i] = gn[i];
+      if constexpr (GATE) zr[i] = zn[i];
+    }
+    if (row + gridDim.x < rows) load(row + gridDim.x);
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -215,18 +226,9 @@ norm_bwd_kernel(const T* __restrict__ x, const T* __restrict__ z, Strides zs,
 
 __global__ void __launch_bounds__(256)
 norm_reduce_kernel(const float* __restrict__ part, int64_t n, int64_t D, float* __restrict__ dw) {
-  __shared__ double sums[16][16];
-  const int64_t c = (int64_t)blockIdx.x * 16 + threadIdx.x % 16;
-  double s = 0.0;
-  if (c < D)
-    for (int64_t r = threadIdx.x / 16; r < n; r += 16) s += (double)part[r * D + c];
-  sums[threadIdx.x / 16][threadIdx.x % 16] = s;
-  __syncthreads();
-  if (threadIdx.x < 16 && c < D) {
-    double v = 0.0;
-    for (int q = 0; q < 16; ++q) v += sums[q][threadIdx.x];
-    dw[c] = (float)v;
-  }
+  const int64_t c = (int64_t)blockIdx.x * 32 + threadIdx.x % 32;
+  const float v = column_sum(c < D ? part + c : nullptr, n, D);
+  if (threadIdx.x < 32 && c < D) dw[c] = v;
 }
 
 // ---- host ----
@@ -241,22 +243,26 @@ struct NormGrid {
 
 // Pieces per thread before a group takes more threads: 16 elements in fp32
 // registers either way, a few single ones where nothing is aligned.
+constexpr int kNormStripes = 1024;   // workgroups of the backward pass
 constexpr int norm_wide(int V) { return V == 8 ? 2 : 4; }
 
 NormGrid norm_grid(int64_t rows, int64_t D, int64_t G, int V) {
   NormGrid g;
   const int64_t S = D / G, pieces = (S + V - 1) / V;
-  int tg = 1;
-  while (tg < kWave && tg < pieces) tg *= 2;
-  while (tg < 1024 && pieces > (int64_t)tg * norm_wide(V)) tg *= 2;
-  g.tg = tg;
-  g.threads = tg > kNormThreads ? tg : kNormThreads;
-  if (rows * G * tg <= 64 * 256) g.threads = tg > 64 ? tg : 64;
-  const int64_t need = (pieces + tg - 1) / tg;
-  g.nv = (int)need;
-  const int64_t per = g.threads / tg;
+  if (pieces <= kWave) {
+    g.tg = 1;
+    while (g.tg < pieces) g.tg *= 2;
+  } else {
+    const int64_t wide = V == 1 && pieces > 4096 ? 8 : norm_wide(V);
+    g.tg = (int)((pieces + kWave * wide - 1) / (kWave * wide)) * kWave;
+  }
+  g.nv = (int)((pieces + g.tg - 1) / g.tg);
+  // small groups share a workgroup of four waves, or of one where there are few
+  const int few = rows * G * g.tg <= 64 * 256 ? kWave : kNormThreads;
+  const int64_t per = g.tg < few ? few / g.tg : 1;
+  g.threads = (int)(g.tg * per);
   g.sets = (G + per - 1) / per;
-  g.stripes = 2048 / g.sets;
+  g.stripes = kNormStripes / g.sets;
   if (g.stripes < 1) g.stripes = 1;
   if (g.stripes > rows) g.stripes = rows;
   return g;
@@ -350,7 +356,7 @@ static hipError_t norm_bwd_v(const NormArgs& a, hipStream_t stream) {
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(norm_reduce_kernel, dim3((unsigned)((a.D + 15) / 16)), dim3(256), 0, stream,
+  hipLaunchKernelGGL(norm_reduce_kernel, dim3((unsigned)((a.D + 31) / 32)), dim3(256), 0, stream,
                      part, g.stripes, a.D, a.dw);
   return hipGetLastError();
 }

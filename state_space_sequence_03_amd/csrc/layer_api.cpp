@@ -325,8 +325,7 @@ ssd_status ssd_conv_bwd_workspace_size(const ssd_conv_problem* prob, size_t* byt
     ssd_status st = conv_shape(*prob);
     if (st == SSD_OK) st = conv_supported(*prob);
     if (st != SSD_OK) return st;
-    *bytes = ssd::conv_bwd_workspace(prob->batch, prob->seqlen, prob->channels, (int)prob->width,
-                                     prob->io_dtype == SSD_BF16);
+    *bytes = ssd::conv_bwd_workspace(prob->batch, prob->seqlen, prob->channels, (int)prob->width);
     return ok();
   });
 }
@@ -362,7 +361,7 @@ ssd_status ssd_conv_bwd(const ssd_conv_problem* prob, const void* x, const ssd_s
     if (st != SSD_OK) return st;
     ssd::ConvArgs a{};
     conv_args(p, xs, x, weight, bias, &a);
-    const size_t need = ssd::conv_bwd_workspace(p.batch, p.seqlen, p.channels, a.W, a.bf16);
+    const size_t need = ssd::conv_bwd_workspace(p.batch, p.seqlen, p.channels, a.W);
     if (workspace_bytes < need)
       return fail(SSD_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
     a.init = init_state;

@@ -11,16 +11,18 @@ struct Strides {
   int64_t batch, token;
 };
 
-// V consecutive io elements <-> fp32.  V is the elements of 16 bytes, and
-// p 16-byte aligned; or V is 1.
+// V consecutive io elements <-> fp32, p aligned to all of them.
+template <typename T, int V> struct RawV { typedef T type; };
+template <> struct RawV<bf16, 8> { typedef bf16x8 type; };
+template <> struct RawV<bf16, 4> { typedef bf16x4 type; };
+template <> struct RawV<float, 4> { typedef floatx4 type; };
 template <int V> __device__ __forceinline__ void load_v(const bf16* p, float* v) {
-  if constexpr (V == 8) {
-    const bf16x8 w = *reinterpret_cast<const bf16x8*>(p);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(w[e]);
+  const typename RawV<bf16, V>::type w = *reinterpret_cast<const typename RawV<bf16, V>::type*>(p);
+  if constexpr (V == 1) {
+    v[0] = static_cast<float>(w);
   } else {
-    static_assert(V == 1, "one element or 16 bytes");
-    v[0] = static_cast<float>(*p);
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = static_cast<float>(w[e]);
   }
 }
 template <int V> __device__ __forceinline__ void load_v(const float* p, float* v) {
@@ -34,14 +36,14 @@ template <int V> __device__ __forceinline__ void load_v(const float* p, float* v
   }
 }
 template <int V> __device__ __forceinline__ void store_v(bf16* p, const float* v) {
-  if constexpr (V == 8) {
-    bf16x8 w;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = static_cast<bf16>(v[e]);
-    *reinterpret_cast<bf16x8*>(p) = w;
+  typename RawV<bf16, V>::type w;
+  if constexpr (V == 1) {
+    w = static_cast<bf16>(v[0]);
   } else {
-    *p = static_cast<bf16>(v[0]);
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[e] = static_cast<bf16>(v[e]);
   }
+  *reinterpret_cast<typename RawV<bf16, V>::type*>(p) = w;
 }
 template <int V> __device__ __forceinline__ void store_v(float* p, const float* v) {
   if constexpr (V == 4) {
@@ -50,11 +52,8 @@ template <int V> __device__ __forceinline__ void store_v(float* p, const float* 
     *p = v[0];
   }
 }
-// The same 16 bytes (or one element) held unconverted, so that rows loaded
-// ahead cost the registers of their io type only.
-template <typename T, int V> struct RawV { typedef T type; };
-template <> struct RawV<bf16, 8> { typedef bf16x8 type; };
-template <> struct RawV<float, 4> { typedef floatx4 type; };
+// The same held unconverted, so that rows loaded ahead cost the registers of
+// their io type only.
 template <typename T, int V>
 __device__ __forceinline__ typename RawV<T, V>::type load_raw(const T* p) {
   return *reinterpret_cast<const typename RawV<T, V>::type*>(p);
@@ -88,6 +87,32 @@ __device__ __forceinline__ float sigmoid_f32(float v) {
 // d silu(v) / dv for silu(v) = v s, s = sigmoid(v)
 __device__ __forceinline__ float silu_slope(float v, float s) {
   return s * fmaf(v, 1.0f - s, 1.0f);
+}
+
+// Sums over the rows of a [n][ld] array of part sums, one column per 8 threads of
+// a 256-thread workgroup (32 columns of 128 bytes, every eighth row each, four
+// loads in flight), in 64 bits and in a fixed order.  The first 32 threads get the
+// sums; `p` points to the thread's column, or is null past the last one.
+__device__ __forceinline__ float column_sum(const float* p, int64_t n, int64_t ld) {
+  __shared__ double sums[8][32];
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  if (p) {
+    int64_t r = threadIdx.x / 32;
+    for (; r + 24 < n; r += 32) {
+      float v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = p[(r + 8 * u) * ld];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) s[u] += (double)v[u];
+    }
+    for (; r < n; r += 8) s[0] += (double)p[r * ld];
+  }
+  sums[threadIdx.x / 32][threadIdx.x % 32] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+  double v = 0.0;
+  if (threadIdx.x < 32)
+    for (int q = 0; q < 8; ++q) v += sums[q][threadIdx.x];
+  return (float)v;
 }
 
 }  // namespace ssd

@@ -30,7 +30,7 @@ struct ConvArgs {
 };
 hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t stream);
 hipError_t launch_conv_bwd(const ConvArgs& a, hipStream_t stream);
-size_t conv_bwd_workspace(int64_t batch, int64_t L, int64_t C, int W, int io_bf16);
+size_t conv_bwd_workspace(int64_t batch, int64_t L, int64_t C, int W);
 int conv_grid_ok(int64_t batch, int64_t L, int64_t C);
 
 struct NormArgs {

@@ -377,20 +377,11 @@ __global__ void __launch_bounds__(256)
 selscan_reduce_a_kernel(const float* __restrict__ dAp, const float* __restrict__ dDp,
                         const float* __restrict__ dbp, int64_t n, int64_t D, int64_t N, int NP,
                         float* __restrict__ dA, float* __restrict__ dD, float* __restrict__ db) {
-  __shared__ double sums[4][64];
   const int64_t per = D * NP, cols = per + 2 * D;
-  const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x % 64;
-  double s = 0.0;
-  if (i < cols) {
-    const float* p = i < per ? dAp + i : i < per + D ? dDp + (i - per) : dbp + (i - per - D);
-    const int64_t ld = i < per ? per : D;
-    for (int64_t r = threadIdx.x / 64; r < n; r += 4) s += (double)p[r * ld];
-  }
-  sums[threadIdx.x / 64][threadIdx.x % 64] = s;
-  __syncthreads();
-  if (threadIdx.x >= 64 || i >= cols) return;
-  const float v = (float)((sums[0][threadIdx.x] + sums[1][threadIdx.x]) +
-                          (sums[2][threadIdx.x] + sums[3][threadIdx.x]));
+  const int64_t i = (int64_t)blockIdx.x * 32 + threadIdx.x % 32;
+  const float* p = i >= cols ? nullptr : i < per ? dAp + i : i < per + D ? dDp + (i - per) : dbp + (i - per - D);
+  const float v = column_sum(p, n, i < per ? per : D);
+  if (threadIdx.x >= 32 || i >= cols) return;
   if (i < per) {
     if (i % NP < N) dA[i / NP * N + i % NP] = v;
   } else if (i < per + D) {
@@ -442,7 +433,7 @@ int selscan_grid_ok(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
   const int np = selscan_np(N);
   return batch <= 65535 && (__int128)s.tiles * G * s.K <= most &&
          (__int128)batch * L * G * 2 * np / 256 < most &&
-         (__int128)batch * D * np / 64 < most;
+         (__int128)batch * D * np / 16 < most;
 }
 
 // The forward kernels tile channels more widely than the backward one.
@@ -501,7 +492,7 @@ static hipError_t bwd_g(const ScanArgs& a, hipStream_t stream) {
                      np, a.N);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(selscan_reduce_a_kernel, dim3((unsigned)((a.D * (np + 2) + 63) / 64)), dim3(256), 0,
+  hipLaunchKernelGGL(selscan_reduce_a_kernel, dim3((unsigned)((a.D * (np + 2) + 31) / 32)), dim3(256), 0,
                      stream, io.dApart, io.dDpart, io.dbpart, a.batch * s.K, a.D, a.N, np, a.dA, a.dD,
                      a.dbias);
   return hipGetLastError();
