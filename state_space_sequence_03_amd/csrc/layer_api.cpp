@@ -198,7 +198,7 @@ ssd_status scan_supported(const ssd_selscan_problem& p) {
 }
 // The kernels reach eight rows of z and dz by 32-bit byte offsets.
 ssd_status scan_rows(const ssd_selscan_problem& p, const ssd::ScanArgs& a) {
-  const int64_t most = (int64_t(1) << 28) / (int64_t)element(p.io_dtype);
+  const int64_t most = ((int64_t(1) << 28) - 1) / (int64_t)element(p.io_dtype);
   if ((a.z && a.zs[1] > most) || (a.dz && a.dzs[1] > most))
     return fail(SSD_ERR_UNSUPPORTED, "tokens of z and dz must be less than 2^28 bytes apart");
   return SSD_OK;

@@ -31,7 +31,7 @@ enum { kStates = 0, kOut = 1, kBoth = 2 };
 // What a wave of the chunked kernels reads and writes.  kStates: end states of
 // chunks.  kOut: y (and the final state).  kBoth: end states, and the gradient that
 // chunk k's own outputs send to its start state (R = sum_t (prod_{s<=t} a_s)
-// ds_t C_t), for the backward pass.
+// ds_t C_t), for the backward pass, and the states every 8 tokens.
 template <typename T>
 struct ScanIo {
   const T *x, *dt;
@@ -48,6 +48,8 @@ struct ScanIo {
   float* H;       // [batch][K][D][NP]: start state of each chunk
   float* R;       // [batch][K][D][NP]: gradient at each chunk's end
   float* sumdt;   // [batch][K][D]
+  float* ckpt;    // [batch][ceil(L / 8)][D][NP]: kBoth, states every 8 tokens from a zero start
+  float* sumsub;  // [batch][ceil(L / 8)][D]: the chunk's step sizes before them
   T* y;
   float* fin;
   DtXform xf;
@@ -149,6 +151,12 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
   const T* const Bp = io.B + b * io.bs.batch + t0 * io.bs.token + g * N;
   const T* const Cp = MODE == kStates ? nullptr : io.C + b * io.cs.batch + t0 * io.cs.token + g * N;
 
+  unsigned oc[2];   // byte offsets of the lane's states in a row of checkpoints
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int lc = base + dl * 2 + j;
+    oc[j] = lc < Dg ? (unsigned)((g * Dg + lc) * NP + n0) * 4u : kOutside;
+  }
   // B and C of one tile, held in registers from their load to their place in LDS
   float rb[PER], rc[MODE == kStates ? 1 : PER];
   auto fetch = [&](int t) {
@@ -213,6 +221,17 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
           ds[u] = MODE == kBoth ? to_f32(gr[u]) : 0.0f;
         }
         if (ts + U < len) load(ts + U);
+        if constexpr (MODE == kBoth) {
+          if (ts > 0) {   // the state and the step sizes so far, before these 8 tokens
+            const int64_t at = (b * ((sh.L + kSub - 1) / kSub) + (t0 + ts) / kSub) * sh.D;
+            const Rows rs = rows_at(io.ckpt + at * NP, 1, 0, sh.D * NP);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int q = 0; q < 8; q += 4) row_store4(rs, oc[j] + 4 * q, h[j] + q);
+            row_store<float>(rows_at(io.sumsub + at, 1, 0, sh.D), own < Dg ? (unsigned)c * 4u : kOutside, sum);
+          }
+        }
         dt_values<U, false>(f, d, none);
         if (ts + U > len) {   // past the last token x and dy are zero; the decays have to be one
 #pragma unroll
@@ -512,30 +531,30 @@ hipError_t launch_selscan_fwd(const ScanArgs& a, hipStream_t stream) {
 // to its start, then both chains.
 template <typename T, int NP>
 static hipError_t both_np(const ScanArgs& a, const ScanShape& s, float* H, float* R, float* sumdt,
-                          hipStream_t stream) {
+                          float* ckpt, float* sumsub, hipStream_t stream) {
   ScanIo<T> io = scan_io<T>(a);
   io.H = H;
   io.R = R;
   io.sumdt = sumdt;
-  if (s.K > 1) {
-    launch_scan<T, NP, kBoth>(io, s, a.batch, s.K, stream);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
+  io.ckpt = ckpt;
+  io.sumsub = sumsub;
+  launch_scan<T, NP, kBoth>(io, s, a.batch, s.K, stream);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   if (s.K > 2) launch_selscan_pass(H, a.A, sumdt, nullptr, a.batch, s, 0, stream);
   launch_selscan_pass(R, a.A, sumdt, a.dfin, a.batch, s, 1, stream);
   return hipGetLastError();
 }
 hipError_t launch_selscan_both(const ScanArgs& a, const ScanShape& s, float* H, float* R,
-                               float* sumdt, hipStream_t stream) {
+                               float* sumdt, float* ckpt, float* sumsub, hipStream_t stream) {
   const int np = selscan_np(a.N);
   if (a.bf16)
-    return np == 16 ? both_np<bf16, 16>(a, s, H, R, sumdt, stream)
-           : np == 32 ? both_np<bf16, 32>(a, s, H, R, sumdt, stream)
-                      : both_np<bf16, 64>(a, s, H, R, sumdt, stream);
-  return np == 16 ? both_np<float, 16>(a, s, H, R, sumdt, stream)
-         : np == 32 ? both_np<float, 32>(a, s, H, R, sumdt, stream)
-                    : both_np<float, 64>(a, s, H, R, sumdt, stream);
+    return np == 16 ? both_np<bf16, 16>(a, s, H, R, sumdt, ckpt, sumsub, stream)
+           : np == 32 ? both_np<bf16, 32>(a, s, H, R, sumdt, ckpt, sumsub, stream)
+                      : both_np<bf16, 64>(a, s, H, R, sumdt, ckpt, sumsub, stream);
+  return np == 16 ? both_np<float, 16>(a, s, H, R, sumdt, ckpt, sumsub, stream)
+         : np == 32 ? both_np<float, 32>(a, s, H, R, sumdt, ckpt, sumsub, stream)
+                    : both_np<float, 64>(a, s, H, R, sumdt, ckpt, sumsub, stream);
 }
 
 template <typename T, int RN, bool GATE>

@@ -9,13 +9,15 @@
 //     dA = sum_t dt_t a_t g_t h_{t-1},          dD = sum_t ds_t x_t
 //     dz_t = dy_t s_t silu'(z_t)                dinit = a_0 g_0
 //
-// The states are needed from the last token to the first.  Chunks of T tokens:
-// selscan_kernel<both> and its chains (selscan.hip) give each chunk's start state
-// and the gradient at its end; selscan_bwd_kernel then walks one chunk forwards,
-// leaving the state every 8 tokens in LDS, and backwards 8 tokens at a time,
-// forming their states and decays again in registers.  Each decay is formed
-// three times in all; keeping the states of all tokens would move 4 N bytes per (t, c),
-// 64 at dstate 16 against the 14 that the gradients themselves move.
+// The states are needed from the last token to the first.  selscan_kernel<both> and
+// its chains (selscan.hip) give each chunk's start state, the gradient at its end
+// and, every 8 tokens, the state from a zero start of the chunk; the true state
+// there is that plus the decayed start state.  selscan_bwd_kernel walks a chunk
+// backwards 8 tokens at a time and forms their states and decays again in
+// registers: each decay is formed twice in all, and the checkpoints move 8 N / 8
+// bytes per (t, c) (16 at dstate 16, beside the 22 of the operands).  Walking each
+// chunk forwards once more in place of the checkpoints took 334 us against
+// YY us for 2 x 2048 x 5120 channels x 16 states.
 //
 // dB and dC are sums over channels: over the lane groups of a wave by lane
 // swaps, over a workgroup's waves in LDS, and over workgroups by
@@ -31,16 +33,18 @@ namespace ssd {
 
 constexpr int kBwdThreads = 256;
 constexpr int kBwdWaves = kBwdThreads / kWave;
-constexpr int kSub = 8;             // tokens whose states are held in registers
 constexpr int kPairs = kSub / 2;    // lanes prepare two tokens of two channels at a time
+// The decays of the last tokens of each 8 stay in registers, those of the first
+// kAgain are formed a second time: all of them would not fit beside the states.
+constexpr int kAgain = 2;
 
-// Tokens per chunk: the checkpoints of all of it share LDS with its B and C.
-__host__ __device__ constexpr int bwd_tokens(int RN) { return RN == 16 ? 32 : 64; }
-// Floats of one checkpoint of a wave (8 per lane), which the 8 tokens' 16 NP sums
-// of dB and dC replace once they are formed.
-__host__ __device__ constexpr int bwd_slot(int RN) { return 16 * 4 * RN > 512 ? 16 * 4 * RN : 512; }
-constexpr int bwd_smem_floats(int RN) {
-  return bwd_tokens(RN) * 4 * RN * 2 + kBwdWaves * (bwd_tokens(RN) / kSub) * bwd_slot(RN);
+// Tokens per chunk at most: B and C of all of it, and the waves' parts of dB and
+// dC, fit LDS for two workgroups per CU (dstate up to 32), so that the waves meet
+// at two barriers only.  One barrier per 8 tokens, with chunks three times as long,
+// took ZZ us against YY us for 2 x 2048 x 5120 channels x 16 states.
+__host__ __device__ constexpr int bwd_tokens(int NP) { return NP == 16 ? 64 : 32; }
+constexpr int bwd_smem_bytes(int NP) {
+  return (bwd_tokens(NP) * 2 * NP * (1 + kBwdWaves) + kBwdThreads * 8) * (int)sizeof(float);
 }
 
 template <typename T>
@@ -57,6 +61,7 @@ struct ScanBwdIo {
   const T* dy;
   const float* init;
   const float *H, *R;   // [batch][K][D][NP]
+  const float *ckpt, *sumsub;   // [batch][ceil(L / 8)][D][NP], [batch][ceil(L / 8)][D]
   float* dApart;        // [batch][K][D][NP]: H's slots, each read before it is written
   float *dDpart, *dbpart;   // [batch][K][D]
   float* bcpart;        // [batch][L][G][tiles][2][NP]
@@ -69,150 +74,123 @@ struct ScanBwdIo {
 template <typename T, int RN, bool GATE>
 __global__ void __launch_bounds__(kBwdThreads, 2)
 selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
-  constexpr int NP = 4 * RN, CW = 128 / RN, TB = bwd_tokens(RN), SUBS = TB / kSub;
-  constexpr int SLOT = bwd_slot(RN);
+  constexpr int NP = 4 * RN, CW = 128 / RN;
+  constexpr int ROW = kSub * 2 * NP;           // B and C, or dB and dC, of 8 tokens: [token][2][NP]
+  constexpr int SUBS = bwd_tokens(NP) / kSub;
   extern __shared__ float smem[];
-  float* const sB = smem;                 // [TB][NP]
-  float* const sC = smem + TB * NP;       // [TB][NP]
+  float* const bc = smem;                      // [SUBS][ROW], the chunk's B and C
+  float* const sums = bc + SUBS * ROW;         // [wave][SUBS][ROW], the waves' parts of dB and dC
+  float* const start = sums + kBwdWaves * SUBS * ROW + threadIdx.x * 4;   // [2][thread][4]: start states
   const int tid = threadIdx.x, lane = tid % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  float* const slots = smem + 2 * TB * NP + wave * SUBS * SLOT;   // [SUBS][SLOT], this wave's
   const int tiles = (int)sh.tiles, groups = (int)sh.G, Dg = (int)sh.Dg, N = (int)sh.N;
   const int tile = blockIdx.x % (tiles * groups);
-  const int64_t k = blockIdx.x / (tiles * groups);
+  const int k = blockIdx.x / (tiles * groups);
   const int64_t b = blockIdx.y;
   const int g = tile / tiles;
   const int base = ((tile % tiles) * kBwdWaves + wave) * CW;
-  const bool live = base < Dg;
+  const bool live = base < Dg;                       // whole waves past the group only stage and sum
   const int nl = lane % RN, dl = lane / RN, n0 = 4 * nl;
   const int par = (lane >> 1) & 1;                   // which token of a pair this lane prepares
   const int own = base + dl * 2 + (lane & 1);        // and which channel
   const int c = g * Dg + (own < Dg ? own : Dg - 1);
   const bool mine = own < Dg && nl < 4;
-  const int64_t t0 = k * TB;
-  const int len = (int)(t0 + TB < sh.L ? TB : sh.L - t0);   // tokens of this chunk
+  const int64_t t0 = k * sh.T;
+  const int len = (int)(t0 + sh.T < sh.L ? sh.T : sh.L - t0);   // tokens of this chunk
+  const int subs = (len + kSub - 1) / kSub;
 
+  float A2[2][4], gr[2][4], dA[2][4];
+  unsigned oc[2];                        // byte offsets of the lane's states in a row of checkpoints
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int lc = base + dl * 2 + j;
+    const int64_t cj = g * Dg + (lc < Dg ? lc : Dg - 1);
+    const int64_t at = ((b * sh.K + k) * sh.D + cj) * NP + n0;
+    oc[j] = (unsigned)(cj * NP + n0) * 4u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int n = n0 + i;
+      A2[j][i] = n < N ? io.A[cj * N + n] * kLog2e : 0.0f;
+      start[j * kBwdThreads * 4 + i] = k > 0 ? io.H[at + i]
+                              : io.init && n < N ? io.init[(b * sh.D + cj) * N + n] : 0.0f;
+      gr[j][i] = io.R[at + i];
+      dA[j][i] = 0.0f;
+    }
+  }
+  const DtLane f = dt_lane(io.xf, c);
+  const float Dc = io.Dv ? io.Dv[c] : 0.0f;
+  float dD = 0.0f, dbias = 0.0f;
+
+  // this chunk's rows, and byte offsets of the lane's channel and token in 8 of them;
+  // lanes that share both store the same values
+  const int64_t row = (b * sh.L + t0) * sh.D;
+  const T* const xp = io.x + row;
+  const T* const dp = io.dt + row;
+  const T* const gp = io.dy + row;
+  const T* const zp = GATE ? io.z + b * io.zs.batch + t0 * io.zs.token : nullptr;
+  T* const zo = GATE ? io.dz + b * io.dzs.batch + t0 * io.dzs.token : nullptr;
+  const int64_t sub0 = b * ((sh.L + kSub - 1) / kSub) + t0 / kSub;
+  const unsigned xrow = (unsigned)(sh.D * sizeof(T)), zrow = GATE ? (unsigned)(io.zs.token * sizeof(T)) : 0;
+  const unsigned zorow = GATE ? (unsigned)(io.dzs.token * sizeof(T)) : 0;
+  const unsigned cb = own < Dg ? (unsigned)c * (unsigned)sizeof(T) : kOutside;
+  const unsigned ox = cb + par * xrow, oz = cb + par * zrow, ozo = cb + par * zorow;
+  // what 8 tokens need, loaded while the 8 after them are worked on
+  T xr[kPairs], dr[kPairs], zr[kPairs], yr[kPairs];
+  float ck[2][4], cs[2];
+  auto load = [&](int s) {
+    const int more = (s * kSub + kSub <= len ? kSub : len - s * kSub) - 1;   // valid rows after the first
+    const int64_t t = (int64_t)s * kSub * sh.D;
+    const unsigned bytes = (more + 1) * xrow;
+    const Rows rx = rows_bytes(xp + t, bytes), rd = rows_bytes(dp + t, bytes), rg = rows_bytes(gp + t, bytes);
+    const unsigned o = fresh(ox);
+#pragma unroll
+    for (int p = 0; p < kPairs; ++p) {
+      xr[p] = row_load<T>(rx, o + 2 * p * xrow);
+      dr[p] = row_load<T>(rd, o + 2 * p * xrow);
+      yr[p] = row_load<T>(rg, o + 2 * p * xrow);
+    }
+    if constexpr (GATE) {
+      const Rows rz = rows_bytes(zp + s * kSub * io.zs.token, more * zrow + xrow);
+      const unsigned q = fresh(oz);
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) zr[p] = row_load<T>(rz, q + 2 * p * zrow);
+    }
+    if (s > 0) {
+      const Rows rc = rows_bytes(io.ckpt + (sub0 + s) * sh.D * NP, (unsigned)(sh.D * NP) * 4u);
+      const Rows rs = rows_bytes(io.sumsub + (sub0 + s) * sh.D, (unsigned)sh.D * 4u);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        row_load4(rc, oc[j], ck[j]);
+        cs[j] = row_load<float>(rs, fresh(oc[j]) / (4 * NP) * 4);
+      }
+    }
+  };
+  if (live) load(subs - 1);
   {
-    const T* Bp = io.B + b * io.bs.batch + t0 * io.bs.token + g * N;
-    const T* Cp = io.C + b * io.cs.batch + t0 * io.cs.token + g * N;
-    for (int i = tid; i < TB * NP; i += kBwdThreads) {
+    const T* const Bp = io.B + b * io.bs.batch + t0 * io.bs.token + g * N;
+    const T* const Cp = io.C + b * io.cs.batch + t0 * io.cs.token + g * N;
+    for (int i = tid; i < SUBS * ROW / 2; i += kBwdThreads) {
       const int tok = i / NP, n = i % NP;
       const bool in = tok < len && n < N;
-      sB[i] = in ? to_f32(Bp[tok * io.bs.token + n]) : 0.0f;
-      sC[i] = in ? to_f32(Cp[tok * io.cs.token + n]) : 0.0f;
+      bc[tok * 2 * NP + n] = in ? to_f32(Bp[tok * io.bs.token + n]) : 0.0f;
+      bc[(tok * 2 + 1) * NP + n] = in ? to_f32(Cp[tok * io.cs.token + n]) : 0.0f;
     }
   }
   __syncthreads();
-
   if (live) {
-    float A2[2][4], h[2][4], gr[2][4], dA[2][4];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int lc = base + dl * 2 + j;
-      const int64_t cj = g * Dg + (lc < Dg ? lc : Dg - 1);
-      const int64_t at = ((b * sh.K + k) * sh.D + cj) * NP + n0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int n = n0 + i;
-        A2[j][i] = n < N ? io.A[cj * N + n] * kLog2e : 0.0f;
-        h[j][i] = k > 0 ? io.H[at + i]
-                        : io.init && n < N ? io.init[(b * sh.D + cj) * N + n] : 0.0f;
-        gr[j][i] = io.R[at + i];
-        dA[j][i] = 0.0f;
-      }
-    }
-    const DtLane f = dt_lane(io.xf, c);
-    const float Dc = io.Dv ? io.Dv[c] : 0.0f;
-    float dD = 0.0f, dbias = 0.0f;
-    // this chunk's rows: the lane's channel, and its token of each pair
-    const int64_t row = (b * sh.L + t0) * sh.D;
-    const T* const xp = io.x + row;
-    const T* const dp = io.dt + row;
-    const T* const gp = io.dy + row;
-    const T* const zp = GATE ? io.z + b * io.zs.batch + t0 * io.zs.token : nullptr;
-    T* const zo = GATE ? io.dz + b * io.dzs.batch + t0 * io.dzs.token : nullptr;
-    const int subs = (len + kSub - 1) / kSub;
-    // byte offsets of the lane's channel and token in 8 rows; lanes that share both
-    // store the same values
-    unsigned ox[kPairs], oz[kPairs], ozo[kPairs];
-#pragma unroll
-    for (int p = 0; p < kPairs; ++p) {
-      const int u = 2 * p + par;
-      ox[p] = own < Dg ? (unsigned)(u * sh.D + c) * (unsigned)sizeof(T) : kOutside;
-      oz[p] = GATE && own < Dg ? (unsigned)(u * io.zs.token + c) * (unsigned)sizeof(T) : kOutside;
-      ozo[p] = GATE && own < Dg ? (unsigned)(u * io.dzs.token + c) * (unsigned)sizeof(T) : kOutside;
-    }
-
-    // forwards, one checkpoint per 8 tokens
-    T xr[kPairs], dr[kPairs], zr[kPairs], yr[kPairs];
-    auto load = [&](int s, bool all) {
-      const int64_t t = s * kSub;
-      const int valid = s * kSub + kSub <= len ? kSub : len - s * kSub;
-      const Rows rx = rows_at(xp + t * sh.D, valid, sh.D, sh.D);
-      const Rows rd = rows_at(dp + t * sh.D, valid, sh.D, sh.D);
-#pragma unroll
-      for (int p = 0; p < kPairs; ++p) {
-        xr[p] = row_load<T>(rx, ox[p]);
-        dr[p] = row_load<T>(rd, ox[p]);
-      }
-      if (all) {
-        const Rows rg = rows_at(gp + t * sh.D, valid, sh.D, sh.D);
-#pragma unroll
-        for (int p = 0; p < kPairs; ++p) yr[p] = row_load<T>(rg, ox[p]);
-        if constexpr (GATE) {
-          const Rows rz = rows_at(zp + t * io.zs.token, valid, io.zs.token, sh.D);
-#pragma unroll
-          for (int p = 0; p < kPairs; ++p) zr[p] = row_load<T>(rz, oz[p]);
-        }
-      }
-    };
-    load(0, false);
-    for (int s = 0; s < subs; ++s) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        *reinterpret_cast<floatx4*>(slots + s * SLOT + (j * kWave + lane) * 4) =
-            floatx4{h[j][0], h[j][1], h[j][2], h[j][3]};
-      if (s + 1 == subs) break;
-      float d[kPairs], dx[kPairs], none[1];
-#pragma unroll
-      for (int p = 0; p < kPairs; ++p) {   // only the last 8 tokens can lie past the end
-        d[p] = to_f32(dr[p]);
-        dx[p] = to_f32(xr[p]);
-      }
-      dt_values<kPairs, false>(f, d, none);
-#pragma unroll
-      for (int p = 0; p < kPairs; ++p) dx[p] *= d[p];
-      if (s + 2 < subs) load(s + 1, false);
-#pragma unroll
-      for (int p = 0; p < kPairs; ++p) {
-        auto token = [&](auto Q) {
-          constexpr int q = decltype(Q)::value;
-          const floatx4 Bv = *reinterpret_cast<const floatx4*>(sB + (s * kSub + 2 * p + q) * NP + n0);
-          const float d0 = quad_bcast<2 * q>(d[p]), d1 = quad_bcast<2 * q + 1>(d[p]);
-          const float x0 = quad_bcast<2 * q>(dx[p]), x1 = quad_bcast<2 * q + 1>(dx[p]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            h[0][i] = fmaf(fast_exp2(d0 * A2[0][i]), h[0][i], x0 * Bv[i]);
-            h[1][i] = fmaf(fast_exp2(d1 * A2[1][i]), h[1][i], x1 * Bv[i]);
-          }
-        };
-        token(std::integral_constant<int, 0>{});
-        token(std::integral_constant<int, 1>{});
-      }
-    }
-
-    // backwards, 8 tokens at a time
-    load(subs - 1, true);
     for (int s = subs - 1; s >= 0; --s) {
-      float* const slot = slots + s * SLOT;
-      float h0[2][4], hist[kSub][2][4], dec[kSub][2][4];
+      const float* const sBC = bc + s * ROW + n0;
+      float* const slot = sums + (wave * SUBS + s) * ROW;
+      float h0[2][4], hist[kSub][2][4], dec[kSub - kAgain + (kAgain == kSub)][2][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const floatx4 v = *reinterpret_cast<const floatx4*>(slot + (j * kWave + lane) * 4);
+      for (int j = 0; j < 2; ++j) load_v<4>(start + j * kBwdThreads * 4, h0[j]);
+      if (s > 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h0[j][i] = v[i];
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)   // (chunk 0's checkpoints start from the caller's state)
+            h0[j][i] = k > 0 ? fmaf(fast_exp2(A2[j][i] * cs[j]), h0[j][i], ck[j][i]) : ck[j][i];
       }
-      wave_sync();   // other lanes' sums will be written over this checkpoint
       float d[kPairs], dx[kPairs], ds[kPairs], xv[kPairs], slope[kPairs], yv[kPairs], zv[kPairs];
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) d[p] = to_f32(dr[p]);
@@ -226,20 +204,19 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
         dx[p] = d[p] * xv[p];
         ds[p] = GATE ? yv[p] * (zv[p] * sigmoid_f32(zv[p])) : yv[p];
       }
-      if (s > 0) load(s - 1, true);
-      const int valid = s * kSub + kSub <= len ? kSub : len - s * kSub;
-      const Rows wx = rows_at(io.dx + row + (int64_t)s * kSub * sh.D, valid, sh.D, sh.D);
-      const Rows wd = rows_at(io.ddt + row + (int64_t)s * kSub * sh.D, valid, sh.D, sh.D);
-      const Rows wz = rows_at(GATE ? zo + (int64_t)s * kSub * io.dzs.token : nullptr, valid,
-                              GATE ? io.dzs.token : 0, sh.D);
+      if (s > 0) load(s - 1);
+      const int more = (s * kSub + kSub <= len ? kSub : len - s * kSub) - 1;
+      const int64_t t8 = row + (int64_t)s * kSub * sh.D;
+      const Rows wx = rows_bytes(io.dx + t8, (more + 1) * xrow), wd = rows_bytes(io.ddt + t8, (more + 1) * xrow);
+      const Rows wz = rows_bytes(GATE ? zo + s * kSub * io.dzs.token : nullptr, more * zorow + xrow);
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) {
         float yp[4];
         auto token = [&](auto Q) {
           constexpr int q = decltype(Q)::value;
           const int t = 2 * p + q;
-          const floatx4 Bv = *reinterpret_cast<const floatx4*>(sB + (s * kSub + t) * NP + n0);
-          const floatx4 Cv = *reinterpret_cast<const floatx4*>(sC + (s * kSub + t) * NP + n0);
+          const floatx4 Bv = *reinterpret_cast<const floatx4*>(sBC + 2 * t * NP);
+          const floatx4 Cv = *reinterpret_cast<const floatx4*>(sBC + (2 * t + 1) * NP);
           const float dj[2] = {quad_bcast<2 * q>(d[p]), quad_bcast<2 * q + 1>(d[p])};
           const float xj[2] = {quad_bcast<2 * q>(dx[p]), quad_bcast<2 * q + 1>(dx[p])};
 #pragma unroll
@@ -247,8 +224,9 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
             float y = 0.0f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              dec[t][j][i] = fast_exp2(dj[j] * A2[j][i]);
-              hist[t][j][i] = fmaf(dec[t][j][i], t ? hist[t ? t - 1 : 0][j][i] : h0[j][i], xj[j] * Bv[i]);
+              const float a = fast_exp2(dj[j] * A2[j][i]);
+              if (t >= kAgain) dec[t >= kAgain ? t - kAgain : 0][j][i] = a;
+              hist[t][j][i] = fmaf(a, t ? hist[t ? t - 1 : 0][j][i] : h0[j][i], xj[j] * Bv[i]);
               if constexpr (GATE) y = fmaf(Cv[i], hist[t][j][i], y);
             }
             yp[2 * q + j] = y;
@@ -258,7 +236,7 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
         token(std::integral_constant<int, 1>{});
         if constexpr (GATE) {
           const float o = fmaf(Dc, xv[p], quads_sum<RN>(quad_fold(yp, lane)));
-          row_store<T>(wz, ozo[p], to_io<T>(yv[p] * o * silu_slope(zv[p], sigmoid_f32(zv[p]))));
+          row_store<T>(wz, fresh(ozo) + 2 * p * zorow, to_io<T>(yv[p] * o * silu_slope(zv[p], sigmoid_f32(zv[p]))));
         }
       }
 #pragma unroll
@@ -267,8 +245,8 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
         auto token = [&](auto Q) {
           constexpr int q = decltype(Q)::value;
           const int t = 2 * p + q;
-          const floatx4 Bv = *reinterpret_cast<const floatx4*>(sB + (s * kSub + t) * NP + n0);
-          const floatx4 Cv = *reinterpret_cast<const floatx4*>(sC + (s * kSub + t) * NP + n0);
+          const floatx4 Bv = *reinterpret_cast<const floatx4*>(sBC + 2 * t * NP);
+          const floatx4 Cv = *reinterpret_cast<const floatx4*>(sBC + (2 * t + 1) * NP);
           const float dj[2] = {quad_bcast<2 * q>(d[p]), quad_bcast<2 * q + 1>(d[p])};
           const float xj[2] = {quad_bcast<2 * q>(dx[p]), quad_bcast<2 * q + 1>(dx[p])};
           const float sj[2] = {quad_bcast<2 * q>(ds[p]), quad_bcast<2 * q + 1>(ds[p])};
@@ -277,13 +255,15 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             float qs = 0.0f, rs = 0.0f;
+            const float da = __builtin_bit_cast(float, fresh(__builtin_bit_cast(unsigned, dj[j])));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float gt = fmaf(sj[j], Cv[i], gr[j][i]);
               vC[4 * q + i] = fmaf(sj[j], hist[t][j][i], vC[4 * q + i]);
               vB[4 * q + i] = fmaf(xj[j], gt, vB[4 * q + i]);
               qs = fmaf(gt, Bv[i], qs);
-              const float ag = dec[t][j][i] * gt;
+              const float a = t >= kAgain ? dec[t >= kAgain ? t - kAgain : 0][j][i] : fast_exp2(da * A2[j][i]);
+              const float ag = a * gt;
               const float flow = ag * (t ? hist[t ? t - 1 : 0][j][i] : h0[j][i]);
               dA[j][i] = fmaf(dj[j], flow, dA[j][i]);
               rs = fmaf(A2[j][i], flow, rs);
@@ -300,8 +280,9 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
         const float ddt = fmaf(xv[p], qv, rv) * slope[p];   // (past the end x, ds and slope are zero)
         dbias += ddt;
         dD = fmaf(ds[p], xv[p], dD);
-        row_store<T>(wx, ox[p], to_io<T>(fmaf(d[p], qv, Dc * ds[p])));
-        row_store<T>(wd, ox[p], to_io<T>(ddt));
+        const unsigned o = fresh(ox) + 2 * p * xrow;
+        row_store<T>(wx, o, to_io<T>(fmaf(d[p], qv, Dc * ds[p])));
+        row_store<T>(wd, o, to_io<T>(ddt));
         // the wave's sums over channels: the lower half of the wave gets the pair's
         // first token, even rows states 0 and 1 of the four, odd rows 2 and 3
         auto channels = [&](const float (&v)[8], int which) {
@@ -325,36 +306,33 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
         channels(vC, 1);
       }
     }
-
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int lc = base + dl * 2 + j;
-      if (lc >= Dg) continue;
-      const int64_t cj = g * Dg + lc;
-      *reinterpret_cast<floatx4*>(io.dApart + ((b * sh.K + k) * sh.D + cj) * NP + n0) =
-          floatx4{dA[j][0], dA[j][1], dA[j][2], dA[j][3]};
-      if (k == 0 && io.dinit)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (n0 + i < N) io.dinit[(b * sh.D + cj) * N + n0 + i] = gr[j][i];
-    }
-    dD += dpp_move<0x4E>(dD);         // both tokens of the pairs
-    dbias += dpp_move<0x4E>(dbias);
-    if (mine && par == 0) {
-      io.dDpart[(b * sh.K + k) * sh.D + c] = dD;
-      io.dbpart[(b * sh.K + k) * sh.D + c] = dbias;
-    }
   }
   __syncthreads();
   // the workgroup's sums of dB and dC: live waves in order
   const int left = Dg - (tile % tiles) * kBwdWaves * CW;
   const int waves = left >= kBwdWaves * CW ? kBwdWaves : (left + CW - 1) / CW;
   for (int i = tid; i < len * 2 * NP; i += kBwdThreads) {
-    const int tok = i / (2 * NP), e = i % (2 * NP);
-    const float* q = smem + 2 * TB * NP + (tok / kSub) * SLOT + (tok % kSub) * 2 * NP + e;
     float v = 0.0f;
-    for (int w = 0; w < waves; ++w) v += q[w * SUBS * SLOT];
-    io.bcpart[(((b * sh.L + t0 + tok) * groups + g) * tiles + tile % tiles) * 2 * NP + e] = v;
+    for (int w = 0; w < waves; ++w) v += sums[w * SUBS * ROW + i];
+    io.bcpart[(((b * sh.L + t0 + i / (2 * NP)) * groups + g) * tiles + tile % tiles) * 2 * NP + i % (2 * NP)] = v;
+  }
+  if (!live) return;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int lc = base + dl * 2 + j;
+    if (lc >= Dg) continue;
+    const int64_t cj = g * Dg + lc;
+    store_v<4>(io.dApart + ((b * sh.K + k) * sh.D + cj) * NP + n0, dA[j]);
+    if (k == 0 && io.dinit)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n0 + i < N) io.dinit[(b * sh.D + cj) * N + n0 + i] = gr[j][i];
+  }
+  dD += dpp_move<0x4E>(dD);         // both tokens of the pairs
+  dbias += dpp_move<0x4E>(dbias);
+  if (mine && par == 0) {
+    io.dDpart[(b * sh.K + k) * sh.D + c] = dD;
+    io.dbpart[(b * sh.K + k) * sh.D + c] = dbias;
   }
 }
 
@@ -368,7 +346,16 @@ selscan_reduce_bc_kernel(const float* __restrict__ part, T* __restrict__ dB, T* 
   const int e = (int)(i % (2 * NP)), n = e % NP;
   if (r >= rows || n >= N) return;
   float v = 0.0f;
-  for (int64_t t = 0; t < tiles; ++t) v += part[(r * tiles + t) * 2 * NP + e];
+  const float* p = part + r * tiles * 2 * NP + e;
+  int64_t t = 0;
+  for (; t + 8 <= tiles; t += 8) {   // eight loads in flight
+    float q[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) q[u] = p[(t + u) * 2 * NP];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v += q[u];
+  }
+  for (; t < tiles; ++t) v += p[t * 2 * NP];
   (e < NP ? dB : dC)[r * N + n] = to_io<T>(v);
 }
 
@@ -393,45 +380,51 @@ selscan_reduce_a_kernel(const float* __restrict__ dAp, const float* __restrict__
 
 // ---- host ----
 
-static ScanShape bwd_shape(int64_t L, int64_t D, int64_t N, int64_t G) {
+// Chunks: as long as LDS allows, half that where their waves would not fill the chip.
+static ScanShape bwd_shape(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
   ScanShape s;
-  const int rn = selscan_np(N) / 4;
-  const int64_t per = 128 / rn * kBwdWaves;
+  const int np = selscan_np(N);
+  const int64_t cw = 512 / np, per = cw * kBwdWaves;
   s.L = L; s.D = D; s.N = N; s.G = G; s.Dg = D / G;
-  s.T = bwd_tokens(rn);
-  s.K = (L + s.T - 1) / s.T;
   s.tiles = (s.Dg + per - 1) / per;
+  const int64_t waves = batch * G * ((s.Dg + cw - 1) / cw);
+  s.T = bwd_tokens(np);
+  if (waves * ((L + s.T - 1) / s.T) < 2048) s.T /= 2;
+  s.K = (L + s.T - 1) / s.T;
   return s;
 }
 static size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 
 struct ScanBwdLayout {
-  size_t h, r, sum, dd, db, bc, bytes;
+  size_t h, r, sum, dd, db, ckpt, sumsub, bc, bytes;
 };
 static ScanBwdLayout bwd_layout(int64_t batch, const ScanShape& s) {
   ScanBwdLayout w;
   const size_t st = selscan_state_bytes(batch, s), sm = selscan_sum_bytes(batch, s);
+  const size_t subs = size_t(batch) * ((s.L + kSub - 1) / kSub) * s.D * sizeof(float);
   w.h = 0;
   w.r = st;
   w.sum = 2 * st;
   w.dd = w.sum + sm;
   w.db = w.dd + sm;
-  w.bc = w.db + sm;
+  w.ckpt = w.db + sm;
+  w.sumsub = w.ckpt + up256(subs * selscan_np(s.N));
+  w.bc = w.sumsub + up256(subs);
   w.bytes = w.bc + up256(size_t(batch) * s.L * s.G * s.tiles * 2 * selscan_np(s.N) * sizeof(float));
   return w;
 }
 
 size_t selscan_bwd_workspace(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
-  return bwd_layout(batch, bwd_shape(L, D, N, G)).bytes;
+  return bwd_layout(batch, bwd_shape(batch, L, D, N, G)).bytes;
 }
 
 // Whether every launch of the scan stays within a grid: workgroups along x
 // (channels x chunks, rows of the reductions), batches along y.
 int selscan_grid_ok(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
-  const ScanShape s = bwd_shape(L, D, N, G);
+  const ScanShape s = bwd_shape(batch, L, D, N, G);
   const __int128 most = (1 << 24) - 1;   // of 256 threads each: a launch has fewer than 2^32
   const int np = selscan_np(N);
-  return batch <= 65535 && (__int128)s.tiles * G * s.K <= most &&
+  return batch <= 65535 && D * np < (1 << 29) && (__int128)s.tiles * G * s.K <= most &&
          (__int128)batch * L * G * 2 * np / 256 < most &&
          (__int128)batch * D * np / 16 < most;
 }
@@ -445,12 +438,15 @@ static ScanShape fwd_tiles(ScanShape s) {
 
 template <typename T, int RN, bool GATE>
 static hipError_t bwd_g(const ScanArgs& a, hipStream_t stream) {
-  const ScanShape s = bwd_shape(a.L, a.D, a.N, a.G);
+  const ScanShape s = bwd_shape(a.batch, a.L, a.D, a.N, a.G);
   const ScanBwdLayout w = bwd_layout(a.batch, s);
   char* ws = static_cast<char*>(a.workspace);
   float* H = reinterpret_cast<float*>(ws + w.h);
   float* R = reinterpret_cast<float*>(ws + w.r);
-  hipError_t e = launch_selscan_both(a, fwd_tiles(s), H, R, reinterpret_cast<float*>(ws + w.sum), stream);
+  float* ckpt = reinterpret_cast<float*>(ws + w.ckpt);
+  float* sumsub = reinterpret_cast<float*>(ws + w.sumsub);
+  hipError_t e = launch_selscan_both(a, fwd_tiles(s), H, R, reinterpret_cast<float*>(ws + w.sum), ckpt,
+                                     sumsub, stream);
   if (e != hipSuccess) return e;
   ScanBwdIo<T> io{};
   io.x = static_cast<const T*>(a.x);
@@ -467,6 +463,8 @@ static hipError_t bwd_g(const ScanArgs& a, hipStream_t stream) {
   io.init = a.init;
   io.H = H;
   io.R = R;
+  io.ckpt = ckpt;
+  io.sumsub = sumsub;
   io.dApart = H;
   io.dDpart = reinterpret_cast<float*>(ws + w.dd);
   io.dbpart = reinterpret_cast<float*>(ws + w.db);
@@ -477,7 +475,7 @@ static hipError_t bwd_g(const ScanArgs& a, hipStream_t stream) {
   io.dzs = {a.dzs[0], a.dzs[1]};
   io.dinit = a.dinit;
   io.xf = a.xf ? *a.xf : DtXform{nullptr, 0, -INFINITY, INFINITY};
-  constexpr int smem = bwd_smem_floats(RN) * (int)sizeof(float);
+  constexpr int smem = bwd_smem_bytes(4 * RN);
   e = ensure_dyn_lds<selscan_bwd_kernel<T, RN, GATE>>(smem);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((selscan_bwd_kernel<T, RN, GATE>),

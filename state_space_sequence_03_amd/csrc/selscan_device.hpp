@@ -40,7 +40,14 @@ template <int J> __device__ __forceinline__ float pair_bcast(float v) {
 // past it give zero and stores past it are dropped, as at kOutside for lanes
 // without a channel.
 typedef __amdgpu_buffer_rsrc_t Rows;
-constexpr unsigned kOutside = 0xffffff00u;
+constexpr unsigned kOutside = 0x80000000u;   // eight rows end before it, and it plus them below 2^32
+__device__ __forceinline__ unsigned fresh(unsigned v) {
+  __asm__ volatile("" : "+v"(v));   // sums with it are formed where they are used, not kept across a loop
+  return v;
+}
+template <typename T> __device__ __forceinline__ Rows rows_bytes(const T* first, unsigned bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(first), (short)0, (int)bytes, 0x00020000);
+}
 template <typename T>
 __device__ __forceinline__ Rows rows_at(const T* first, int valid, int64_t stride, int64_t width) {
   const unsigned bytes = (unsigned)(valid - 1) * (unsigned)(stride * sizeof(T)) + (unsigned)(width * sizeof(T));
@@ -51,6 +58,16 @@ template <typename T> __device__ __forceinline__ T row_load(Rows r, unsigned byt
     return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b16(r, (int)bytes, 0, 0));
   else
     return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, (int)bytes, 0, 0));
+}
+__device__ __forceinline__ void row_load4(Rows r, unsigned bytes, float* v) {
+  const floatx4 w = __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)bytes, 0, 0));
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = w[e];
+}
+__device__ __forceinline__ void row_store4(Rows r, unsigned bytes, const float* v) {
+  typedef unsigned uintx4 __attribute__((ext_vector_type(4)));
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(uintx4, floatx4{v[0], v[1], v[2], v[3]}), r,
+                                         (int)bytes, 0, 0);
 }
 template <typename T> __device__ __forceinline__ void row_store(Rows r, unsigned bytes, T v) {
   if constexpr (sizeof(T) == 2)
@@ -145,6 +162,7 @@ __device__ __forceinline__ void dt_values(const DtLane& f, float (&v)[M], float 
 
 // Workspace rows of the chunked passes: [batch][chunks][channels][NP] fp32
 // states and [batch][chunks][channels] step-size sums.
+constexpr int kSub = 8;     // tokens whose states the backward pass holds in registers
 struct ScanShape {
   int64_t L, D, N, G, Dg;   // Dg = channels per group
   int64_t K, T;             // chunks and tokens per chunk
@@ -152,11 +170,11 @@ struct ScanShape {
 };
 
 // Padded states, and what the two source files of the scan share on
-// the host: chained start states and end gradients of every chunk, workspace sizes.
+// the host: chained start states and end gradients of every chunk, checkpoints, sizes.
 inline int selscan_np(int64_t N) { return N <= 16 ? 16 : N <= 32 ? 32 : 64; }
 struct ScanArgs;
 hipError_t launch_selscan_both(const ScanArgs& a, const ScanShape& s, float* H, float* R,
-                               float* sumdt, hipStream_t stream);
+                               float* sumdt, float* ckpt, float* sumsub, hipStream_t stream);
 size_t selscan_state_bytes(int64_t batch, const ScanShape& s);
 size_t selscan_sum_bytes(int64_t batch, const ScanShape& s);
 
