@@ -442,6 +442,9 @@ ssd_status ssd_selscan_step(const ssd_selscan_problem* prob, const ssd_dt_transf
     if (st != SSD_OK) return st;
     st = scan_supported(*prob);
     if (st != SSD_OK) return st;
+    const size_t four = 4 * element(prob->io_dtype);
+    a.vec = a.N % 4 == 0 && is_aligned(B, four) && is_aligned(C, four) && a.bs[0] % 4 == 0 &&
+            a.bs[1] % 4 == 0 && a.cs[0] % 4 == 0 && a.cs[1] % 4 == 0;
     return launched(ssd::launch_selscan_step(a, static_cast<hipStream_t>(stream)),
                     "selective scan step launch");
   });

@@ -57,6 +57,7 @@ int norm_grid_ok(int64_t batch, int64_t L, int64_t D, int64_t G);
 struct ScanArgs {
   int64_t batch, L, D, N, G;
   int bf16;
+  int vec;           // the step: B and C allow accesses of 4 elements, dstate is a multiple of 4
   const DtXform* xf;
   const void *x, *dt;
   const float* A;

@@ -351,75 +351,94 @@ selscan_pass_kernel(float* __restrict__ H, const float* __restrict__ A,
 }
 
 // Single tokens: the recurrence from a resident state, in place.  Bound by the
-// state's bytes (8 per element against ~8 slots of ALU work), so every lane holds
-// four consecutive states of one channel and takes all of the call's tokens.
-template <typename T, int RN, bool GATE, bool VEC>
-__global__ void __launch_bounds__(256)
+// state's bytes (8 per element).  A lane holds four consecutive states of one
+// channel for NB batches, whose loads are all in flight before the first is used
+// and which share the channel's A, D and bias, and takes all of the call's tokens.
+// VEC: dstate is a multiple of 4 and B and C allow accesses of 4 elements.
+constexpr int kStepThreads = 256;
+template <typename T, int RN, bool VEC, int NB>
+__global__ void __launch_bounds__(kStepThreads)
 selscan_step_kernel(float* __restrict__ state, const T* __restrict__ x, const T* __restrict__ dt,
                     const float* __restrict__ A, const T* __restrict__ B, Strides bs,
                     const T* __restrict__ C, Strides cs, const float* __restrict__ Dv,
-                    const T* __restrict__ z, Strides zs, T* __restrict__ y, DtXform xf, int64_t batch,
-                    int64_t L, int64_t D, int64_t N, int64_t Dg) {
-  const int nl = threadIdx.x % RN;
-  const int n0 = 4 * nl;
-  const int64_t item = (int64_t)blockIdx.x * (256 / RN) + threadIdx.x / RN;
-  const bool live = item < batch * D;
-  const int64_t b = live ? item / D : 0, c = live ? item % D : 0;
-  const int64_t g = c / Dg;
-  float* sp = state + (b * D + c) * N + n0;
-  const float* ap = A + c * N + n0;
-  float h[4], A2[4];
-  if constexpr (VEC) {
-    const bool in = n0 < N;
-    const floatx4 hv = in ? *reinterpret_cast<const floatx4*>(sp) : floatx4{0, 0, 0, 0};
-    const floatx4 av = in ? *reinterpret_cast<const floatx4*>(ap) : floatx4{0, 0, 0, 0};
+                    const T* __restrict__ z, Strides zs, T* __restrict__ y, DtXform xf, int batch,
+                    int64_t L, int D, int N, int Dg) {
+  const int nl = threadIdx.x % RN, n0 = 4 * nl;
+  const int own = blockIdx.x * (kStepThreads / RN) + threadIdx.x / RN;
+  const bool live = own < D;
+  const int c = live ? own : D - 1;
+  const int g = c / Dg;
+  const int b0 = blockIdx.y * NB;
+  const bool states = n0 < N;
+  auto load4 = [&](const float* p, float* v) {
+    if constexpr (VEC) {
+      v[0] = v[1] = v[2] = v[3] = 0.0f;
+      if (states) load_v<4>(p, v);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      h[i] = hv[i];
-      A2[i] = av[i] * kLog2e;
+      for (int i = 0; i < 4; ++i) v[i] = n0 + i < N ? p[i] : 0.0f;
     }
-  } else {
+  };
+  auto load_bc = [&](const T* p, float* v) {
+    if constexpr (VEC) {
+      v[0] = v[1] = v[2] = v[3] = 0.0f;
+      if (states) load_v<4>(p, v);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      h[i] = n0 + i < N ? sp[i] : 0.0f;
-      A2[i] = n0 + i < N ? ap[i] * kLog2e : 0.0f;
+      for (int i = 0; i < 4; ++i) v[i] = n0 + i < N ? to_f32(p[i]) : 0.0f;
     }
+  };
+  float h[NB][4], A2[4];
+#pragma unroll
+  for (int u = 0; u < NB; ++u) {
+    const int64_t b = b0 + u < batch ? b0 + u : batch - 1;
+    load4(state + (b * D + c) * N + n0, h[u]);
   }
+  load4(A + (int64_t)c * N + n0, A2);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) A2[i] *= kLog2e;
   const DtLane f = dt_lane(xf, c);
   const float Dc = Dv ? Dv[c] : 0.0f;
-  const T* Bp = B + b * bs.batch + g * N + n0;
-  const T* Cp = C + b * cs.batch + g * N + n0;
   for (int64_t t = 0; t < L; ++t) {
-    const int64_t at = (b * L + t) * D + c;
-    const float xv = to_f32(x[at]);
-    float dv[1] = {to_f32(dt[at])}, none[1];
-    dt_values<1, false>(f, dv, none);
-    const float d = dv[0], dx = d * xv;
-    float part = 0.0f;
+    float xv[NB], d[NB], zv[NB], Bv[NB][4], Cv[NB][4], none[1];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool in = n0 + i < N;
-      const float bv = in ? to_f32(Bp[t * bs.token + i]) : 0.0f;
-      const float cv = in ? to_f32(Cp[t * cs.token + i]) : 0.0f;
-      h[i] = fmaf(fast_exp2(d * A2[i]), h[i], dx * bv);
-      part = fmaf(cv, h[i], part);
+    for (int u = 0; u < NB; ++u) {
+      const int64_t b = b0 + u < batch ? b0 + u : batch - 1;
+      xv[u] = to_f32(x[(b * L + t) * D + c]);
+      d[u] = to_f32(dt[(b * L + t) * D + c]);
+      zv[u] = z ? to_f32(z[b * zs.batch + t * zs.token + c]) : 0.0f;
+      load_bc(B + b * bs.batch + t * bs.token + (int64_t)g * N + n0, Bv[u]);
+      load_bc(C + b * cs.batch + t * cs.token + (int64_t)g * N + n0, Cv[u]);
     }
+    dt_values<NB, false>(f, d, none);
 #pragma unroll
-    for (int off = RN / 2; off >= 1; off >>= 1) part += __shfl_xor(part, off, kWave);
-    float o = fmaf(Dc, xv, part);
-    if constexpr (GATE) {
-      const float zv = to_f32(z[b * zs.batch + t * zs.token + c]);
-      o *= zv * sigmoid_f32(zv);
+    for (int u = 0; u < NB; ++u) {
+      const float dx = d[u] * xv[u];
+      float part = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        h[u][i] = fmaf(fast_exp2(d[u] * A2[i]), h[u][i], dx * Bv[u][i]);
+        part = fmaf(Cv[u][i], h[u][i], part);
+      }
+      part += dpp_move<0xB1>(part);                          // the four lanes of a quad, then RN
+      part += dpp_move<0x4E>(part);
+      part = quads_sum<RN>(part);
+      float o = fmaf(Dc, xv[u], part);
+      if (z) o *= zv[u] * sigmoid_f32(zv[u]);
+      if (live && nl == 0 && b0 + u < batch) y[((int64_t)(b0 + u) * L + t) * D + c] = to_io<T>(o);
     }
-    if (live && nl == 0) y[at] = to_io<T>(o);
   }
-  if (!live) return;
-  if constexpr (VEC) {
-    if (n0 < N) *reinterpret_cast<floatx4*>(sp) = floatx4{h[0], h[1], h[2], h[3]};
-  } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (n0 + i < N) sp[i] = h[i];
+  for (int u = 0; u < NB; ++u) {
+    if (!live || b0 + u >= batch) continue;
+    float* p = state + ((int64_t)(b0 + u) * D + c) * N + n0;
+    if constexpr (VEC) {
+      if (states) store_v<4>(p, h[u]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n0 + i < N) p[i] = h[u][i];
+    }
   }
 }
 
@@ -557,29 +576,35 @@ hipError_t launch_selscan_both(const ScanArgs& a, const ScanShape& s, float* H, 
                     : both_np<float, 64>(a, s, H, R, sumdt, ckpt, sumsub, stream);
 }
 
-template <typename T, int RN, bool GATE>
-static hipError_t step_g(const ScanArgs& a, hipStream_t stream) {
-  const int64_t items = a.batch * a.D;
-  const dim3 grid((unsigned)((items + 256 / RN - 1) / (256 / RN)));
+template <typename T, int RN, int NB>
+static hipError_t step_nb(const ScanArgs& a, hipStream_t stream) {
+  constexpr int per = kStepThreads / RN;
+  const dim3 grid((unsigned)((a.D + per - 1) / per), (unsigned)((a.batch + NB - 1) / NB));
   const DtXform xf = a.xf ? *a.xf : DtXform{nullptr, 0, -INFINITY, INFINITY};
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, grid, dim3(256), 0, stream, a.state, static_cast<const T*>(a.x),
+    hipLaunchKernelGGL(kernel, grid, dim3(kStepThreads), 0, stream, a.state, static_cast<const T*>(a.x),
                        static_cast<const T*>(a.dt), a.A, static_cast<const T*>(a.B),
                        Strides{a.bs[0], a.bs[1]}, static_cast<const T*>(a.C),
                        Strides{a.cs[0], a.cs[1]}, a.Dv, static_cast<const T*>(a.z),
-                       Strides{a.zs[0], a.zs[1]}, static_cast<T*>(a.y), xf, a.batch, a.L, a.D, a.N,
-                       a.D / a.G);
+                       Strides{a.zs[0], a.zs[1]}, static_cast<T*>(a.y), xf, (int)a.batch, a.L, (int)a.D,
+                       (int)a.N, (int)(a.D / a.G));
   };
-  if (a.N % 4 == 0) go(selscan_step_kernel<T, RN, GATE, true>);
-  else go(selscan_step_kernel<T, RN, GATE, false>);
+  if (a.vec) go(selscan_step_kernel<T, RN, true, NB>);
+  else go(selscan_step_kernel<T, RN, false, NB>);
   return hipGetLastError();
+}
+template <typename T, int RN>
+static hipError_t step_rn(const ScanArgs& a, hipStream_t stream) {
+  // two batches per lane where that still leaves eight waves per SIMD (128 x 5120 x 16
+  // states: 20.5 us, one 22.2, four 25.1; smaller calls need the waves)
+  return a.batch * a.D * RN / 64 >= 2 * 8192 ? step_nb<T, RN, 2>(a, stream) : step_nb<T, RN, 1>(a, stream);
 }
 template <typename T>
 static hipError_t step_t(const ScanArgs& a, hipStream_t stream) {
   const int rn = selscan_np(a.N) / 4;
-  if (rn == 4) return a.z ? step_g<T, 4, true>(a, stream) : step_g<T, 4, false>(a, stream);
-  if (rn == 8) return a.z ? step_g<T, 8, true>(a, stream) : step_g<T, 8, false>(a, stream);
-  return a.z ? step_g<T, 16, true>(a, stream) : step_g<T, 16, false>(a, stream);
+  if (rn == 4) return step_rn<T, 4>(a, stream);
+  if (rn == 8) return step_rn<T, 8>(a, stream);
+  return step_rn<T, 16>(a, stream);
 }
 hipError_t launch_selscan_step(const ScanArgs& a, hipStream_t stream) {
   return a.bf16 ? step_t<bf16>(a, stream) : step_t<float>(a, stream);

@@ -200,10 +200,15 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
         xv[p] = to_f32(xr[p]);
         yv[p] = to_f32(yr[p]);   // x and dy are zero past the last token and the last channel
         zv[p] = GATE ? to_f32(zr[p]) : 0.0f;
-        if (s * kSub + 2 * p + par >= len) d[p] = slope[p] = 0.0f;
-        dx[p] = d[p] * xv[p];
         ds[p] = GATE ? yv[p] * (zv[p] * sigmoid_f32(zv[p])) : yv[p];
       }
+      if (s * kSub + kSub > len) {
+#pragma unroll
+        for (int p = 0; p < kPairs; ++p)
+          if (s * kSub + 2 * p + par >= len) d[p] = slope[p] = 0.0f;
+      }
+#pragma unroll
+      for (int p = 0; p < kPairs; ++p) dx[p] = d[p] * xv[p];
       if (s > 0) load(s - 1);
       const int more = (s * kSub + kSub <= len ? kSub : len - s * kSub) - 1;
       const int64_t t8 = row + (int64_t)s * kSub * sh.D;
@@ -221,15 +226,15 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
           const float xj[2] = {quad_bcast<2 * q>(dx[p]), quad_bcast<2 * q + 1>(dx[p])};
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float y = 0.0f;
+            float y;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float a = fast_exp2(dj[j] * A2[j][i]);
               if (t >= kAgain) dec[t >= kAgain ? t - kAgain : 0][j][i] = a;
               hist[t][j][i] = fmaf(a, t ? hist[t ? t - 1 : 0][j][i] : h0[j][i], xj[j] * Bv[i]);
-              if constexpr (GATE) y = fmaf(Cv[i], hist[t][j][i], y);
+              if constexpr (GATE) y = i ? fmaf(Cv[i], hist[t][j][i], y) : Cv[i] * hist[t][j][i];
             }
-            yp[2 * q + j] = y;
+            if constexpr (GATE) yp[2 * q + j] = y;
           }
         };
         token(std::integral_constant<int, 0>{});
@@ -251,22 +256,21 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
           const float xj[2] = {quad_bcast<2 * q>(dx[p]), quad_bcast<2 * q + 1>(dx[p])};
           const float sj[2] = {quad_bcast<2 * q>(ds[p]), quad_bcast<2 * q + 1>(ds[p])};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) vB[4 * q + i] = vC[4 * q + i] = 0.0f;
-#pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float qs = 0.0f, rs = 0.0f;
+            float qs, rs;
             const float da = __builtin_bit_cast(float, fresh(__builtin_bit_cast(unsigned, dj[j])));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float gt = fmaf(sj[j], Cv[i], gr[j][i]);
-              vC[4 * q + i] = fmaf(sj[j], hist[t][j][i], vC[4 * q + i]);
-              vB[4 * q + i] = fmaf(xj[j], gt, vB[4 * q + i]);
-              qs = fmaf(gt, Bv[i], qs);
+              // the first term of each sum is a product of its own
+              vC[4 * q + i] = j ? fmaf(sj[j], hist[t][j][i], vC[4 * q + i]) : sj[j] * hist[t][j][i];
+              vB[4 * q + i] = j ? fmaf(xj[j], gt, vB[4 * q + i]) : xj[j] * gt;
+              qs = i ? fmaf(gt, Bv[i], qs) : gt * Bv[i];
               const float a = t >= kAgain ? dec[t >= kAgain ? t - kAgain : 0][j][i] : fast_exp2(da * A2[j][i]);
               const float ag = a * gt;
               const float flow = ag * (t ? hist[t ? t - 1 : 0][j][i] : h0[j][i]);
               dA[j][i] = fmaf(dj[j], flow, dA[j][i]);
-              rs = fmaf(A2[j][i], flow, rs);
+              rs = i ? fmaf(A2[j][i], flow, rs) : A2[j][i] * flow;
               gr[j][i] = ag;
             }
             vq[2 * q + j] = qs;

@@ -162,7 +162,7 @@ def _launch(fn, dev: int, *args) -> None:
     """Call an entry point on the current stream of device `dev`, with that device
     current: launches go to streams of the current device."""
     stream = torch._C._cuda_getCurrentRawStream(dev)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
