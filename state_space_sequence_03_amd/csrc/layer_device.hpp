@@ -16,6 +16,8 @@ template <typename T, int V> struct RawV { typedef T type; };
 template <> struct RawV<bf16, 8> { typedef bf16x8 type; };
 template <> struct RawV<bf16, 4> { typedef bf16x4 type; };
 template <> struct RawV<float, 4> { typedef floatx4 type; };
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+template <> struct RawV<float, 2> { typedef floatx2 type; };
 template <int V> __device__ __forceinline__ void load_v(const bf16* p, float* v) {
   const typename RawV<bf16, V>::type w = *reinterpret_cast<const typename RawV<bf16, V>::type*>(p);
   if constexpr (V == 1) {
@@ -26,13 +28,12 @@ template <int V> __device__ __forceinline__ void load_v(const bf16* p, float* v)
   }
 }
 template <int V> __device__ __forceinline__ void load_v(const float* p, float* v) {
-  if constexpr (V == 4) {
-    const floatx4 w = *reinterpret_cast<const floatx4*>(p);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = w[e];
+  const typename RawV<float, V>::type w = *reinterpret_cast<const typename RawV<float, V>::type*>(p);
+  if constexpr (V == 1) {
+    v[0] = w;
   } else {
-    static_assert(V == 1, "one element or 16 bytes");
-    v[0] = *p;
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = w[e];
   }
 }
 template <int V> __device__ __forceinline__ void store_v(bf16* p, const float* v) {
@@ -46,11 +47,14 @@ template <int V> __device__ __forceinline__ void store_v(bf16* p, const float* v
   *reinterpret_cast<typename RawV<bf16, V>::type*>(p) = w;
 }
 template <int V> __device__ __forceinline__ void store_v(float* p, const float* v) {
-  if constexpr (V == 4) {
-    *reinterpret_cast<floatx4*>(p) = floatx4{v[0], v[1], v[2], v[3]};
+  typename RawV<float, V>::type w;
+  if constexpr (V == 1) {
+    w = v[0];
   } else {
-    *p = v[0];
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[e] = v[e];
   }
+  *reinterpret_cast<typename RawV<float, V>::type*>(p) = w;
 }
 // The same held unconverted, so that rows loaded ahead cost the registers of
 // their io type only.

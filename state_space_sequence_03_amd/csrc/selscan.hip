@@ -55,10 +55,11 @@ struct ScanIo {
   DtXform xf;
 };
 
-template <typename T, int NP, int MODE, bool GATE>
+template <typename T, int RN, int SN, int MODE, bool GATE>
 __global__ void __launch_bounds__(kScanThreads, 2)
 selscan_kernel(ScanIo<T> io, ScanShape sh) {
-  constexpr int RN = NP / 8, CW = 128 / RN;   // lanes per channel, channels per wave
+  constexpr int NP = RN * SN, CW = 128 / RN;   // padded states, channels per wave
+  constexpr int VS = SN % 4 == 0 ? 4 : 2;      // states per access
   constexpr int PER = kScanTile * NP / kScanThreads;
   constexpr int U = kScanAhead;
   __shared__ float sB[2][kScanTile][NP];
@@ -74,7 +75,7 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
   const int Dg = (int)sh.Dg, N = (int)sh.N;
   const bool live = base < Dg;             // whole waves past the group only stage
   const int nl = lane % RN, dl = lane / RN;
-  const int n0 = 8 * nl;
+  const int n0 = SN * nl;
   const int own = base + dl * 2 + (lane & 1);   // the channel this lane prepares
   const int c = g * Dg + (own < Dg ? own : Dg - 1);
   const bool mine = own < Dg && nl < 2;
@@ -89,13 +90,13 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
   const int64_t t0 = k * sh.T;
   const int len = (int)(t0 + sh.T < sh.L ? sh.T : sh.L - t0);   // tokens of this chunk
 
-  float A2[2][8], h[2][8], P[2][8], R[2][8];
+  float A2[2][SN], h[2][SN], P[2][SN], R[2][SN];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int lc = base + dl * 2 + j;
     const int64_t cj = g * Dg + (lc < Dg ? lc : Dg - 1);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < SN; ++i) {
       const int n = n0 + i;
       A2[j][i] = n < N ? io.A[cj * N + n] * kLog2e : 0.0f;
       h[j][i] = 0.0f;
@@ -112,7 +113,7 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
     if (k > 0) {
       constexpr int M = 4;   // chunks loaded at a time
       for (int m0 = 1; m0 <= k; m0 += M) {
-        float s[M][2], v[M][2][8];
+        float s[M][2], v[M][2][SN];
 #pragma unroll
         for (int u = 0; u < M; ++u) {
           const int m = m0 + u <= k ? m0 + u : k;
@@ -122,7 +123,7 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
             const int64_t at = (b * sh.K + m) * sh.D + g * Dg + (lc < Dg ? lc : Dg - 1);
             s[u][j] = io.sumdt[at - sh.D];
 #pragma unroll
-            for (int q = 0; q < 8; q += 4) load_v<4>(io.H + at * NP + n0 + q, v[u][j] + q);
+            for (int q = 0; q < SN; q += VS) load_v<VS>(io.H + at * NP + n0 + q, v[u][j] + q);
           }
         }
 #pragma unroll
@@ -131,7 +132,7 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
+              for (int i = 0; i < SN; ++i)
                 h[j][i] = m0 + u == 1 ? v[u][j][i]
                                       : fmaf(fast_exp2(A2[j][i] * s[u][j]), h[j][i], v[u][j][i]);
       }
@@ -228,7 +229,7 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-              for (int q = 0; q < 8; q += 4) row_store4(rs, oc[j] + 4 * q, h[j] + q);
+              for (int q = 0; q < SN; q += VS) row_store4(rs, oc[j] + 4 * q, h[j] + q);
             row_store<float>(rows_at(io.sumsub + at, 1, 0, sh.D), own < Dg ? (unsigned)c * 4u : kOutside, sum);
           }
         }
@@ -249,11 +250,11 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          float Bv[8], Cv[8], part[2];
+          float Bv[SN], Cv[SN], part[2];
 #pragma unroll
-          for (int q = 0; q < 8; q += 4) {
-            load_v<4>(&sB[buf][s + u][n0 + q], Bv + q);
-            if constexpr (MODE != kStates) load_v<4>(&sC[buf][s + u][n0 + q], Cv + q);
+          for (int q = 0; q < SN; q += VS) {
+            load_v<VS>(&sB[buf][s + u][n0 + q], Bv + q);
+            if constexpr (MODE != kStates) load_v<VS>(&sC[buf][s + u][n0 + q], Cv + q);
           }
           auto channel = [&](auto J) {
             constexpr int j = decltype(J)::value;
@@ -261,7 +262,7 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
             const float sj = MODE == kBoth ? pair_bcast<j>(ds[u]) : 0.0f;
             part[j] = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < SN; ++i) {
               const float a = fast_exp2(dj * A2[j][i]);
               h[j][i] = fmaf(a, h[j][i], xj * Bv[i]);
               if constexpr (MODE == kOut) part[j] = fmaf(Cv[i], h[j][i], part[j]);
@@ -293,18 +294,18 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
     if constexpr (MODE == kOut) {
       if (last && io.fin)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < SN; ++i)
           if (n0 + i < N) io.fin[(b * sh.D + cj) * N + n0 + i] = h[j][i];
     } else {
       if (!last)
 #pragma unroll
-        for (int q = 0; q < 8; q += 4)
-          store_v<4>(io.H + ((b * sh.K + k + 1) * sh.D + cj) * NP + n0 + q, h[j] + q);
+        for (int q = 0; q < SN; q += VS)
+          store_v<VS>(io.H + ((b * sh.K + k + 1) * sh.D + cj) * NP + n0 + q, h[j] + q);
       if constexpr (MODE == kBoth)
         if (k > 0)
 #pragma unroll
-          for (int q = 0; q < 8; q += 4)
-            store_v<4>(io.R + ((b * sh.K + k - 1) * sh.D + cj) * NP + n0 + q, R[j] + q);
+          for (int q = 0; q < SN; q += VS)
+            store_v<VS>(io.R + ((b * sh.K + k - 1) * sh.D + cj) * NP + n0 + q, R[j] + q);
     }
   }
   if constexpr (MODE != kOut)
@@ -448,7 +449,8 @@ selscan_step_kernel(float* __restrict__ state, const T* __restrict__ x, const T*
 // otherwise as many as give about three waves per SIMD, of at least 64 tokens.
 ScanShape selscan_fwd_shape(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
   ScanShape s;
-  const int64_t cw = 1024 / selscan_np(N), per = cw * (kScanThreads / kWave);
+  const int np = selscan_fwd_np(N);
+  const int64_t cw = np <= 16 ? 64 : np <= 32 ? 32 : 16, per = cw * (kScanThreads / kWave);
   s.L = L; s.D = D; s.N = N; s.G = G; s.Dg = D / G;
   s.tiles = (s.Dg + per - 1) / per;
   const int64_t waves = batch * G * ((s.Dg + cw - 1) / cw);
@@ -466,8 +468,8 @@ ScanShape selscan_fwd_shape(int64_t batch, int64_t L, int64_t D, int64_t N, int6
 }
 
 static size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
-size_t selscan_state_bytes(int64_t batch, const ScanShape& s) {
-  return up256(size_t(batch) * s.K * s.D * selscan_np(s.N) * sizeof(float));
+size_t selscan_state_bytes(int64_t batch, const ScanShape& s, int np) {
+  return up256(size_t(batch) * s.K * s.D * np * sizeof(float));
 }
 size_t selscan_sum_bytes(int64_t batch, const ScanShape& s) {
   return up256(size_t(batch) * s.K * s.D * sizeof(float));
@@ -475,7 +477,7 @@ size_t selscan_sum_bytes(int64_t batch, const ScanShape& s) {
 
 size_t selscan_fwd_workspace(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
   const ScanShape s = selscan_fwd_shape(batch, L, D, N, G);
-  return s.K == 1 ? 0 : selscan_state_bytes(batch, s) + selscan_sum_bytes(batch, s);
+  return s.K == 1 ? 0 : selscan_state_bytes(batch, s, selscan_fwd_np(N)) + selscan_sum_bytes(batch, s);
 }
 
 template <typename T>
@@ -499,17 +501,17 @@ static ScanIo<T> scan_io(const ScanArgs& a) {
   return io;
 }
 
-template <typename T, int NP, int MODE>
+template <typename T, int RN, int SN, int MODE>
 static void launch_scan(const ScanIo<T>& io, const ScanShape& s, int64_t batch, int64_t chunks,
                         hipStream_t stream) {
   const dim3 grid((unsigned)(s.tiles * s.G * chunks), (unsigned)batch);
   if constexpr (MODE != kStates) {
     if (io.z) {
-      hipLaunchKernelGGL((selscan_kernel<T, NP, MODE, true>), grid, dim3(kScanThreads), 0, stream, io, s);
+      hipLaunchKernelGGL((selscan_kernel<T, RN, SN, MODE, true>), grid, dim3(kScanThreads), 0, stream, io, s);
       return;
     }
   }
-  hipLaunchKernelGGL((selscan_kernel<T, NP, MODE, false>), grid, dim3(kScanThreads), 0, stream, io, s);
+  hipLaunchKernelGGL((selscan_kernel<T, RN, SN, MODE, false>), grid, dim3(kScanThreads), 0, stream, io, s);
 }
 
 void launch_selscan_pass(float* H, const float* A, const float* sumdt, const float* last,
@@ -519,27 +521,31 @@ void launch_selscan_pass(float* H, const float* A, const float* sumdt, const flo
                      stream, H, A, sumdt, last, batch, s.K, s.D, s.N, np, reverse);
 }
 
-template <typename T, int NP>
+template <typename T, int RN, int SN>
 static hipError_t fwd_np(const ScanArgs& a, hipStream_t stream) {
   const ScanShape s = selscan_fwd_shape(a.batch, a.L, a.D, a.N, a.G);
   ScanIo<T> io = scan_io<T>(a);
   if (s.K > 1) {
     io.H = static_cast<float*>(a.workspace);
-    io.sumdt = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + selscan_state_bytes(a.batch, s));
-    launch_scan<T, NP, kStates>(io, s, a.batch, s.K - 1, stream);
+    io.sumdt = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + selscan_state_bytes(a.batch, s, RN * SN));
+    launch_scan<T, RN, SN, kStates>(io, s, a.batch, s.K - 1, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  launch_scan<T, NP, kOut>(io, s, a.batch, s.K, stream);
+  launch_scan<T, RN, SN, kOut>(io, s, a.batch, s.K, stream);
   return hipGetLastError();
 }
 
 template <typename T>
 static hipError_t fwd_t(const ScanArgs& a, hipStream_t stream) {
-  const int np = selscan_np(a.N);
-  if (np == 16) return fwd_np<T, 16>(a, stream);
-  if (np == 32) return fwd_np<T, 32>(a, stream);
-  return fwd_np<T, 64>(a, stream);
+  switch (selscan_fwd_np(a.N)) {
+    case 8: return fwd_np<T, 2, 4>(a, stream);
+    case 16: return fwd_np<T, 2, 8>(a, stream);
+    case 24: return fwd_np<T, 4, 6>(a, stream);
+    case 32: return fwd_np<T, 4, 8>(a, stream);
+    case 48: return fwd_np<T, 8, 6>(a, stream);
+    default: return fwd_np<T, 8, 8>(a, stream);
+  }
 }
 
 hipError_t launch_selscan_fwd(const ScanArgs& a, hipStream_t stream) {
@@ -557,7 +563,7 @@ static hipError_t both_np(const ScanArgs& a, const ScanShape& s, float* H, float
   io.sumdt = sumdt;
   io.ckpt = ckpt;
   io.sumsub = sumsub;
-  launch_scan<T, NP, kBoth>(io, s, a.batch, s.K, stream);
+  launch_scan<T, NP / 8, 8, kBoth>(io, s, a.batch, s.K, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (s.K > 2) launch_selscan_pass(H, a.A, sumdt, nullptr, a.batch, s, 0, stream);

@@ -404,7 +404,7 @@ struct ScanBwdLayout {
 };
 static ScanBwdLayout bwd_layout(int64_t batch, const ScanShape& s) {
   ScanBwdLayout w;
-  const size_t st = selscan_state_bytes(batch, s), sm = selscan_sum_bytes(batch, s);
+  const size_t st = selscan_state_bytes(batch, s, selscan_np(s.N)), sm = selscan_sum_bytes(batch, s);
   const size_t subs = size_t(batch) * ((s.L + kSub - 1) / kSub) * s.D * sizeof(float);
   w.h = 0;
   w.r = st;

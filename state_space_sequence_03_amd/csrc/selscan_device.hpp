@@ -3,8 +3,8 @@
 //
 // A wave holds a tile of channels x states: RN neighbouring lanes share the
 // states, padded with zero B and C to NP of them, and the 64 / RN lane groups hold
-// consecutive channels, two per lane.  The forward kernels give a lane 8 states
-// (RN = NP / 8), which keeps the sum over states (y) short; the backward kernel
+// consecutive channels, two per lane.  The forward kernels give a lane up to 8 states
+// (RN = 2, 4 or 8), which keeps the sum over states (y) short; the backward kernel
 // 4 (RN = NP / 4), because it sums over channels (dB, dC) as well and holds the
 // states of 8 tokens.  What belongs to a channel alone (step size, gate) is prepared
 // once per channel, by one lane of its group, and read by the others as a DPP
@@ -172,10 +172,14 @@ struct ScanShape {
 // Padded states, and what the two source files of the scan share on
 // the host: chained start states and end gradients of every chunk, checkpoints, sizes.
 inline int selscan_np(int64_t N) { return N <= 16 ? 16 : N <= 32 ? 32 : 64; }
+// The forward pass alone pads less: 2, 4 or 8 lanes of 4, 6 or 8 states.
+inline int selscan_fwd_np(int64_t N) {
+  return N <= 8 ? 8 : N <= 16 ? 16 : N <= 24 ? 24 : N <= 32 ? 32 : N <= 48 ? 48 : 64;
+}
 struct ScanArgs;
 hipError_t launch_selscan_both(const ScanArgs& a, const ScanShape& s, float* H, float* R,
                                float* sumdt, float* ckpt, float* sumsub, hipStream_t stream);
-size_t selscan_state_bytes(int64_t batch, const ScanShape& s);
+size_t selscan_state_bytes(int64_t batch, const ScanShape& s, int np);
 size_t selscan_sum_bytes(int64_t batch, const ScanShape& s);
 
 }  // namespace ssd
