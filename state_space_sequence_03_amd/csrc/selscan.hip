@@ -445,8 +445,14 @@ selscan_step_kernel(float* __restrict__ state, const T* __restrict__ x, const T*
 
 // ---- host ----
 
-// Chunks of the forward pass.  One chunk where its waves fill the chip;
-// otherwise as many as give about three waves per SIMD, of at least 64 tokens.
+// Chunks of the forward pass.  One where its waves nearly fill the chip (1024 tokens
+// of 5120 channels: for 8 batches, 640 waves, chunks take 353 us and one chunk 398, for
+// 10 batches 451 and 402); otherwise as many as give about two waves per SIMD
+// (2048 tokens of 5120 channels x 16 states: 25 chunks 104 us, 12 chunks 128, 38
+// chunks 107, 50 chunks 123: more chunks cost more starts and longer chains), of at
+// least 16 tokens (300 tokens of 2560 channels: at least 16 28 us, 32 35, 64 54), and
+// 64 to 128 of them at most (64 channels: 8192 tokens in 128 chunks 80 us, in 64 95;
+// 2048 tokens 56 and 44).
 ScanShape selscan_fwd_shape(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
   ScanShape s;
   const int np = selscan_fwd_np(N);
@@ -456,10 +462,11 @@ ScanShape selscan_fwd_shape(int64_t batch, int64_t L, int64_t D, int64_t N, int6
   const int64_t waves = batch * G * ((s.Dg + cw - 1) / cw);
   s.K = 1;
   s.T = L;
-  if (waves < 640 && L > 128) {
+  if (waves < 720 && L > 64) {
     int64_t k = 2000 / waves;
-    if (k > L / 32) k = L / 32;
-    if (k > 64) k = 64;
+    if (k > L / 16) k = L / 16;
+    const int64_t most = L / 64 < 64 ? 64 : L / 64 < 128 ? L / 64 : 128;
+    if (k > most) k = most;
     if (k < 1) k = 1;
     s.T = ((L + k - 1) / k + 7) / 8 * 8;
     s.K = (L + s.T - 1) / s.T;
