@@ -312,19 +312,22 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
     if (mine) io.sumdt[(b * sh.K + k) * sh.D + c] = sum;
 }
 
-// Chains the chunks, one thread per (b, c, n).  Forwards, slot k of H holds chunk
-// k - 1's end state from a zero start (chunk 0's from the caller's state) and
-// becomes chunk k's start state; backwards, slot k of R holds what chunk k + 1
-// sends to its start and becomes the gradient at chunk k's end.
+// Chains the chunks for the backward pass, one thread per (b, c, n) and direction.
+// Forwards, slot k of H holds chunk k - 1's end state from a zero start (chunk
+// 0's from the caller's state) and becomes chunk k's start state; backwards, slot k
+// of R holds what chunk k + 1 sends to its start and becomes the gradient at chunk
+// k's end.
 __global__ void __launch_bounds__(256)
-selscan_pass_kernel(float* __restrict__ H, const float* __restrict__ A,
+selscan_pass_kernel(float* __restrict__ H, float* __restrict__ R, const float* __restrict__ A,
                     const float* __restrict__ sumdt, const float* __restrict__ last, int64_t batch,
-                    int64_t K, int64_t D, int64_t N, int NP, int reverse) {
+                    int64_t K, int64_t D, int64_t N, int NP) {
+  const bool reverse = blockIdx.y == 0;
+  if (!reverse && K < 3) return;
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (i >= batch * D * NP) return;
   const int64_t n = i % NP, c = i / NP % D, b = i / NP / D;
   const float a2 = n < N ? A[c * N + n] * kLog2e : 0.0f;
-  float* const p = H + (b * K * D + c) * NP + n;
+  float* const p = (reverse ? R : H) + (b * K * D + c) * NP + n;
   const float* const sp = sumdt + b * K * D + c;
   const int64_t step = D * NP;
   // slots `at` from `first` on, `dir` apart, the decay of slot k being chunk
@@ -521,13 +524,6 @@ static void launch_scan(const ScanIo<T>& io, const ScanShape& s, int64_t batch, 
   hipLaunchKernelGGL((selscan_kernel<T, RN, SN, MODE, false>), grid, dim3(kScanThreads), 0, stream, io, s);
 }
 
-void launch_selscan_pass(float* H, const float* A, const float* sumdt, const float* last,
-                         int64_t batch, const ScanShape& s, int reverse, hipStream_t stream) {
-  const int np = selscan_np(s.N);
-  hipLaunchKernelGGL(selscan_pass_kernel, dim3((unsigned)((batch * s.D * np + 255) / 256)), dim3(256), 0,
-                     stream, H, A, sumdt, last, batch, s.K, s.D, s.N, np, reverse);
-}
-
 template <typename T, int RN, int SN>
 static hipError_t fwd_np(const ScanArgs& a, hipStream_t stream) {
   const ScanShape s = selscan_fwd_shape(a.batch, a.L, a.D, a.N, a.G);
@@ -573,8 +569,8 @@ static hipError_t both_np(const ScanArgs& a, const ScanShape& s, float* H, float
   launch_scan<T, NP / 8, 8, kBoth>(io, s, a.batch, s.K, stream);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (s.K > 2) launch_selscan_pass(H, a.A, sumdt, nullptr, a.batch, s, 0, stream);
-  launch_selscan_pass(R, a.A, sumdt, a.dfin, a.batch, s, 1, stream);
+  hipLaunchKernelGGL(selscan_pass_kernel, dim3((unsigned)((a.batch * s.D * NP + 255) / 256), s.K > 2 ? 2 : 1),
+                     dim3(256), 0, stream, H, R, a.A, sumdt, a.dfin, a.batch, s.K, s.D, s.N, NP);
   return hipGetLastError();
 }
 hipError_t launch_selscan_both(const ScanArgs& a, const ScanShape& s, float* H, float* R,

@@ -21,9 +21,9 @@
 //
 // dB and dC are sums over channels: over the lane groups of a wave by lane
 // swaps, over a workgroup's waves in LDS, and over workgroups by
-// selscan_reduce_bc_kernel from the workspace, each in a fixed order.  dA, dD
-// and the bias gradient are sums over tokens: per chunk in registers, then over
-// chunks by selscan_reduce_a_kernel.
+// selscan_reduce_kernel from the workspace, each in a fixed order.  dA, dD and the
+// bias gradient are sums over tokens: per chunk in registers, then over chunks by
+// the same kernel.
 #include <type_traits>
 
 #include "layer_host.hpp"
@@ -340,36 +340,38 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
   }
 }
 
-// dB and dC [batch, L, G, N] from the workgroups' sums, `tiles` for each (b, t, g).
+// The last sums.  The first `bc_blocks` workgroups form dB and dC [rows, N] (rows =
+// batch x tokens x groups) from the scan's workgroups' sums, `tiles` for each row;
+// the others dA [D, N], dD [D] and the bias gradient [D] from `n` (batch x chunks)
+// rows of sums.
 template <typename T>
 __global__ void __launch_bounds__(256)
-selscan_reduce_bc_kernel(const float* __restrict__ part, T* __restrict__ dB, T* __restrict__ dC,
-                         int64_t rows, int64_t tiles, int NP, int64_t N) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t r = i / (2 * NP);
-  const int e = (int)(i % (2 * NP)), n = e % NP;
-  if (r >= rows || n >= N) return;
-  float v = 0.0f;
-  const float* p = part + r * tiles * 2 * NP + e;
-  int64_t t = 0;
-  for (; t + 8 <= tiles; t += 8) {   // eight loads in flight
-    float q[8];
+selscan_reduce_kernel(const float* __restrict__ part, T* __restrict__ dB, T* __restrict__ dC,
+                      int64_t rows, int64_t tiles, unsigned bc_blocks, const float* __restrict__ dAp,
+                      const float* __restrict__ dDp, const float* __restrict__ dbp, int64_t n, int64_t D,
+                      int64_t N, int NP, float* __restrict__ dA, float* __restrict__ dD,
+                      float* __restrict__ db) {
+  if (blockIdx.x < bc_blocks) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t r = i / (2 * NP);
+    const int e = (int)(i % (2 * NP)), m = e % NP;
+    if (r >= rows || m >= N) return;
+    float v = 0.0f;
+    const float* p = part + r * tiles * 2 * NP + e;
+    int64_t t = 0;
+    for (; t + 8 <= tiles; t += 8) {   // eight loads in flight
+      float q[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) q[u] = p[(t + u) * 2 * NP];
+      for (int u = 0; u < 8; ++u) q[u] = p[(t + u) * 2 * NP];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v += q[u];
+      for (int u = 0; u < 8; ++u) v += q[u];
+    }
+    for (; t < tiles; ++t) v += p[t * 2 * NP];
+    (e < NP ? dB : dC)[r * N + m] = to_io<T>(v);
+    return;
   }
-  for (; t < tiles; ++t) v += p[t * 2 * NP];
-  (e < NP ? dB : dC)[r * N + n] = to_io<T>(v);
-}
-
-// dA [D, N], dD [D] and the bias gradient [D] from `n` (batch x chunks) rows of sums.
-__global__ void __launch_bounds__(256)
-selscan_reduce_a_kernel(const float* __restrict__ dAp, const float* __restrict__ dDp,
-                        const float* __restrict__ dbp, int64_t n, int64_t D, int64_t N, int NP,
-                        float* __restrict__ dA, float* __restrict__ dD, float* __restrict__ db) {
   const int64_t per = D * NP, cols = per + 2 * D;
-  const int64_t i = (int64_t)blockIdx.x * 32 + threadIdx.x % 32;
+  const int64_t i = (int64_t)(blockIdx.x - bc_blocks) * 32 + threadIdx.x % 32;
   const float* p = i >= cols ? nullptr : i < per ? dAp + i : i < per + D ? dDp + (i - per) : dbp + (i - per - D);
   const float v = column_sum(p, n, i < per ? per : D);
   if (threadIdx.x >= 32 || i >= cols) return;
@@ -429,8 +431,8 @@ int selscan_grid_ok(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
   const __int128 most = (1 << 24) - 1;   // of 256 threads each: a launch has fewer than 2^32
   const int np = selscan_np(N);
   return batch <= 65535 && D * np < (1 << 29) && (__int128)s.tiles * G * s.K <= most &&
-         (__int128)batch * L * G * 2 * np / 256 < most &&
-         (__int128)batch * D * np / 16 < most;
+         (__int128)batch * L * G * 2 * np / 256 + (__int128)D * (np + 2) / 32 + 2 < most &&
+         (__int128)batch * D * np / 256 < most;
 }
 
 // The forward kernels tile channels more widely than the backward one.
@@ -489,14 +491,11 @@ static hipError_t bwd_g(const ScanArgs& a, hipStream_t stream) {
   if (e != hipSuccess) return e;
   const int64_t rows = a.batch * a.L * a.G;
   const int np = 4 * RN;
-  hipLaunchKernelGGL(selscan_reduce_bc_kernel<T>, dim3((unsigned)((rows * 2 * np + 255) / 256)), dim3(256),
-                     0, stream, io.bcpart, static_cast<T*>(a.dB), static_cast<T*>(a.dC), rows, s.tiles,
-                     np, a.N);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(selscan_reduce_a_kernel, dim3((unsigned)((a.D * (np + 2) + 31) / 32)), dim3(256), 0,
-                     stream, io.dApart, io.dDpart, io.dbpart, a.batch * s.K, a.D, a.N, np, a.dA, a.dD,
-                     a.dbias);
+  const unsigned bc_blocks = (unsigned)((rows * 2 * np + 255) / 256);
+  const unsigned a_blocks = (unsigned)((a.D * (np + 2) + 31) / 32);
+  hipLaunchKernelGGL(selscan_reduce_kernel<T>, dim3(bc_blocks + a_blocks), dim3(256), 0, stream, io.bcpart,
+                     static_cast<T*>(a.dB), static_cast<T*>(a.dC), rows, s.tiles, bc_blocks, io.dApart,
+                     io.dDpart, io.dbpart, a.batch * s.K, a.D, a.N, np, a.dA, a.dD, a.dbias);
   return hipGetLastError();
 }
 
