@@ -56,7 +56,7 @@ struct ScanIo {
 };
 
 template <typename T, int RN, int SN, int MODE, bool GATE>
-__global__ void __launch_bounds__(kScanThreads, 2)
+__global__ void __launch_bounds__(kScanThreads, 3)
 selscan_kernel(ScanIo<T> io, ScanShape sh) {
   constexpr int NP = RN * SN, CW = 128 / RN;   // padded states, channels per wave
   constexpr int VS = SN % 4 == 0 ? 4 : 2;      // states per access
