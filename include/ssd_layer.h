@@ -20,7 +20,8 @@
  * only are enqueued (so every call can be captured into a HIP graph), the
  * same call gives the same bits, and no exception crosses the interface.
  * `stream` belongs to the current device.  Outputs must not overlap inputs or
- * each other.  One workspace serves one call at a
+ * each other (a final_state that overlaps init_state, which ssd_fwd allows, is
+ * SSD_ERR_BAD_VALUE here: chunks of the sequence run side by side).  One workspace serves one call at a
  * time; its contents on entry do not matter.
  *
  * io dtype is SSD_BF16 or SSD_F32.  Sums, states and statistics are fp32;
@@ -32,8 +33,8 @@
  * ssd_strides means contiguous.  Strides of inputs may be any values >= 0 (0
  * repeats a row); strides of outputs must keep rows apart.  A strided pointer
  * needs the alignment of its element only; every other pointer is 16-byte
- * aligned.  Where pointers, strides and sizes allow 16-byte accesses they are
- * used.
+ * aligned.  Where pointers, strides and sizes allow accesses of several elements
+ * they are used.
  *
  * Errors, in this order: SSD_ERR_NULL_POINTER, SSD_ERR_BAD_SHAPE (a size <= 0, sizes
  * that do not divide or add up, or a product overflowing int64),

@@ -11,8 +11,7 @@
 //
 // Both directions are bound by HBM: 2 elements moved per output forwards, 3
 // backwards, against ~20 and ~40 VALU operations.  A thread owns V channels
-// (16 bytes of io elements where sizes and alignment allow, else one) of a run of
-// tokens and slides a window of W - 1 rows in registers, so each row is loaded
+// (four where sizes and alignment allow, else one) of a run of tokens and slides a window of W - 1 rows in registers, so each row is loaded
 // once per run plus W - 1 rows of overlap.
 #include "layer_device.hpp"
 #include "layer_host.hpp"

@@ -79,9 +79,14 @@ ssd_status check_strides(const char* name, const int64_t s[2], int64_t batch, in
   }
   return SSD_OK;
 }
-// 16-byte accesses to every row of a strided operand.
-bool row_vectors(const void* p, const int64_t s[2], int per) {
-  return is_aligned(p, 16) && s[0] % per == 0 && s[1] % per == 0;
+// Accesses of `per` elements of `size` bytes to every row of a strided operand.
+bool row_vectors(const void* p, const int64_t s[2], int per, size_t size) {
+  return is_aligned(p, per * size) && s[0] % per == 0 && s[1] % per == 0;
+}
+// Whether two buffers of `bytes` share memory (neither does where one is absent).
+bool overlap(const void* a, const void* b, int64_t bytes) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p && q && (p < q ? q - p : p - q) < (uintptr_t)bytes;
 }
 
 ssd_status check_io(int32_t io_dtype, int64_t reserved) {
@@ -139,11 +144,11 @@ void conv_args(const ssd_conv_problem& p, const int64_t xs[2], const void* x, co
     a->end[i] = end;
   }
 }
-// 16-byte accesses: x (and dx) by rows, every output or gradient by its own size.
+// Accesses of four channels: x (and dx) by rows, outputs or gradients by their sizes.
+constexpr int kConvVector = 4;
 bool conv_vectors(const ssd_conv_problem& p) {
-  const int per = p.io_dtype == SSD_BF16 ? 8 : 4;
   for (int64_t i = 0; i < p.nsplit; ++i)
-    if (p.split[i] % per != 0) return false;
+    if (p.split[i] % kConvVector != 0) return false;
   return true;
 }
 
@@ -159,6 +164,8 @@ ssd_status conv_run(const ssd_conv_problem* prob, const void* x, const ssd_strid
   strides_of(xst, p.seqlen, p.channels, xs);
   st = check_strides("x", xs, p.batch, p.seqlen, p.channels, false);
   if (st != SSD_OK) return st;
+  if (!in_place && overlap(init, fin, p.batch * (p.width - 1) * p.channels * (int64_t)element(p.io_dtype)))
+    return fail(SSD_ERR_BAD_VALUE, "final_state must not overlap init_state");
   if (!is_aligned(x, element(p.io_dtype)))
     return fail(SSD_ERR_MISALIGNED, "x must have the alignment of its element");
   bool fine = aligned16(weight, bias, init, fin);
@@ -172,7 +179,7 @@ ssd_status conv_run(const ssd_conv_problem* prob, const void* x, const ssd_strid
   a.fin = fin;
   a.one_run = in_place;
   for (int64_t i = 0; i < p.nsplit; ++i) a.y[i] = y[i];
-  a.vec = conv_vectors(p) && row_vectors(x, xs, a.bf16 ? 8 : 4);
+  a.vec = conv_vectors(p) && row_vectors(x, xs, kConvVector, element(p.io_dtype));
   return launched(ssd::launch_conv_fwd(a, static_cast<hipStream_t>(stream)), "convolution launch");
 }
 
@@ -374,8 +381,7 @@ ssd_status ssd_conv_bwd(const ssd_conv_problem* prob, const void* x, const ssd_s
     a.db = dbias;
     a.dinit = dinit;
     a.workspace = workspace;
-    const int per = a.bf16 ? 8 : 4;
-    a.vec = conv_vectors(p) && row_vectors(x, xs, per) && row_vectors(dx, dxs, per);
+    a.vec = conv_vectors(p) && row_vectors(x, xs, kConvVector, e) && row_vectors(dx, dxs, kConvVector, e);
     return launched(ssd::launch_conv_bwd(a, static_cast<hipStream_t>(stream)),
                     "convolution backward launch");
   });
@@ -407,6 +413,8 @@ ssd_status ssd_selscan_fwd(const ssd_selscan_problem* prob, const ssd_dt_transfo
     ssd::DtXform xf{};
     ssd_status st = scan_common(*prob, dtx, x, dt, A, B, b_strides, C, c_strides, D, z, z_strides, &xf, &a);
     if (st != SSD_OK) return st;
+    if (overlap(init_state, final_state, a.batch * a.D * a.N * (int64_t)sizeof(float)))
+      return fail(SSD_ERR_BAD_VALUE, "final_state must not overlap init_state");
     a.init = init_state;
     a.y = y;
     a.fin = final_state;
@@ -534,7 +542,7 @@ ssd_status ssd_gated_norm_fwd(const ssd_gated_norm_problem* prob, const void* x,
     if (st != SSD_OK) return st;
     a.y = y;
     const int per = a.bf16 ? 8 : 4;
-    a.vec = (a.D / a.G) % per == 0 && (!z || row_vectors(z, a.zs, per));
+    a.vec = (a.D / a.G) % per == 0 && (!z || row_vectors(z, a.zs, per, element(p.io_dtype)));
     return launched(ssd::launch_norm_fwd(a, static_cast<hipStream_t>(stream)), "gated norm launch");
   });
 }
@@ -587,7 +595,8 @@ ssd_status ssd_gated_norm_bwd(const ssd_gated_norm_problem* prob, const void* x,
     a.dw = dweight;
     a.workspace = workspace;
     const int per = a.bf16 ? 8 : 4;
-    a.vec = (a.D / a.G) % per == 0 && (!z || (row_vectors(z, a.zs, per) && row_vectors(dz, a.dzs, per)));
+    a.vec = (a.D / a.G) % per == 0 && (!z || (row_vectors(z, a.zs, per, element(p.io_dtype)) &&
+                                         row_vectors(dz, a.dzs, per, element(p.io_dtype))));
     return launched(ssd::launch_norm_bwd(a, static_cast<hipStream_t>(stream)), "gated norm backward launch");
   });
 }

@@ -12,7 +12,7 @@ namespace ssd {
 struct ConvArgs {
   int64_t batch, L, C;
   int W, bf16, silu;
-  int vec;        // every pointer, stride and split allows 16-byte accesses
+  int vec;        // every pointer, stride and split allows accesses of four channels
   int one_run;    // forward with fin == init: one thread takes all tokens of its channels
   const void* x;
   int64_t xs[2];
@@ -37,7 +37,8 @@ struct NormArgs {
   int64_t batch, L, D;
   int64_t G;
   float eps;
-  int before, bf16, vec;
+  int before, bf16;
+  int vec;        // every pointer, stride and group allows 16-byte accesses
   const void *x, *z;
   int64_t zs[2];
   const float* w;

@@ -207,10 +207,12 @@ def _conv(x, weight, bias, activation, split):
     dev = x.get_device()
     if activation not in _ACTIVATIONS:
         raise SsdArgumentError(10, "activation must be None or 'silu', got %r" % (activation,))
-    wshape = tuple(weight.shape)
+    wshape = tuple(weight.shape) if isinstance(weight, torch.Tensor) else ()
     if len(wshape) != 2 or wshape[0] != shape[2]:
         raise SsdArgumentError(2, "weight must be [channels, width]")
     sizes = (shape[2],) if split is None else tuple(split)
+    if sum(sizes) != shape[2] or min(sizes) < 1:
+        raise SsdArgumentError(2, "split must be positive and add up to channels, got %s" % (sizes,))
     key = shape + (wshape[1], sizes, _io_code(x), _ACTIVATIONS[activation])
     ptrs = _rows(x, "x", x.dtype, shape, dev) + (_plain(weight, "weight", _F32, wshape, dev),
                                                  _plain(bias, "bias", _F32, (shape[2],), dev))
@@ -326,6 +328,8 @@ def _selscan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit):
     dev, io = x.get_device(), x.dtype
     if not isinstance(B, torch.Tensor) or B.dim() != 4:
         raise SsdArgumentError(2, "B and C must be [batch, seqlen, ngroups, dstate]")
+    if A is None:
+        raise SsdArgumentError(1, "A must be a GPU tensor")
     G, N = B.shape[2], B.shape[3]
     key = shape + (N, G, _io_code(x))
     ch = (shape[2],)
@@ -442,6 +446,8 @@ def _norm_bwd_bytes(*args):
 def _gated_norm(x, z, weight, ngroups, eps, norm_before_gate):
     shape = _three(x)
     dev = x.get_device()
+    if weight is None:
+        raise SsdArgumentError(1, "weight must be a GPU tensor")
     key = shape + (ngroups, eps, norm_before_gate, _io_code(x))
     return dev, shape, key, (_plain(x, "x", x.dtype, shape, dev),) + _rows(z, "z", x.dtype, shape, dev) + \
         (_plain(weight, "weight", _F32, (shape[2],), dev),)

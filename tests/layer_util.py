@@ -30,13 +30,14 @@ def half_step(dtype):
     return torch.finfo(dtype).eps / 2
 
 
-def within(got, ref, count, mag, what):
-    """|got - ref| <= half a step of got's type |ref| (1 + count e) + count e mag."""
+def within(got, ref, count, mag, what, floor=1e-37):
+    """|got - ref| <= half a step of got's type |ref| + count e mag + floor, where floor
+    covers what falls below fp32's smallest normal value, 2^-126."""
     assert got is not None, what
     ref = np.asarray(ref)
     dtype, got = got.dtype, got.detach().double().cpu().numpy()
     assert got.shape == ref.shape, (what, got.shape, ref.shape)
-    bound = half_step(dtype) * np.abs(ref) + 1.01 * count * E * np.asarray(mag) + 1e-37
+    bound = half_step(dtype) * np.abs(ref) + 1.01 * count * E * np.asarray(mag) + floor
     off = np.abs(got - ref)
     bad = ~(off <= bound)
     assert not bad.any(), "%s: %d of %d outside the bound, at %s: %r for %r (bound %.2g)" % (

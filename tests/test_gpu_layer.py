@@ -499,3 +499,86 @@ def test_offsets_past_32_bits():
     g = lib.ssd_conv_bwd(near, w, None, None, dy)["dx"]
     lib.ssd_conv_bwd(near, w, None, None, dy, dx_out=x)
     assert torch.equal(x, g)
+
+
+# ---- refusals of the binding that need GPU tensors ----
+
+def test_binding_refuses():
+    d = Draw(51)
+    x, w = d.normal(2, 5, 16), d.normal(16, 4)
+    A, B, z = -d.uniform(1, 2, 16, 8), d.normal(2, 5, 1, 8), d.normal(2, 5, 32)
+    h = d.normal(2, 16, 8)
+    bad = [
+        lambda: lib.ssd_conv_fwd(x, w[:8]), lambda: lib.ssd_conv_fwd(x, None), lambda: lib.ssd_conv_fwd(x[0], w),
+        lambda: lib.ssd_conv_fwd(x.half(), w), lambda: lib.ssd_conv_fwd(x, w, w[0]), lambda: lib.ssd_conv_fwd(x, w.cpu()),
+        lambda: lib.ssd_conv_fwd(x, w, activation="relu"), lambda: lib.ssd_conv_fwd(x, w, split=(8, 4)),
+        lambda: lib.ssd_conv_fwd(x, w, split=(4, 4, 4, 4)), lambda: lib.ssd_conv_fwd(x, w, split=(24, -8)),
+        lambda: lib.ssd_conv_fwd(x.transpose(1, 2), w[:5]), lambda: lib.ssd_conv_fwd(x, d.normal(16, 5)),
+        lambda: lib.ssd_conv_fwd(x, w, out=x[:, :4]), lambda: lib.ssd_conv_fwd(x[:, :0], w),
+        lambda: lib.ssd_conv_step(x, x, w), lambda: lib.ssd_conv_bwd(x, w, None, None, z),
+        lambda: lib.ssd_conv_bwd(x, w, None, None, x, dx_out=x[:, :1].expand(2, 5, 16)),
+        lambda: lib.ssd_selscan_fwd(x, x.double(), A, B, B), lambda: lib.ssd_selscan_fwd(x, x, A.bfloat16(), B, B),
+        lambda: lib.ssd_selscan_fwd(x, x, A, B, B[:, :, :, :4]), lambda: lib.ssd_selscan_fwd(x, x, None, B, B),
+        lambda: lib.ssd_selscan_fwd(x, z[..., ::2], A, B, B), lambda: lib.ssd_selscan_fwd(x, x, A, B, B, z=z),
+        lambda: lib.ssd_selscan_fwd(x, x, A, B, B, z=z[..., ::2]), lambda: lib.ssd_selscan_fwd(x, x, A, B, B, init_state=h[:1]),
+        lambda: lib.ssd_selscan_fwd(x, x, A, B, B, init_state=h, final_out=h),
+        lambda: lib.ssd_selscan_fwd(x, x, A, B, B, dt_bias=A), lambda: lib.ssd_selscan_fwd(x, x, A, B, B, dt_limit=(2.0, 1.0)),
+        lambda: lib.ssd_selscan_step(h.bfloat16(), x, x, A, B, B), lambda: lib.ssd_selscan_bwd(x, x, A, B, B, None, None, None, z),
+        lambda: lib.ssd_selscan_bwd(x, x, A, B, B, None, None, None, x, workspace=torch.empty(16, device="cuda")),
+        lambda: lib.ssd_gated_norm_fwd(x, z, w[:, 0].contiguous()), lambda: lib.ssd_gated_norm_fwd(x, None, w[:, 0]),
+        lambda: lib.ssd_gated_norm_fwd(x, None, None), lambda: lib.ssd_gated_norm_fwd(x, None, w[:, 0].contiguous(), ngroups=3),
+        lambda: lib.ssd_gated_norm_fwd(x, None, w[:, 0].contiguous(), ngroups=0),
+        lambda: lib.ssd_gated_norm_fwd(x, None, w[:, 0].contiguous(), eps=-1.0),
+        lambda: lib.ssd_gated_norm_fwd(x.expand(2, 2, 5, 16), None, w[:, 0].contiguous()),
+        lambda: lib.ssd_gated_norm_bwd(x, x, w[:, 0].contiguous(), x[:, :1]),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(lib.SsdArgumentError):
+            call()
+            print("accepted", i)
+    lib.ssd_conv_fwd(x, w)      # and goes on working
+    torch.cuda.synchronize()
+
+
+def test_inputs_repeated_by_strides():
+    # rows broadcast over batch and tokens, and one tensor in several places
+    d = Draw(52)
+    Bz, L, D, N = 3, 70, 24, 16
+    one = d.normal(1, 1, D).expand(Bz, L, D)
+    w, A, dt = d.normal(D, 4), -d.uniform(0.5, 2.0, D, N), d.uniform(0.05, 0.2, Bz, L, D)
+    q = d.normal(1, L, 1, N).expand(Bz, L, 1, N)
+    assert torch.equal(lib.ssd_conv_fwd(one, w)[0], lib.ssd_conv_fwd(one.contiguous(), w)[0])
+    x = d.normal(Bz, L, D)
+    a = lib.ssd_selscan_fwd(x, dt, A, q, q, None, one)
+    b = lib.ssd_selscan_fwd(x, dt, A, q.contiguous(), q.contiguous(), None, one.contiguous())
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    dy = d.normal(Bz, L, D)
+    a = lib.ssd_selscan_bwd(x, dt, A, q, q, None, one, None, dy)
+    b = lib.ssd_selscan_bwd(x, dt, A, q.contiguous(), q.contiguous(), None, one.contiguous(), None, dy)
+    assert all(a[k] is None or torch.equal(a[k], b[k]) for k in a)
+
+
+def test_long_decay_and_wide_ranges():
+    # steps so large that nothing is carried, and none at all: both ends of exp
+    Bz, L, D, N = 1, 300, 64, 16
+    d = Draw(53)
+    x, B, C = d.normal(Bz, L, D), d.normal(Bz, L, 1, N), d.normal(Bz, L, 1, N)
+    A = -d.uniform(1.0, 16.0, D, N)
+    init = d.normal(Bz, D, N)
+    for dt in (torch.full((Bz, L, D), 80.0, device="cuda"), torch.zeros(Bz, L, D, device="cuda"),
+               torch.where(d.normal(Bz, L, D) > 0, 60.0, 1e-6)):
+        y, fin = lib.ssd_selscan_fwd(x, dt, A, B, C, None, None, init)
+        yr, hr, _, _ = ref.selscan(x, dt, A, B, C, None, None, init)
+        ym, hm, _, _ = ref.selscan(np.abs(f(x)), dt, A, np.abs(f(B)), np.abs(f(C)), None, None, np.abs(f(init)))
+        dy = d.normal(Bz, L, D)
+        # a decay below 2^-126 is zero: it is missing from up to L terms, each at most
+        # 2^-126 times a step size of 80, a state, and a gradient sum_t |dy| |C| <= L max max
+        floor = 2.0 ** -126 * L * 80.0 * hm.max() * L * float(dy.abs().max()) * float(C.abs().max()) * 16.0
+        within(y, yr, 400 + 4 * L, ym, "y", floor)
+        within(fin, hr, 400 + 4 * L, hm, "final state", floor)
+        got = lib.ssd_selscan_bwd(x, dt, A, B, C, None, None, init, dy, None, want_dinit=True)
+        want = ref.selscan_bwd(x, dt, A, B, C, None, None, init, dy)
+        mag = ref.selscan_bwd(np.abs(f(x)), dt, A, np.abs(f(B)), np.abs(f(C)), None, None, np.abs(f(init)),
+                              np.abs(f(dy)), mag=True)
+        for k in ("dx", "ddt", "dA", "dB", "dC", "dinit"):
+            within(got[k], want[k], 800 + 8 * L, mag[k], k, floor)

@@ -17,6 +17,7 @@ HEADER = os.path.join(ROOT, "include", "ssd_layer.h")
 OK, NULLP, SHAPE, DTYPE, MISAL, WS, UNSUP, BADVAL = 0, 1, 2, 4, 5, 6, 7, 10
 PTR = 1 << 20      # 16-byte aligned, never dereferenced: a check fails first
 ODD = PTR + 2
+FAR = PTR << 24
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -59,7 +60,7 @@ def outs(*v):
     return (ctypes.c_void_p * 3)(*v)
 
 
-def conv_fwd(prob, x=PTR, xs=None, w=PTR, bias=PTR, init=PTR, y=(PTR, PTR, PTR), fin=PTR):
+def conv_fwd(prob, x=PTR, xs=None, w=PTR, bias=PTR, init=PTR, y=(PTR, PTR, PTR), fin=FAR):
     return lib.load_library().ssd_conv_fwd(None if prob is None else ctypes.byref(prob), p(x), xs, p(w), p(bias),
                                            p(init), None if y is None else outs(*y), p(fin), None)
 
@@ -99,11 +100,13 @@ def test_conv_pointers_and_strides():
     assert conv_step(CP(), state=0) == NULLP and conv_bwd(CP(), ws=0) == NULLP
     assert conv_bwd(CP(), dy=(PTR, PTR, 0)) == NULLP
     assert conv_fwd(CP(batch=0), y=(0, 0, 0)) == SHAPE          # the shape says how many outputs there are
-    for kw in (dict(w=ODD), dict(bias=ODD), dict(init=ODD), dict(fin=ODD), dict(y=(PTR, ODD, PTR)), dict(x=PTR + 1)):
+    for kw in (dict(w=ODD), dict(bias=ODD), dict(init=ODD), dict(fin=FAR + 2), dict(y=(PTR, ODD, PTR)), dict(x=PTR + 1)):
         assert conv_fwd(CP(), **kw) == MISAL, kw
     assert conv_fwd(CP(), xs=st(-1, 64)) == BADVAL and conv_fwd(CP(), xs=st(640, -64)) == BADVAL
     assert conv_fwd(CP(), xs=st(2 ** 62, 64)) == SHAPE
     assert conv_fwd(CP(), x=PTR + 1, xs=st(-1, 64)) == BADVAL   # strides before alignment
+    assert conv_fwd(CP(), fin=PTR) == BADVAL                    # final_state on init_state
+    assert conv_fwd(CP(), fin=PTR + 2 * 3 * 64 * 2 - 16) == BADVAL
     # rows of an output that overlap: tokens, batches
     for s in (st(640, 63), st(639, 64), st(0, 64), st(0, 0)):
         assert conv_bwd(CP(), dxs=s, n=2 ** 60) == BADVAL
@@ -126,7 +129,7 @@ def XF(bias=0, softplus=1, reserved=0, lo=0.0, hi=float("inf")):
 
 
 def scan_fwd(prob, xf=None, x=PTR, dt=PTR, A=PTR, B=PTR, bs=None, C=PTR, cs=None, D=PTR, z=PTR, zs=None, init=PTR,
-             y=PTR, fin=PTR, ws=PTR, n=2 ** 60):
+             y=PTR, fin=FAR, ws=PTR, n=2 ** 60):
     return lib.load_library().ssd_selscan_fwd(ctypes.byref(prob), None if xf is None else ctypes.byref(xf), p(x), p(dt),
                                               p(A), p(B), bs, p(C), cs, p(D), p(z), zs, p(init), p(y), p(fin), p(ws),
                                               n, None)
@@ -168,7 +171,8 @@ def test_scan_bad_transform(xf):
 def test_scan_pointers_and_strides():
     for k in ("x", "dt", "A", "B", "C", "y"):
         assert scan_fwd(SP(), **{k: 0}) == NULLP, k
-    for k in ("x", "dt", "A", "D", "init", "y", "fin", "ws"):
+    assert scan_fwd(SP(), fin=FAR + 2) == MISAL
+    for k in ("x", "dt", "A", "D", "init", "y", "ws"):
         assert scan_fwd(SP(), **{k: ODD}) == MISAL, k
     for k in ("B", "C", "z"):
         assert scan_fwd(SP(), **{k: PTR + 1}) == MISAL, k
@@ -177,6 +181,9 @@ def test_scan_pointers_and_strides():
         assert scan_fwd(SP(), **{k: st(2 ** 62, 32)}) == SHAPE, k
     assert scan_fwd(SP(), z=0, zs=st(-8, 32), n=0) == WS        # strides of an absent z are not looked at
     assert scan_fwd(SP(), XF(bias=ODD)) == MISAL
+    assert scan_fwd(SP(), fin=PTR) == BADVAL and scan_fwd(SP(), fin=PTR - 16) == BADVAL
+    assert scan_fwd(SP(), zs=st(2 ** 40, 2 ** 27)) == UNSUP     # tokens of z 2^28 bytes apart
+    assert scan_bwd(SP(), dzs=st(2 ** 40, 2 ** 27)) == UNSUP
     assert scan_step(SP(), state=0) == NULLP and scan_step(SP(), state=ODD) == MISAL
     assert scan_bwd(SP(), dz=0) == NULLP and scan_bwd(SP(), z=0, dz=0, n=0) == WS
     assert scan_bwd(SP(), dB=ODD) == MISAL and scan_bwd(SP(), ws=0) == NULLP
