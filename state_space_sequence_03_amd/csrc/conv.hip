@@ -11,8 +11,12 @@
 //
 // Both directions are bound by HBM: 2 elements moved per output forwards, 3
 // backwards, against ~20 and ~40 VALU operations.  A thread owns V channels
-// (four where sizes and alignment allow, else one) of a run of tokens and slides a window of W - 1 rows in registers, so each row is loaded
-// once per run plus W - 1 rows of overlap.
+// (four where sizes and alignment allow, else one) of a run of tokens and slides a
+// window of W - 1 rows in registers, so each row is loaded once per run plus W - 1
+// rows of overlap.  Four channels a thread keep enough waves in flight (eight: 87 us
+// against 80 forwards, 102 against 86 backwards).  bf16, width 4: 2 x 8192 tokens of
+// 5376 channels 74 us forwards (4.8 TB/s of the 5.15 that a large copy reaches), 2 x
+// 4096 tokens 70 us backwards (3.8 TB/s; the part sums take 5 of them).
 #include "layer_device.hpp"
 #include "layer_host.hpp"
 

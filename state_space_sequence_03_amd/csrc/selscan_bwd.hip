@@ -14,10 +14,18 @@
 // and, every 8 tokens, the state from a zero start of the chunk; the true state
 // there is that plus the decayed start state.  selscan_bwd_kernel walks a chunk
 // backwards 8 tokens at a time and forms their states and decays again in
-// registers: each decay is formed twice in all, and the checkpoints move 8 N / 8
-// bytes per (t, c) (16 at dstate 16, beside the 22 of the operands).  Walking each
-// chunk forwards once more in place of the checkpoints took 334 us against
-// YY us for 2 x 2048 x 5120 channels x 16 states.
+// registers (a quarter of the decays a third time), and the checkpoints move N
+// bytes per (t, c): 16 at dstate 16, beside the 22 of bf16 operands.
+//
+// Bound by the issue of vector ALU instructions: about 1600 per wave and 8 tokens
+// (64 elements a lane), 860 of them the sums above, the rest the step sizes, the
+// sums across lanes and the broadcasts; counters show the vector ALU busy 75% of
+// the time.  2 x 2048 tokens x 5120 channels x 16 states, bf16 with gate: 452 us in
+// all, 324 of them here, 130 in selscan_kernel<both>, 19 in the chains and 9 in
+// the last sums (kernel trace; the parts run at lower clocks there than the
+// whole).  Walking each chunk forwards once more in place of the checkpoints took
+// the same 472 us when both were measured, and 81 against 69 us for 2 x 515 x 770
+// channels in fp32.
 //
 // dB and dC are sums over channels: over the lane groups of a wave by lane
 // swaps, over a workgroup's waves in LDS, and over workgroups by
@@ -35,13 +43,15 @@ constexpr int kBwdThreads = 256;
 constexpr int kBwdWaves = kBwdThreads / kWave;
 constexpr int kPairs = kSub / 2;    // lanes prepare two tokens of two channels at a time
 // The decays of the last tokens of each 8 stay in registers, those of the first
-// kAgain are formed a second time: all of them would not fit beside the states.
+// kAgain are formed a second time: all of them would not fit beside the states
+// (0, which spills: 468 us, 1: 470, 2: 472, 4: 478; at 38 spilled registers 546).
 constexpr int kAgain = 2;
 
 // Tokens per chunk at most: B and C of all of it, and the waves' parts of dB and
 // dC, fit LDS for two workgroups per CU (dstate up to 32), so that the waves meet
-// at two barriers only.  One barrier per 8 tokens, with chunks three times as long,
-// took ZZ us against YY us for 2 x 2048 x 5120 channels x 16 states.
+// at two barriers only: one barrier per 8 tokens, with chunks three times as long,
+// took 505 us against 472 for 2 x 2048 x 5120 channels x 16 states; chunks of 32
+// tokens 517, of 80 485, of 112 496.
 __host__ __device__ constexpr int bwd_tokens(int NP) { return NP == 16 ? 64 : 32; }
 constexpr int bwd_smem_bytes(int NP) {
   return (bwd_tokens(NP) * 2 * NP * (1 + kBwdWaves) + kBwdThreads * 8) * (int)sizeof(float);
@@ -386,7 +396,9 @@ selscan_reduce_kernel(const float* __restrict__ part, T* __restrict__ dB, T* __r
 
 // ---- host ----
 
-// Chunks: as long as LDS allows, half that where their waves would not fill the chip.
+// Chunks: as long as LDS allows, half that where their waves would not fill the chip
+// (512 tokens of 5120 channels: halved from 2048 waves down 104 us, from 1024 down
+// 114; 2 x 512 x 2048 channels x 4 states: 75 and 92).
 static ScanShape bwd_shape(int64_t batch, int64_t L, int64_t D, int64_t N, int64_t G) {
   ScanShape s;
   const int np = selscan_np(N);
