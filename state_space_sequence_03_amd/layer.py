@@ -211,18 +211,30 @@ def _conv(x, weight, bias, activation, split):
     if len(wshape) != 2 or wshape[0] != shape[2]:
         raise SsdArgumentError(2, "weight must be [channels, width]")
     sizes = (shape[2],) if split is None else tuple(split)
-    if sum(sizes) != shape[2] or min(sizes) < 1:
-        raise SsdArgumentError(2, "split must be positive and add up to channels, got %s" % (sizes,))
+    if not 1 <= len(sizes) <= 3 or sum(sizes) != shape[2] or min(sizes) < 1:
+        raise SsdArgumentError(2, "split must have one to three positive parts that add up to channels, got %s"
+                               % (sizes,))
     key = shape + (wshape[1], sizes, _io_code(x), _ACTIVATIONS[activation])
     ptrs = _rows(x, "x", x.dtype, shape, dev) + (_plain(weight, "weight", _F32, wshape, dev),
                                                  _plain(bias, "bias", _F32, (shape[2],), dev))
     return dev, shape, wshape[1], sizes, key, ptrs
 
 
-def _conv_outputs(x, shape, sizes, split, out):
+def _conv_outputs(x, shape, sizes, split, out, dev):
+    """The outputs and the array of their pointers."""
     if out is None:
-        return [x.new_empty((shape[0], shape[1], c)) for c in sizes]
-    return [out] if split is None else list(out)
+        ys = [x.new_empty((shape[0], shape[1], c)) for c in sizes]
+        return ys, (ctypes.c_void_p * 3)(*[t.data_ptr() for t in ys])
+    ys = [out] if split is None else list(out)
+    return ys, _conv_parts(ys, x, shape, sizes, "out", dev)
+
+
+def _like(x, out, dev):
+    """A contiguous output of the shape of x (the caller's or a new one) and its pointer."""
+    if out is None:
+        out = torch.empty_like(x)
+        return out, out.data_ptr()
+    return out, _plain(out, "out", x.dtype, x.shape, dev)
 
 
 def _conv_parts(ts, x, shape, sizes, name, dev):
@@ -246,13 +258,13 @@ def ssd_conv_fwd(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Ten
     lib = load_library()
     dev, shape, width, sizes, key, ptrs = _conv(x, weight, bias, activation, split)
     state = (shape[0], width - 1, shape[2])
-    ys = _conv_outputs(x, shape, sizes, split, out)
+    ys, parts = _conv_outputs(x, shape, sizes, split, out, dev)
     fin = None
     if want_final_state:
         fin = final_out if final_out is not None else x.new_empty(state)
     _launch(lib.ssd_conv_fwd, dev, _conv_problem(*key), *ptrs,
             _plain(init_state, "init_state", x.dtype, state, dev),
-            _conv_parts(ys, x, shape, sizes, "out", dev), _plain(fin, "final_out", x.dtype, state, dev))
+            parts, _plain(fin, "final_out", x.dtype, state, dev))
     return (ys[0] if split is None else ys), fin
 
 
@@ -263,10 +275,10 @@ def ssd_conv_step(state: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
     seqlen tokens of x.  Returns y as ssd_conv_fwd does."""
     lib = load_library()
     dev, shape, width, sizes, key, ptrs = _conv(x, weight, bias, activation, split)
-    ys = _conv_outputs(x, shape, sizes, split, out)
+    ys, parts = _conv_outputs(x, shape, sizes, split, out, dev)
     _launch(lib.ssd_conv_step, dev, _conv_problem(*key),
             _plain(state, "state", x.dtype, (shape[0], width - 1, shape[2]), dev), *ptrs,
-            _conv_parts(ys, x, shape, sizes, "out", dev))
+            parts)
     return ys[0] if split is None else ys
 
 
@@ -364,13 +376,13 @@ def ssd_selscan_fwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch
     dt_bias [channels], dt_softplus, dt_limit: raw step size, as in ssd_fwd."""
     lib = load_library()
     dev, key, (xf, xfp), ptrs, state = _selscan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit)
-    y = out if out is not None else torch.empty_like(x)
+    y, yp = _like(x, out, dev)
     fin = None
     if want_final_state:
         fin = final_out if final_out is not None else A.new_empty(state)
     ws, ws_bytes, held = _scratch(x, workspace, _scan_bytes(False, *key) if workspace is None else 0, dev)
     _launch(lib.ssd_selscan_fwd, dev, _scan_problem(*key), xfp, *ptrs,
-            _plain(init_state, "init_state", _F32, state, dev), _plain(y, "out", x.dtype, x.shape, dev),
+            _plain(init_state, "init_state", _F32, state, dev), yp,
             _plain(fin, "final_out", _F32, state, dev), ws, ws_bytes)
     return y, fin
 
@@ -384,9 +396,9 @@ def ssd_selscan_step(state: torch.Tensor, x: torch.Tensor, dt: torch.Tensor, A: 
     tokens of x one at a time.  Arguments as for ssd_selscan_fwd; returns y."""
     lib = load_library()
     dev, key, (xf, xfp), ptrs, shape = _selscan(x, dt, A, B, C, D, z, dt_bias, dt_softplus, dt_limit)
-    y = out if out is not None else torch.empty_like(x)
+    y, yp = _like(x, out, dev)
     _launch(lib.ssd_selscan_step, dev, _scan_problem(*key), xfp, _plain(state, "state", _F32, shape, dev),
-            *ptrs, _plain(y, "out", x.dtype, x.shape, dev))
+            *ptrs, yp)
     return y
 
 
@@ -461,8 +473,8 @@ def ssd_gated_norm_fwd(x: torch.Tensor, z: Optional[torch.Tensor], weight: torch
     norm_before_gate to the normalised output.  Returns y."""
     lib = load_library()
     dev, shape, key, ptrs = _gated_norm(x, z, weight, ngroups, eps, norm_before_gate)
-    y = out if out is not None else torch.empty_like(x)
-    _launch(lib.ssd_gated_norm_fwd, dev, _norm_problem(*key), *ptrs, _plain(y, "out", x.dtype, shape, dev))
+    y, yp = _like(x, out, dev)
+    _launch(lib.ssd_gated_norm_fwd, dev, _norm_problem(*key), *ptrs, yp)
     return y
 
 
