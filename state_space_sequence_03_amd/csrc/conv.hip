@@ -16,7 +16,10 @@
 // rows of overlap.  Four channels a thread keep enough waves in flight (eight: 87 us
 // against 80 forwards, 102 against 86 backwards).  bf16, width 4: 2 x 8192 tokens of
 // 5376 channels 74 us forwards (4.8 TB/s of the 5.15 that a large copy reaches), 2 x
-// 4096 tokens 70 us backwards (3.8 TB/s; the part sums take 5 of them).
+// 4096 tokens 66 us backwards (4.0 TB/s; the part sums take 5 of them; 72 with
+// every row's conditions tested inside the run).
+#include <type_traits>
+
 #include "layer_device.hpp"
 #include "layer_host.hpp"
 
@@ -146,12 +149,12 @@ conv_fwd_kernel(const T* __restrict__ x, Strides xs, const float* __restrict__ w
 // their dw and dbias in LDS, in order, and leave one row of part sums
 // [W + 1][C] in the workspace; conv_reduce_kernel adds those rows in order, so the
 // same call gives the same bits.
-template <typename T, int V, int W>
+template <typename T, int V, int W, bool ACT>
 __global__ void __launch_bounds__(kConvThreads)
 conv_bwd_kernel(const T* __restrict__ x, Strides xs, const float* __restrict__ w,
                 const float* __restrict__ bias, const T* __restrict__ init, ConvParts dy,
                 const T* __restrict__ dfin, T* __restrict__ dx, Strides dxs, T* __restrict__ dinit,
-                float* __restrict__ part, int silu, int64_t L, int64_t C, ConvTiles tiles,
+                float* __restrict__ part, int64_t L, int64_t C, ConvTiles tiles,
                 int lc_log, int64_t run) {
   const int lanes = 1 << lc_log;
   const int lane = threadIdx.x & (lanes - 1);
@@ -208,6 +211,71 @@ conv_bwd_kernel(const T* __restrict__ x, Strides xs, const float* __restrict__ w
           gn[a] = load_raw<T, V>(g.p + (t + a) * g.ld);
         }
     };
+    // Row t: du there (zero where not IN: past the last token), the sums of dw and
+    // dbias (ADD: rows of this run), and row s = t - (W - 1) of dx, which takes du[s ..
+    // s + W - 1] = gw[0 .. W - 2], du (OUT; before the first token it is dinit's).
+    auto form = [&](auto IN, auto ADD, auto OUT, const Raw& xr, const Raw& gr, int64_t t) {
+      float xc[V], du[V];
+      if constexpr (decltype(IN)::value) {
+        float gc[V];
+        widen<T, V>(xr, xc);
+        widen<T, V>(gr, gc);
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float u = fmaf(wt[W - 1][v], xc[v], bs[v]);
+#pragma unroll
+          for (int k = 0; k < W - 1; ++k) u = fmaf(wt[k][v], xw[k][v], u);
+          du[v] = ACT ? gc[v] * silu_slope(u, sigmoid_f32(u)) : gc[v];
+        }
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) xc[v] = du[v] = 0.0f;
+      }
+      if constexpr (decltype(ADD)::value) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          db[v] += du[v];
+          dw[W - 1][v] = fmaf(du[v], xc[v], dw[W - 1][v]);
+#pragma unroll
+          for (int k = 0; k < W - 1; ++k) dw[k][v] = fmaf(du[v], xw[k][v], dw[k][v]);
+        }
+      }
+      if constexpr (decltype(OUT)::value) {
+        const int64_t s = t - (W - 1);
+        float o[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          o[v] = wt[0][v] * du[v];
+#pragma unroll
+          for (int k = 0; k < W - 1; ++k) o[v] = fmaf(wt[W - 1 - k][v], gw[k][v], o[v]);
+        }
+        const int64_t f = s - (L - (W - 1));   // this input's row in the final state
+        if (f >= 0 && dfin) {
+          float d[V];
+          load_v<V>(dfin + (b * (W - 1) + f) * C + c, d);
+#pragma unroll
+          for (int v = 0; v < V; ++v) o[v] += d[v];
+        }
+        if (s >= 0)
+          store_v<V>(dxp + s * dxs.token, o);
+        else if (dinit)
+          store_v<V>(dinit + (b * (W - 1) + s + (W - 1)) * C + c, o);
+      }
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int k = 0; k + 1 < W - 1; ++k) {
+          xw[k][v] = xw[k + 1][v];
+          gw[k][v] = gw[k + 1][v];
+        }
+        xw[W - 2][v] = xc[v];
+        gw[W - 2][v] = du[v];
+      }
+    };
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+    // the run's own rows; the first W - 1 complete no row of dx, but for the sequence's
+    // first run, whose dinit they are
 #pragma unroll
     for (int a = 0; a < M; ++a) xn[a] = gn[a] = zero_raw<T, V>();
     load(t0);
@@ -219,65 +287,25 @@ conv_bwd_kernel(const T* __restrict__ x, Strides xs, const float* __restrict__ w
         gr[a] = gn[a];
       }
       load(tt + M);
+      if (tt >= t0 + W - 1 && tt + M <= t1) {
 #pragma unroll
-      for (int a = 0; a < M; ++a) {
-        const int64_t t = tt + a;
-        if (t >= end) break;
-        float xc[V], du[V];
+        for (int a = 0; a < M; ++a) form(yes, yes, yes, xr[a], gr[a], tt + a);
+      } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) xc[v] = du[v] = 0.0f;
-        if (t < L) {
-          float gc[V];
-          widen<T, V>(xr[a], xc);
-          widen<T, V>(gr[a], gc);
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            float u = fmaf(wt[W - 1][v], xc[v], bs[v]);
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k) u = fmaf(wt[k][v], xw[k][v], u);
-            du[v] = silu ? gc[v] * silu_slope(u, sigmoid_f32(u)) : gc[v];
-          }
+        for (int a = 0; a < M; ++a) {
+          const int64_t t = tt + a;
+          if (t >= end) break;
+          const bool out = t - (W - 1) >= first;
           if (t < t1) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-              db[v] += du[v];
-              dw[W - 1][v] = fmaf(du[v], xc[v], dw[W - 1][v]);
-#pragma unroll
-              for (int k = 0; k < W - 1; ++k) dw[k][v] = fmaf(du[v], xw[k][v], dw[k][v]);
-            }
+            if (out) form(yes, yes, yes, xr[a], gr[a], t);
+            else form(yes, yes, no, xr[a], gr[a], t);
+          } else if (t < L) {
+            if (out) form(yes, no, yes, xr[a], gr[a], t);
+            else form(yes, no, no, xr[a], gr[a], t);
+          } else {
+            if (out) form(no, no, yes, xr[a], gr[a], t);
+            else form(no, no, no, xr[a], gr[a], t);
           }
-        }
-        // row s = t - (W - 1) of dx takes du[s .. s + W - 1] = gw[0 .. W - 2], du
-        const int64_t s = t - (W - 1);
-        if (s >= first && s < t1) {
-          float o[V];
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            o[v] = wt[0][v] * du[v];
-#pragma unroll
-            for (int k = 0; k < W - 1; ++k) o[v] = fmaf(wt[W - 1 - k][v], gw[k][v], o[v]);
-          }
-          const int64_t f = s - (L - (W - 1));   // this input's row in the final state
-          if (dfin && f >= 0) {
-            float d[V];
-            load_v<V>(dfin + (b * (W - 1) + f) * C + c, d);
-#pragma unroll
-            for (int v = 0; v < V; ++v) o[v] += d[v];
-          }
-          if (s >= 0)
-            store_v<V>(dxp + s * dxs.token, o);
-          else if (dinit)
-            store_v<V>(dinit + (b * (W - 1) + s + (W - 1)) * C + c, o);
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-#pragma unroll
-          for (int k = 0; k + 1 < W - 1; ++k) {
-            xw[k][v] = xw[k + 1][v];
-            gw[k][v] = gw[k + 1][v];
-          }
-          xw[W - 2][v] = xc[v];
-          gw[W - 2][v] = du[v];
         }
       }
     }
@@ -404,12 +432,12 @@ static hipError_t conv_bwd_v(const ConvArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(kernel, grid, dim3(g.threads()), 0, stream, static_cast<const T*>(a.x),
                        Strides{a.xs[0], a.xs[1]}, a.w, a.bias, static_cast<const T*>(a.init), dy,
                        static_cast<const T*>(a.dfin), static_cast<T*>(a.dx),
-                       Strides{a.dxs[0], a.dxs[1]}, static_cast<T*>(a.dinit), part, a.silu, a.L,
+                       Strides{a.dxs[0], a.dxs[1]}, static_cast<T*>(a.dinit), part, a.L,
                        a.C, ConvTiles{g.bx, g.by}, g.lc_log, g.run);
   };
-  if (a.W == 2) go(conv_bwd_kernel<T, V, 2>);
-  else if (a.W == 3) go(conv_bwd_kernel<T, V, 3>);
-  else go(conv_bwd_kernel<T, V, 4>);
+  if (a.W == 2) a.silu ? go(conv_bwd_kernel<T, V, 2, true>) : go(conv_bwd_kernel<T, V, 2, false>);
+  else if (a.W == 3) a.silu ? go(conv_bwd_kernel<T, V, 3, true>) : go(conv_bwd_kernel<T, V, 3, false>);
+  else a.silu ? go(conv_bwd_kernel<T, V, 4, true>) : go(conv_bwd_kernel<T, V, 4, false>);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t cols = (a.W + 1) * a.C;
