@@ -210,7 +210,7 @@ def _conv(x, weight, bias, activation, split):
     wshape = tuple(weight.shape) if isinstance(weight, torch.Tensor) else ()
     if len(wshape) != 2 or wshape[0] != shape[2]:
         raise SsdArgumentError(2, "weight must be [channels, width]")
-    sizes = (shape[2],) if split is None else tuple(split)
+    sizes = (shape[2],) if split is None else tuple(map(int, split))
     if not 1 <= len(sizes) <= 3 or sum(sizes) != shape[2] or min(sizes) < 1:
         raise SsdArgumentError(2, "split must have one to three positive parts that add up to channels, got %s"
                                % (sizes,))
@@ -460,7 +460,7 @@ def _gated_norm(x, z, weight, ngroups, eps, norm_before_gate):
     dev = x.get_device()
     if weight is None:
         raise SsdArgumentError(1, "weight must be a GPU tensor")
-    key = shape + (ngroups, eps, norm_before_gate, _io_code(x))
+    key = shape + (int(ngroups), float(eps), bool(norm_before_gate), _io_code(x))
     return dev, shape, key, (_plain(x, "x", x.dtype, shape, dev),) + _rows(z, "z", x.dtype, shape, dev) + \
         (_plain(weight, "weight", _F32, (shape[2],), dev),)
 

@@ -582,3 +582,20 @@ def test_long_decay_and_wide_ranges():
                               np.abs(f(dy)), mag=True)
         for k in ("dx", "ddt", "dA", "dB", "dC", "dinit"):
             within(got[k], want[k], 800 + 8 * L, mag[k], k, floor)
+
+
+def test_options_are_taken_by_value():
+    """Options that change in place between two calls count as they are at each call."""
+    d = Draw(9)
+    x, w, cw = d.rows(2, 3, 16), d.normal(16), d.normal(16, 4)
+    eps = torch.tensor(0.25)
+    first = lib.ssd_gated_norm_fwd(x, None, w, eps=eps)
+    eps.fill_(4.0)
+    assert torch.equal(first, lib.ssd_gated_norm_fwd(x, None, w, eps=0.25))
+    assert torch.equal(lib.ssd_gated_norm_fwd(x, None, w, eps=eps), lib.ssd_gated_norm_fwd(x, None, w, eps=4.0))
+    split = torch.tensor([4, 12])
+    lib.ssd_conv_fwd(x, cw, split=split)
+    split.copy_(torch.tensor([8, 8]))
+    ys = lib.ssd_conv_fwd(x, cw, split=split)[0]
+    assert [t.shape[2] for t in ys] == [8, 8]
+    assert torch.equal(cat(ys), lib.ssd_conv_fwd(x, cw)[0])
