@@ -15,9 +15,10 @@
 // window of W - 1 rows in registers, so each row is loaded once per run plus W - 1
 // rows of overlap.  Four channels a thread keep enough waves in flight (eight: 87 us
 // against 80 forwards, 102 against 86 backwards).  bf16, width 4: 2 x 8192 tokens of
-// 5376 channels 74 us forwards (4.8 TB/s of the 5.15 that a large copy reaches), 2 x
-// 4096 tokens 66 us backwards (4.0 TB/s; the part sums take 5 of them; 72 with
-// every row's conditions tested inside the run).
+// 5376 channels 74 us forwards (4.8 TB/s of the 5.15 that a large copy reaches; runs of
+// 16 tokens, of 8 and 64 tokens 3 us more), 2 x 4096 tokens 66 us backwards (4.0 TB/s;
+// the part sums take 5 of them).  Both have a path without conditions for the rows
+// inside a run: with them 78 and 72 us.
 #include <type_traits>
 
 #include "layer_device.hpp"
@@ -65,11 +66,10 @@ __device__ __forceinline__ bool conv_tile(const ConvTiles& n, int64_t* ix, int64
 
 // Threads of a workgroup: lc lanes along the channels (a power of two up to
 // 64), kConvThreads / lc runs of tokens.
-template <typename T, int V, int W>
+template <typename T, int V, int W, bool ACT>
 __global__ void __launch_bounds__(kConvThreads)
 conv_fwd_kernel(const T* __restrict__ x, Strides xs, const float* __restrict__ w,
-                const float* __restrict__ bias, const T* init, ConvParts y, T* fin, int silu,
-                int64_t L, int64_t C, ConvTiles tiles, int lc_log, int64_t run) {
+                const float* __restrict__ bias, const T* init, ConvParts y, T* fin, int64_t L, int64_t C, ConvTiles tiles, int lc_log, int64_t run) {
   constexpr int M = kFwdAhead;
   int64_t ix, iy;
   if (!conv_tile(tiles, &ix, &iy)) return;
@@ -104,36 +104,49 @@ conv_fwd_kernel(const T* __restrict__ x, Strides xs, const float* __restrict__ w
 #pragma unroll
   for (int a = 0; a < M; ++a)
     next[a] = t0 + a < t1 ? load_raw<T, V>(xp + (t0 + a) * xs.token) : zero_raw<T, V>();
-  for (int64_t t = t0; t < t1; t += M) {
+  auto form = [&](const Raw& cur, int64_t t) {
+    float u[V], r[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) u[v] = bs[v];
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+      widen<T, V>(win[k], r);
+#pragma unroll
+      for (int v = 0; v < V; ++v) u[v] = fmaf(wt[k][v], r[v], u[v]);
+    }
+    widen<T, V>(cur, r);
+#pragma unroll
+    for (int v = 0; v < V; ++v) u[v] = fmaf(wt[W - 1][v], r[v], u[v]);
+    if constexpr (ACT) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) u[v] *= sigmoid_f32(u[v]);
+    }
+    store_v<V>(o.p + t * o.ld, u);
+#pragma unroll
+    for (int k = 0; k + 1 < W - 1; ++k) win[k] = win[k + 1];
+    win[W - 2] = cur;
+  };
+  for (int64_t t = t0; t < t1; t += M) {   // whole groups of M rows without conditions
     Raw cur[M];
 #pragma unroll
     for (int a = 0; a < M; ++a) cur[a] = next[a];
+    if (t + 2 * M <= t1) {
 #pragma unroll
-    for (int a = 0; a < M; ++a)
-      if (t + M + a < t1) next[a] = load_raw<T, V>(xp + (t + M + a) * xs.token);
+      for (int a = 0; a < M; ++a) next[a] = load_raw<T, V>(xp + (t + M + a) * xs.token);
+    } else {
 #pragma unroll
-    for (int a = 0; a < M; ++a) {
-      if (t + a >= t1) break;
-      float u[V], r[V];
+      for (int a = 0; a < M; ++a)
+        if (t + M + a < t1) next[a] = load_raw<T, V>(xp + (t + M + a) * xs.token);
+    }
+    if (t + M <= t1) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) u[v] = bs[v];
+      for (int a = 0; a < M; ++a) form(cur[a], t + a);
+    } else {
 #pragma unroll
-      for (int k = 0; k < W - 1; ++k) {
-        widen<T, V>(win[k], r);
-#pragma unroll
-        for (int v = 0; v < V; ++v) u[v] = fmaf(wt[k][v], r[v], u[v]);
+      for (int a = 0; a < M; ++a) {
+        if (t + a >= t1) break;
+        form(cur[a], t + a);
       }
-      widen<T, V>(cur[a], r);
-#pragma unroll
-      for (int v = 0; v < V; ++v) u[v] = fmaf(wt[W - 1][v], r[v], u[v]);
-      if (silu) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) u[v] *= sigmoid_f32(u[v]);
-      }
-      store_v<V>(o.p + (t + a) * o.ld, u);
-#pragma unroll
-      for (int k = 0; k + 1 < W - 1; ++k) win[k] = win[k + 1];
-      win[W - 2] = cur[a];
     }
   }
   if (fin && t1 == L) {   // the run that ends the sequence holds the last W - 1 inputs
@@ -408,11 +421,11 @@ static hipError_t conv_fwd_v(const ConvArgs& a, hipStream_t stream) {
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, grid, dim3(g.threads()), 0, stream, static_cast<const T*>(a.x),
                        Strides{a.xs[0], a.xs[1]}, a.w, a.bias, static_cast<const T*>(a.init), y,
-                       static_cast<T*>(a.fin), a.silu, a.L, a.C, ConvTiles{g.bx, g.by}, g.lc_log, g.run);
+                       static_cast<T*>(a.fin), a.L, a.C, ConvTiles{g.bx, g.by}, g.lc_log, g.run);
   };
-  if (a.W == 2) go(conv_fwd_kernel<T, V, 2>);
-  else if (a.W == 3) go(conv_fwd_kernel<T, V, 3>);
-  else go(conv_fwd_kernel<T, V, 4>);
+  if (a.W == 2) a.silu ? go(conv_fwd_kernel<T, V, 2, true>) : go(conv_fwd_kernel<T, V, 2, false>);
+  else if (a.W == 3) a.silu ? go(conv_fwd_kernel<T, V, 3, true>) : go(conv_fwd_kernel<T, V, 3, false>);
+  else a.silu ? go(conv_fwd_kernel<T, V, 4, true>) : go(conv_fwd_kernel<T, V, 4, false>);
   return hipGetLastError();
 }
 
