@@ -453,8 +453,8 @@ selscan_step_kernel(float* __restrict__ state, const T* __restrict__ x, const T*
 // ---- host ----
 
 // Chunks of the forward pass.  One where its waves nearly fill the chip (1024 tokens
-// of 5120 channels: for 8 batches, 640 waves, chunks take 353 us and one chunk 398, for
-// 10 batches 451 and 402); otherwise as many as give about two waves per SIMD
+// of 5120 channels: for 8 batches, 640 waves, chunks take 306 us and one chunk 334, for
+// 10 batches 399 and 340); otherwise as many as give about two waves per SIMD
 // (2048 tokens of 5120 channels x 16 states: 25 chunks 104 us, 12 chunks 128, 38
 // chunks 107, 50 chunks 123: more chunks cost more starts and longer chains), of at
 // least 16 tokens (300 tokens of 2560 channels: at least 16 28 us, 32 35, 64 54), and
