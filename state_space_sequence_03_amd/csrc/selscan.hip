@@ -91,6 +91,10 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
     ox[u] = own < Dg ? (unsigned)(u * sh.D + c) * (unsigned)sizeof(T) : kOutside;
     oz[u] = GATE && own < Dg ? (unsigned)(u * io.zs.token + c) * (unsigned)sizeof(T) : kOutside;
   }
+  // kBoth has no registers for them: each offset is formed from the first where it is used
+  auto offset = [&](const unsigned* o, unsigned first, int u, int64_t stride) {
+    return MODE == kBoth ? first + (unsigned)u * (unsigned)(stride * sizeof(T)) : o[u];
+  };
   const int64_t t0 = k * sh.T;
   const int len = (int)(t0 + sh.T < sh.L ? sh.T : sh.L - t0);   // tokens of this chunk
 
@@ -188,20 +192,21 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
     const int valid = t + U <= len ? U : len - t;
     const Rows rx = rows_at(xp + t * sh.D, valid, sh.D, sh.D);
     const Rows rd = rows_at(dp + t * sh.D, valid, sh.D, sh.D);
+    const unsigned fx = MODE == kBoth ? fresh(ox[0]) : 0, fz = MODE == kBoth && GATE ? fresh(oz[0]) : 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      xr[u] = row_load<T>(rx, ox[u]);
-      dr[u] = row_load<T>(rd, ox[u]);
+      xr[u] = row_load<T>(rx, offset(ox, fx, u, sh.D));
+      dr[u] = row_load<T>(rd, offset(ox, fx, u, sh.D));
     }
     if constexpr (GATE && MODE != kStates) {
       const Rows rz = rows_at(zp + t * io.zs.token, valid, io.zs.token, sh.D);
 #pragma unroll
-      for (int u = 0; u < U; ++u) zr[u] = row_load<T>(rz, oz[u]);
+      for (int u = 0; u < U; ++u) zr[u] = row_load<T>(rz, offset(oz, fz, u, io.zs.token));
     }
     if constexpr (MODE == kBoth) {
       const Rows rg = rows_at(gp + t * sh.D, valid, sh.D, sh.D);
 #pragma unroll
-      for (int u = 0; u < U; ++u) gr[u] = row_load<T>(rg, ox[u]);
+      for (int u = 0; u < U; ++u) gr[u] = row_load<T>(rg, offset(ox, fx, u, sh.D));
     }
   };
 
