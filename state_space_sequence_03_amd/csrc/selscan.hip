@@ -166,24 +166,25 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
     const int lc = base + dl * 2 + j;
     oc[j] = lc < Dg ? (unsigned)((g * Dg + lc) * NP + n0) * 4u : kOutside;
   }
-  // B and C of one tile, held in registers from their load to their place in LDS
-  float rb[PER], rc[MODE == kStates ? 1 : PER];
+  // B and C of one tile, held in registers from their load to their place in LDS, and
+  // widened there: a conversion here would wait for them, and for the rows ahead
+  T rb[PER], rc[MODE == kStates ? 1 : PER];
   auto fetch = [&](int t) {
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       const int i = q * kScanThreads + tid;
       const int tok = t + i / NP, n = i % NP;
       const bool in = tok < len && n < N;
-      rb[q] = in ? to_f32(Bp[tok * io.bs.token + n]) : 0.0f;
-      if constexpr (MODE != kStates) rc[q] = in ? to_f32(Cp[tok * io.cs.token + n]) : 0.0f;
+      rb[q] = in ? Bp[tok * io.bs.token + n] : T(0.0f);
+      if constexpr (MODE != kStates) rc[q] = in ? Cp[tok * io.cs.token + n] : T(0.0f);
     }
   };
   auto place = [&](int buf) {
 #pragma unroll
     for (int q = 0; q < PER; ++q) {
       const int i = q * kScanThreads + tid;
-      sB[buf][i / NP][i % NP] = rb[q];
-      if constexpr (MODE != kStates) sC[buf][i / NP][i % NP] = rc[q];
+      sB[buf][i / NP][i % NP] = to_f32(rb[q]);
+      if constexpr (MODE != kStates) sC[buf][i / NP][i % NP] = to_f32(rc[q]);
     }
   };
 
