@@ -231,7 +231,7 @@ selscan_kernel(ScanIo<T> io, ScanShape sh) {
           gate[u] = GATE && MODE != kStates ? to_f32(zr[u]) : 1.0f;
           ds[u] = MODE == kBoth ? to_f32(gr[u]) : 0.0f;
         }
-        if (ts + U < len) load(ts + U);
+        load(ts + U);   // past the chunk's last token an empty resource: zeros, and no branch
         if constexpr (MODE == kBoth) {
           if (ts > 0) {   // the state and the step sizes so far, before these 8 tokens
             const int64_t at = (b * ((sh.L + kSub - 1) / kSub) + (t0 + ts) / kSub) * sh.D;

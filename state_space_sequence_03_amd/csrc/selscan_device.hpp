@@ -38,7 +38,7 @@ template <int J> __device__ __forceinline__ float pair_bcast(float v) {
 // byte offsets from the first row stay in registers, moving on by some rows costs
 // scalar work only, and the resource ends after the last valid row, so that loads
 // past it give zero and stores past it are dropped, as at kOutside for lanes
-// without a channel.
+// without a channel.  With no valid row it is empty.
 typedef __amdgpu_buffer_rsrc_t Rows;
 constexpr unsigned kOutside = 0x80000000u;   // eight rows end before it, and it plus them below 2^32
 __device__ __forceinline__ unsigned fresh(unsigned v) {
@@ -50,7 +50,8 @@ template <typename T> __device__ __forceinline__ Rows rows_bytes(const T* first,
 }
 template <typename T>
 __device__ __forceinline__ Rows rows_at(const T* first, int valid, int64_t stride, int64_t width) {
-  const unsigned bytes = (unsigned)(valid - 1) * (unsigned)(stride * sizeof(T)) + (unsigned)(width * sizeof(T));
+  const unsigned bytes =
+      valid > 0 ? (unsigned)(valid - 1) * (unsigned)(stride * sizeof(T)) + (unsigned)(width * sizeof(T)) : 0u;
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(first), (short)0, (int)bytes, 0x00020000);
 }
 template <typename T> __device__ __forceinline__ T row_load(Rows r, unsigned bytes) {
