@@ -49,9 +49,9 @@ COMMON_FLAGS = [
 # measured ~4% faster (256 VGPRs, no spills at the shapes dispatched there).
 # chunk_state runs four waves per SIMD and loses that occupancy under it.
 # The selective scan holds rows loaded ahead in bf16; the SLP vectoriser pairs them
-# in one register as they arrive, which waits for the loads at once.  Without it 2 x
-# 2048 x 5120 x 16 gradients take 429 us instead of 452, 1 x 2048 forwards 101
-# instead of 104, and 16 x 1024 x 5120 x 8 forwards 376 instead of 851.
+# in one register as they arrive, which waits for the loads at once.  Switching it
+# off took the gradients of 2 x 2048 x 5120 x 16 from 452 to 429 us, 1 x 2048 tokens
+# forwards from 104 to 101, and 16 x 1024 x 5120 x 8 forwards from 851 to 376.
 SOURCE_FLAGS = {
     "selscan.hip": ["-fno-slp-vectorize"],
     "selscan_bwd.hip": ["-fno-slp-vectorize"],

@@ -20,8 +20,8 @@
 // Bound by the issue of vector ALU instructions: about 1600 per wave and 8 tokens
 // (64 elements a lane), 860 of them the sums above, the rest the step sizes, the
 // sums across lanes and the broadcasts; counters show the vector ALU busy 75% of
-// the time.  2 x 2048 tokens x 5120 channels x 16 states, bf16 with gate: 452 us in
-// all, 324 of them here, 130 in selscan_kernel<both>, 19 in the chains and 9 in
+// the time.  2 x 2048 tokens x 5120 channels x 16 states, bf16 with gate: 423 us in
+// all, 320 of them here, 131 in selscan_kernel<both>, 20 in the chains and 9 in
 // the last sums (kernel trace; the parts run at lower clocks there than the
 // whole).  Walking each chunk forwards once more in place of the checkpoints took
 // the same 472 us when both were measured, and 81 against 69 us for 2 x 515 x 770
@@ -44,7 +44,8 @@ constexpr int kBwdWaves = kBwdThreads / kWave;
 constexpr int kPairs = kSub / 2;    // lanes prepare two tokens of two channels at a time
 // The decays of the last tokens of each 8 stay in registers, those of the first
 // kAgain are formed a second time: all of them would not fit beside the states
-// (0, which spills: 468 us, 1: 470, 2: 472, 4: 478; at 38 spilled registers 546).
+// (0 and 1, which spill: 513 and 453 us, 2: 429, 3: 432, 4: 436 for all kernels at the
+// size above).
 constexpr int kAgain = 2;
 
 // Tokens per chunk at most: B and C of all of it, and the waves' parts of dB and
