@@ -31,10 +31,11 @@
  * with its last axis contiguous and an ssd_strides for the other two, in
  * elements: a slice of a wider projection is read or written in place.  A NULL
  * ssd_strides means contiguous.  Strides of inputs may be any values >= 0 (0
- * repeats a row); strides of outputs must keep rows apart.  A strided pointer
- * needs the alignment of its element only; every other pointer is 16-byte
- * aligned.  Where pointers, strides and sizes allow accesses of several elements
- * they are used.
+ * repeats a row); strides of outputs must keep rows apart.  The stride between
+ * tokens (batches) of a call with one token (batch) separates nothing: any value
+ * >= 0 does, of an output too.  A strided pointer needs the alignment of its
+ * element only; every other pointer is 16-byte aligned.  Where pointers, strides
+ * and sizes allow accesses of several elements they are used.
  *
  * Errors, in this order: SSD_ERR_NULL_POINTER, SSD_ERR_BAD_SHAPE (a size <= 0, sizes
  * that do not divide or add up, or a product overflowing int64),
@@ -151,8 +152,8 @@ ssd_status ssd_selscan_fwd_workspace_size(const ssd_selscan_problem* prob, size_
  *   init_state, final_state : [batch, channels, dstate] fp32, or NULL.
  *   workspace   : ssd_selscan_fwd_workspace_size bytes (which may be 0: then it
  *                 may be NULL).
- * Errors: UNSUPPORTED for dstate > 64, batch > 65535, tokens of z 2^28 bytes or
- * more apart, or sizes past a launch's 2^32 threads. */
+ * Errors: UNSUPPORTED for dstate > 64, batch > 65535, several tokens of z 2^28 bytes
+ * or more apart, or sizes past a launch's 2^32 threads. */
 ssd_status ssd_selscan_fwd(const ssd_selscan_problem* prob, const ssd_dt_transform* dtx,
                            const void* x, const void* dt, const float* A, const void* B,
                            const ssd_strides* b_strides, const void* C,

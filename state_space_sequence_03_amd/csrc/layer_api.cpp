@@ -203,7 +203,13 @@ ssd_status scan_supported(const ssd_selscan_problem& p) {
     return fail(SSD_ERR_UNSUPPORTED, "grid too large for this build");
   return SSD_OK;
 }
-// The kernels reach eight rows of z and dz by 32-bit byte offsets.
+// The kernels reach eight rows of z and dz by 32-bit byte offsets, and drop what they
+// store past the last token by its place behind that row's end.  With one token the
+// caller's stride says neither how far rows are apart nor that they are, so a row's
+// width takes its place.
+void one_token_rows(const ssd_selscan_problem& p, int64_t s[2]) {
+  if (p.seqlen == 1) s[1] = p.channels;
+}
 ssd_status scan_rows(const ssd_selscan_problem& p, const ssd::ScanArgs& a) {
   const int64_t most = ((int64_t(1) << 28) - 1) / (int64_t)element(p.io_dtype);
   if ((a.z && a.zs[1] > most) || (a.dz && a.dzs[1] > most))
@@ -247,6 +253,7 @@ ssd_status scan_common(const ssd_selscan_problem& p, const ssd_dt_transform* dtx
   if (z) {
     st = check_strides("z", a->zs, p.batch, p.seqlen, p.channels, false);
     if (st != SSD_OK) return st;
+    one_token_rows(p, a->zs);
   }
   return SSD_OK;
 }
@@ -491,6 +498,7 @@ ssd_status ssd_selscan_bwd(const ssd_selscan_problem* prob, const ssd_dt_transfo
     if (z) {
       st = check_strides("dz", a.dzs, a.batch, a.L, a.D, true);
       if (st != SSD_OK) return st;
+      one_token_rows(*prob, a.dzs);
     }
     a.init = init_state;
     a.dy = dy;

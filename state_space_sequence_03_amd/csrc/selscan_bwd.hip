@@ -224,6 +224,7 @@ selscan_bwd_kernel(ScanBwdIo<T> io, ScanShape sh) {
       const int more = (s * kSub + kSub <= len ? kSub : len - s * kSub) - 1;
       const int64_t t8 = row + (int64_t)s * kSub * sh.D;
       const Rows wx = rows_bytes(io.dx + t8, (more + 1) * xrow), wd = rows_bytes(io.ddt + t8, (more + 1) * xrow);
+      // (rows of dz are at least a row apart, also where there is one: rows past the last end behind it)
       const Rows wz = rows_bytes(GATE ? zo + s * kSub * io.dzs.token : nullptr, more * zorow + xrow);
 #pragma unroll
       for (int p = 0; p < kPairs; ++p) {

@@ -426,7 +426,7 @@ def ssd_selscan_bwd(x: torch.Tensor, dt: torch.Tensor, A: torch.Tensor, B: torch
            "dz": None, "dinit": A.new_empty(state) if want_dinit else None,
            "ddt_bias": A.new_empty((state[1],)) if want_ddt_bias else None}
     if z is not None:
-        got["dz"] = dz_out if dz_out is not None else torch.empty_like(x)
+        got["dz"] = dz_out if dz_out is not None else x.new_empty(x.shape)
     ws, ws_bytes, held = _scratch(x, workspace, _scan_bytes(True, *key) if workspace is None else 0, dev)
     ptr = lambda k: None if got[k] is None else got[k].data_ptr()
     _launch(lib.ssd_selscan_bwd, dev, _scan_problem(*key), xfp, *ptrs,
@@ -493,7 +493,7 @@ def ssd_gated_norm_bwd(x: torch.Tensor, z: Optional[torch.Tensor], weight: torch
     dx = torch.empty_like(x)
     dz = None
     if z is not None:
-        dz = dz_out if dz_out is not None else torch.empty_like(x)
+        dz = dz_out if dz_out is not None else x.new_empty(x.shape)
     dw = torch.empty_like(weight)
     ws, ws_bytes, held = _scratch(x, workspace, _norm_bwd_bytes(*key) if workspace is None else 0, dev)
     _launch(lib.ssd_gated_norm_bwd, dev, _norm_problem(*key), *ptrs, _plain(dy, "dy", x.dtype, shape, dev),
