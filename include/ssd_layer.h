@@ -197,6 +197,9 @@ ssd_status ssd_selscan_bwd(const ssd_selscan_problem* prob, const ssd_dt_transfo
  * (1 without z) and, in each group, r = (sum(u^2) / S + eps)^(-1/2):
  *     norm_before_gate 0:  u = x s(z),  y = weight u r
  *     norm_before_gate 1:  u = x,       y = weight u r s(z)
+ * The sums of u^2 and, for the gradients, of weight dy u (dy s(z) u where the norm
+ * comes first) are fp32 and have to fit it; with eps 0 a group has to have an u that
+ * is not 0.
  */
 typedef struct {
   int64_t batch;
