@@ -1,9 +1,14 @@
 """The operators around the scan where a launch is large enough to choose its other forms: long
-runs of the convolution.  The tests repeat the launch rule a
-case is meant for, so that one which no longer reaches its form says so."""
+runs of the convolution, several batches per lane of the token scan, one chunk for a whole prompt,
+long chunks of the gradients.  The tests repeat the launch
+rule a case is meant for, so that one which no longer reaches its form says so."""
+import numpy as np
 import pytest
 
+import state_space_sequence_03_amd as lib
 import test_gpu_layer as base
+from layer_util import within
+from oracle import layer as ref
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +56,81 @@ def test_conv_runs(case, V, fwd, bwd):
     assert run_of(batch, L, C, V, 16, 4096) == fwd and run_of(batch, L, C, V, 64, 2048) == bwd
     base.test_conv_fwd(case)
     base.test_conv_bwd(case)
+
+
+# ---- selective scan: batches per lane of the token form ----
+
+# two from 16384 waves' worth of lanes on (RN lanes hold a channel); the odd batch is left alone
+# in its lane
+STEP = [
+    (129, 2, 2050, 16, 2, "bf16", True, True, True, "softplus"),
+    (129, 1, 2049, 13, 1, "fp32", False, True, True, "softplus"),      # no vector fits
+    (129, 3, 1030, 19, 1, "bf16", True, True, False, "given"),
+    (130, 1, 1024, 32, 1, "fp32", True, True, True, "clamped"),
+    (131, 1, 520, 64, 2, "fp32", True, False, True, "softplus"),
+]
+
+
+@pytest.mark.parametrize("case", STEP, ids=str)
+def test_token_scan_of_many_batches(case):
+    batch, D, N = case[0], case[2], case[3]
+    rn = 4 if N <= 16 else 8 if N <= 32 else 16
+    assert batch * D * rn // 64 >= 2 * 8192
+    base.test_scan_step(case)
+
+
+# ---- selective scan: chunks ----
+
+def scan_waves(batch, D, G, cw):
+    return batch * G * cdiv(D // G, cw)
+
+
+# prompts of more than 64 tokens in one chunk, from 720 waves of 64, 32 or 16 channels on
+ONE_CHUNK = [
+    (45, 133, 1030, 4, 1, "bf16", True, True, True, "softplus"),
+    (46, 97, 512, 24, 1, "fp32", True, False, True, "softplus"),
+    (46, 66, 510, 20, 2, "bf16", False, True, True, "given"),
+    (45, 70, 260, 64, 1, "fp32", False, True, False, "clamped"),
+]
+
+
+@pytest.mark.parametrize("case", ONE_CHUNK, ids=str)
+def test_prompts_in_one_chunk(case):
+    batch, L, D, N, G = case[:5]
+    assert scan_waves(batch, D, G, 64 if N <= 16 else 32 if N <= 32 else 16) >= 720 and L > 64
+    base.test_scan_fwd(case)
+
+
+# gradients in chunks of 32 tokens with more than 16 states, from 2048 waves on
+LONG_CHUNKS = [
+    (8, 263, 512, 32, 1, "bf16", True, True, True, "softplus"),
+    (8, 263, 510, 19, 2, "fp32", False, True, False, "given"),
+    (4, 263, 500, 64, 1, "fp32", True, False, True, "clamped"),
+]
+
+
+@pytest.mark.parametrize("case", LONG_CHUNKS, ids=str)
+def test_gradients_in_long_chunks(case):
+    batch, L, D, N, G = case[:5]
+    assert scan_waves(batch, D, G, 16 if N <= 32 else 8) * cdiv(L, 32) >= 2048
+    d, s, init, opt, ropt = base.scan_case(case)
+    dy = d.normal(*s["x"].shape, dtype=s["x"].dtype)
+    dfin = d.normal(batch, D, N) if init is not None else None
+    got = lib.ssd_selscan_bwd(s["x"], s["dt"], s["A"], s["B"], s["C"], s["D"], s["z"], init, dy, dfin,
+                              want_dinit=True, want_ddt_bias=True, **opt)
+    want = ref.selscan_bwd(**s, init=init, dy=dy, dfinal=dfin, **ropt)
+    a = lambda t: None if t is None else np.abs(ref.f64(t))
+    m = base.scan_mag(s)
+    m["z"] = ref.f64(s["z"])
+    mag = ref.selscan_bwd(**m, init=a(init), dy=a(dy), dfinal=a(dfin), mag=True, **ropt)
+    count = 800 + 8 * L
+    if s["z"] is not None:
+        # The slope of SiLU, f = p (1 + z (1 - p)) with p = 1 / (1 + e^-z), is zero near -1.28,
+        # where its roundings are not a part of itself: p is off by (2 |z| + 5) e of itself, which f
+        # takes times |1 + z - 2 p z| <= 1.1 + |z|, and three more operations by p (1 + |z|) e each.
+        # With |z| <= 6: 17 x 7.1 + 3 x 7 < 150 e, times |dy| and the terms of s.
+        assert m["z"].max() <= 6 and m["z"].min() >= -6
+        mag["dz"] = mag["dz"] + 150.0 / count * a(dy) * ref.selscan(**dict(m, z=None), init=a(init), **ropt)[2]
+    for k, v in got.items():
+        if v is not None:
+            within(v, want[k], count, mag[k], k)
