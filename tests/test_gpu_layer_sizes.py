@@ -1,6 +1,6 @@
 """The operators around the scan where a launch is large enough to choose its other forms: long
 runs of the convolution, several batches per lane of the token scan, one chunk for a whole prompt,
-long chunks of the gradients.  The tests repeat the launch
+long chunks of the gradients, every number of pieces of the norm.  The tests repeat the launch
 rule a case is meant for, so that one which no longer reaches its form says so."""
 import numpy as np
 import pytest
@@ -134,3 +134,30 @@ def test_gradients_in_long_chunks(case):
     for k, v in got.items():
         if v is not None:
             within(v, want[k], count, mag[k], k)
+
+
+# ---- norm: pieces per thread ----
+
+# a case of test_gpu_layer, then elements per piece, threads of a group, pieces per thread
+NORM = [
+    ((2, 5, 1500, 3, "fp32", True, 4, False), 4, 64, 2),
+    ((2, 5, 1400, 2, "fp32", True, 0, True), 4, 64, 3),
+    ((2, 5, 1000, 1, "fp32", True, 4, False), 4, 64, 4),
+    ((1, 3, 2052, 1, "fp32", True, 4, False), 4, 192, 3),
+    ((2, 5, 303, 3, "bf16", True, 1, False), 1, 64, 2),
+    ((2, 5, 300, 2, "bf16", True, 0, True), 1, 64, 3),
+    ((2, 5, 233, 1, "fp32", True, 3, False), 1, 64, 4),
+    ((1, 3, 2049, 1, "bf16", True, 0, False), 1, 576, 4),
+    ((2, 3, 2010, 2, "bf16", True, 0, False), 1, 256, 4),
+]
+
+
+@pytest.mark.parametrize("case,V,threads,pieces", NORM, ids=str)
+def test_norm_pieces(case, V, threads, pieces):
+    S = case[2] // case[3]
+    n = cdiv(S, V)
+    wide = 8 if V == 1 and n > 4096 else 2 if V == 8 else 4
+    assert S % 8 != 0 or V == 4
+    assert n > 64 and cdiv(n, 64 * wide) * 64 == threads and cdiv(n, threads) == pieces
+    base.test_norm_fwd(case)
+    base.test_norm_bwd(case)
