@@ -15,8 +15,8 @@
 // window of W - 1 rows in registers, so each row is loaded once per run plus W - 1
 // rows of overlap.  Four channels a thread keep enough waves in flight (eight: 87 us
 // against 80 forwards, 102 against 86 backwards).  bf16, width 4: 2 x 8192 tokens of
-// 5376 channels 74 us forwards (4.8 TB/s of the 5.15 that a large copy reaches; runs of
-// 16 tokens, of 8 and 64 tokens 3 us more), 2 x 4096 tokens 66 us backwards (4.0 TB/s;
+// 5376 channels 75 us forwards (4.7 TB/s of the 5.15 that a large copy reaches; runs of
+// 16 tokens, of 8 and 64 tokens 3 us more), 2 x 4096 tokens 65 us backwards (4.1 TB/s;
 // the part sums take 5 of them).  Both have a path without conditions for the rows
 // inside a run: with them 78 and 72 us.
 #include <type_traits>

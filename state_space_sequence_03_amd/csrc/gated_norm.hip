@@ -17,9 +17,9 @@
 // is read once: TG threads hold a group, NV pieces of V elements each (TG at most one
 // wave where a group fits one, so that no barrier is needed and small groups share
 // a wave; otherwise as many waves as the group fills).  The backward pass sums
-// mean(u^2) and mean(t u) = mean(t n) / r in one reduction: neither needs the other.  bf16: 2 x 8192
-// rows of 5120 channels 106 us forwards (4.7 TB/s of the 5.15 that a large copy
-// reaches), 2 x 4096 rows of 8 x 512 channels 75 us backwards (4.5 TB/s; the part
+// mean(u^2) and mean(t u) = mean(t n) / r in one reduction: neither needs the other.
+// bf16: 2 x 8192 rows of 5120 channels 107 us forwards (4.7 TB/s of the 5.15 that a large
+// copy reaches), 2 x 4096 rows of 8 x 512 channels 76 us backwards (4.4 TB/s; the part
 // sums take 6 of them).
 #include "layer_device.hpp"
 #include "layer_host.hpp"

@@ -461,8 +461,8 @@ selscan_step_kernel(float* __restrict__ state, const T* __restrict__ x, const T*
 // Chunks of the forward pass.  One where its waves nearly fill the chip (1024 tokens
 // of 5120 channels: for 8 batches, 640 waves, chunks take 306 us and one chunk 334, for
 // 10 batches 399 and 340); otherwise as many as give about two waves per SIMD
-// (2048 tokens of 5120 channels x 16 states: 25 chunks 101 us, 12 a quarter more, 38
-// chunks 108, 50 chunks 122: more chunks cost more starts and longer chains), of at
+// (2048 tokens of 5120 channels x 16 states: 24 chunks 98 us, 12 chunks 110, 37 chunks
+// 103, 43 chunks 118: more chunks cost more starts and longer chains), of at
 // least 16 tokens (300 tokens of 2560 channels: at least 16 28 us, 32 35, 64 54), and
 // 64 to 128 of them at most (64 channels: 8192 tokens in 128 chunks 80 us, in 64 95;
 // 2048 tokens 56 and 44).

@@ -21,9 +21,8 @@
 // (64 elements a lane), 860 of them the sums above, the rest the step sizes, the
 // sums across lanes and the broadcasts; counters show the vector ALU busy 75% of
 // the time.  2 x 2048 tokens x 5120 channels x 16 states, bf16 with gate: 423 us in
-// all, 320 of them here, 131 in selscan_kernel<both>, 20 in the chains and 9 in
-// the last sums (kernel trace; the parts run at lower clocks there than the
-// whole).  Walking each chunk forwards once more in place of the checkpoints took
+// all, 276 of them here, 119 in selscan_kernel<both>, 19 in the chains and 9 in
+// the last sums (kernel trace).  Walking each chunk forwards once more in place of the checkpoints took
 // the same 472 us when both were measured, and 81 against 69 us for 2 x 515 x 770
 // channels in fp32.
 //
