@@ -119,4 +119,29 @@ __device__ __forceinline__ float column_sum(const float* p, int64_t n, int64_t l
   return (float)v;
 }
 
+// Sums of K values over the TG threads of a group, in every one of them: shuffles
+// inside a wave (TG a power of two up to a wave, or whole waves), then the waves'
+// sums through LDS.
+template <int K>
+__device__ __forceinline__ void group_sum(float (&v)[K], int tg, float* lds) {
+  const int in_wave = tg < kWave ? tg : kWave;
+  for (int off = in_wave / 2; off >= 1; off >>= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] += __shfl_xor(v[k], off, kWave);
+  if (tg > kWave) {
+    const int waves = tg / kWave, wave = threadIdx.x / kWave;
+    __syncthreads();   // the last row's sums have been read
+    if (threadIdx.x % kWave == 0)
+#pragma unroll
+      for (int k = 0; k < K; ++k) lds[wave * K + k] = v[k];
+    __syncthreads();
+    const int first = wave / waves * waves;
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = 0.0f;
+    for (int q = 0; q < waves; ++q)
+#pragma unroll
+      for (int k = 0; k < K; ++k) v[k] += lds[(first + q) * K + k];
+  }
+}
+
 }  // namespace ssd
