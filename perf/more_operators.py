@@ -199,6 +199,7 @@ def _own(s):
         return {"q": y8.q, "scale": y8.scale}
     if op == "quant8":
         rows, cols = ssd.ssd_quant8(s["x"], tile=s["tile"], want_rows=s["rows"], want_cols=s["cols"])
+        rows = (rows.q.flatten(0, -2), rows.scale) if rows else None
         return {"rows": list(rows) if rows else None, "cols": list(cols) if cols else None}
     if op == "matmul8":
         return ssd.ssd_matmul8(ssd.Tensor8(s["x"], s["xs"]), ssd.Tensor8(s["w"], s["ws"]), out_dtype=_DTYPES[s["out"]])
