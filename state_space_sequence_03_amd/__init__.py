@@ -17,7 +17,9 @@ Names match the C ABI in include/ssd.h:
     ssd_last_error_message, ssd_abi_version
 (ssd_fwd_config is reached through ssd_fwd(..., config=...).)  The operators
 around the scan (include/ssd_layer.h: ssd_conv_*, ssd_selscan_*,
-ssd_gated_norm_*) are in layer.py and exported here too.
+ssd_gated_norm_*) are in layer.py, those around a layer (include/ssd_block.h:
+ssd_add_norm_*, ssd_gated_norm_fwd_8bit, ssd_quant8, ssd_matmul8, ssd_clip_grads) in
+block.py, and exported here too.
 """
 from __future__ import annotations
 
@@ -159,6 +161,7 @@ def load_library():
         lib.ssd_bwd.restype = ctypes.c_int
         lib.ssd_bwd.argtypes = [P, X] + [vp] * 18 + [sz, vp]
         layer.declare(lib, ssd_dt_transform)
+        block.declare(lib)
         _lib = lib
         return lib
 
@@ -591,3 +594,9 @@ from . import layer  # noqa: E402
 from .layer import *  # noqa: E402,F401,F403
 
 __all__ += layer.__all__
+
+# The operators of a residual block and of its training step (include/ssd_block.h).
+from . import block  # noqa: E402
+from .block import *  # noqa: E402,F401,F403
+
+__all__ += block.__all__

@@ -20,7 +20,8 @@ LIB_PATH = os.path.join(HERE, "libssd.so")
 
 SOURCES = ["chunk_cumsum.hip", "chunk_state.hip", "state_pass.hip", "compute_out.hip", "step.hip",
            "bwd.hip", "fused_fwd.hip", "noalloc.hip", "out_resident.hip", "conv.hip",
-           "gated_norm.hip", "selscan.hip", "selscan_bwd.hip", "ssd_api.cpp", "layer_api.cpp"]
+           "gated_norm.hip", "selscan.hip", "selscan_bwd.hip", "add_norm.hip", "quant8.hip", "matmul8.hip",
+           "clip.hip", "ssd_api.cpp", "layer_api.cpp", "block_api.cpp"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -1,0 +1,123 @@
+// block_device.hpp -- what the kernels of a residual block share: eight elements at
+// any alignment, 8-bit values with their block's scale.
+#pragma once
+#include "layer_device.hpp"
+
+namespace ssd {
+
+constexpr int kBlock8 = 128;   // elements of one scale
+constexpr float kMost8 = 448.0f;                    // the largest e4m3 value
+constexpr float kLeast8 = 7.888609052210118e-31f;   // 2^-100: a block's least magnitude, so that 448 / it is finite
+
+// Eight elements, aligned to one of them only: a slice may start anywhere, and rows of
+// an odd width do.  The memory system takes such accesses whole.
+typedef bf16 bf16x8_any __attribute__((ext_vector_type(8), aligned(2)));
+typedef float floatx4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+// The first `n` of the eight elements at p (all of them where n >= 8), zeros behind them.
+__device__ __forceinline__ void load8(const bf16* p, int n, float (&v)[8]) {
+  if (n >= 8) {
+    const bf16x8_any w = *reinterpret_cast<const bf16x8_any*>(p);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = static_cast<float>(w[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < n ? static_cast<float>(p[e]) : 0.0f;
+  }
+}
+__device__ __forceinline__ void load8(const float* p, int n, float (&v)[8]) {
+  if (n >= 8) {
+    const floatx4_any a = *reinterpret_cast<const floatx4_any*>(p);
+    const floatx4_any b = *reinterpret_cast<const floatx4_any*>(p + 4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = a[e];
+      v[4 + e] = b[e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < n ? p[e] : 0.0f;
+  }
+}
+__device__ __forceinline__ void store8(bf16* p, int n, const float (&v)[8]) {
+  if (n >= 8) {
+    bf16x8_any w;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = static_cast<bf16>(v[e]);
+    *reinterpret_cast<bf16x8_any*>(p) = w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) p[e] = static_cast<bf16>(v[e]);
+  }
+}
+__device__ __forceinline__ void store8(float* p, int n, const float (&v)[8]) {
+  if (n >= 8) {
+    floatx4_any a, b;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      a[e] = v[e];
+      b[e] = v[4 + e];
+    }
+    *reinterpret_cast<floatx4_any*>(p) = a;
+    *reinterpret_cast<floatx4_any*>(p + 4) = b;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e < n) p[e] = v[e];
+  }
+}
+
+// The offset of a row of a strided operand; fewer than 2^31 rows.
+__device__ __forceinline__ int64_t row_at(const Strides& s, int64_t row, int64_t L) {
+  const uint32_t b = (uint32_t)row / (uint32_t)L;
+  return (int64_t)b * s.batch + (int64_t)((uint32_t)row - b * (uint32_t)L) * s.token;
+}
+
+// max |v|, leaving NaN out (fmaxf takes the other operand).
+__device__ __forceinline__ float most_of(const float (&v)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+  return m;
+}
+// The largest over the lanes that share `lane / 16`, in all of them: a block of 128 in
+// pieces of eight.
+__device__ __forceinline__ float most_of_16(float m) {
+#pragma unroll
+  for (int off = 8; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 16));
+  return m;
+}
+
+// Eight values times `by` as e4m3, to nearest even: v 448 / m is at most 448 (1 + 2^-23),
+// which rounds to 448, so nothing has to be cut off.  The products are formed in 64 bits and
+// rounded to fp32 in front of the conversion, so a value falls on the wrong side of the middle
+// between two e4m3 values only within half a step of fp32 of it; 64-bit operations run at the
+// rate of fp32 ones here, and the kernels wait for memory.
+__device__ __forceinline__ uint2 pack8(const double (&v)[8], double by) {
+  uint2 r;
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32((float)(v[0] * by), (float)(v[1] * by), 0, false);
+  r.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32((float)(v[2] * by), (float)(v[3] * by), w, true);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32((float)(v[4] * by), (float)(v[5] * by), 0, false);
+  r.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32((float)(v[6] * by), (float)(v[7] * by), w, true);
+  return r;
+}
+__device__ __forceinline__ uint2 pack8(const float (&v)[8], double by) {
+  double d[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) d[e] = (double)v[e];
+  return pack8(d, by);
+}
+__device__ __forceinline__ double most_of(const double (&v)[8]) {
+  double m = 0.0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = fmax(m, fabs(v[e]));
+  return m;
+}
+__device__ __forceinline__ double most_of_16(double m) {
+#pragma unroll
+  for (int off = 8; off >= 1; off >>= 1) m = fmax(m, __shfl_xor(m, off, 16));
+  return m;
+}
+
+}  // namespace ssd

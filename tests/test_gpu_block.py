@@ -1,0 +1,570 @@
+"""The operators of a residual block against their fp64 references (oracle/block.py), with the
+bounds derived in block_util.py and layer_util.py, and how they are used: a block of a model
+forwards, token by token and backwards, on other streams, in captured graphs."""
+import numpy as np
+import pytest
+import torch
+
+import state_space_sequence_03_amd as lib
+from block_util import ROUGH, in8, matmul_count
+from layer_util import IO, Draw, within
+from oracle import block as ref
+
+pytestmark = pytest.mark.gpu
+f = ref.f64
+
+
+@pytest.fixture(autouse=True)
+def _announce(request, gpu_available):
+    if not gpu_available:
+        pytest.skip("needs a GPU")
+    print("\n[gpu-case] %s" % request.node.name, flush=True)
+    yield
+    torch.cuda.synchronize()
+
+
+def flat(t):
+    return t.reshape(-1, t.shape[-1])
+
+
+# ---- residual and norm ----
+
+# batch, tokens, channels, pad in front of x's rows, io, residual
+NORM = [
+    (1, 1, 1, 0, "bf16", "fp32"), (1, 1, 128, 0, "fp32", "fp32"), (2, 3, 7, 1, "bf16", "bf16"),
+    (1, 5, 129, 3, "bf16", "fp32"), (3, 1, 256, 8, "bf16", None), (2, 2, 257, 0, "fp32", None),
+    (1, 9, 512, 0, "bf16", "bf16"), (4, 3, 777, 5, "fp32", "fp32"), (1, 2, 2560, 0, "bf16", "fp32"),
+    (2, 600, 520, 16, "bf16", "fp32"), (1, 1100, 1111, 0, "bf16", "bf16"), (1, 3, 4097, 0, "fp32", "fp32"),
+    (1, 1030, 2000, 0, "bf16", "fp32"), (1, 1, 8192, 0, "bf16", "fp32"), (1, 1025, 8191, 1, "bf16", "bf16"),
+]
+
+
+def norm_case(case, seed=0):
+    Bz, L, C, pad, io, res = case
+    d = Draw(seed)
+    x = d.rows(Bz, L, C, pad=pad, dtype=IO[io])
+    r = d.normal(Bz, L, C, dtype=IO[res], std=3.0) if res else None
+    return d, x, r, d.normal(C, std=0.3) + 1.0
+
+
+def stored(x, r):
+    """h as it is stored: the sum rounded once to the residual's type."""
+    return x.clone() if r is None else (x.double() + r.double()).to(torch.float32).to(r.dtype)
+
+
+@pytest.mark.parametrize("case", NORM, ids=str)
+def test_add_norm_fwd(case):
+    d, x, r, w = norm_case(case)
+    y, y8, h = lib.ssd_add_norm_fwd(x, r, w, want_8bit=True)
+    want = stored(x, r)
+    assert torch.equal(h, want)
+    yr = ref.norm(h, w)
+    within(y, yr, 100, np.abs(yr), "y")
+    scaled, scale, m = ref.blocks(flat(yr))
+    assert y8.q.shape == x.shape[:2] + (scaled.shape[1],)
+    in8(y8.q, scaled, 2, "q")
+    within(y8.scale, scale, 100, scale, "scale")
+    # each output alone, a new h or none, the residual updated in place
+    assert torch.equal(lib.ssd_add_norm_fwd(x, r, w, want_h=False)[0], y)
+    none, q2, _ = lib.ssd_add_norm_fwd(x, r, w, want_y=False, want_8bit=True)
+    assert none is None and torch.equal(q2.q.view(torch.uint8), y8.q.view(torch.uint8)) and torch.equal(q2.scale, y8.scale)
+    if r is not None:
+        r2 = r.clone()
+        y2, _, h2 = lib.ssd_add_norm_fwd(x, r2, w, h_out=r2)
+        assert h2 is r2 and torch.equal(r2, want) and torch.equal(y2, y)
+    elif x.dtype == torch.bfloat16:   # a stream that begins here in fp32
+        _, _, h32 = lib.ssd_add_norm_fwd(x, None, w, residual_dtype=torch.float32)
+        assert h32.dtype == torch.float32 and torch.equal(h32, x.float())
+
+
+@pytest.mark.parametrize("case", NORM, ids=str)
+@pytest.mark.parametrize("up", [False, True])
+def test_add_norm_bwd(case, up):
+    Bz, L, C, _, io, res = case
+    d, x, r, w = norm_case(case, 1)
+    h = stored(x, r).contiguous()
+    dy = d.normal(Bz, L, C, dtype=IO[io])
+    dh = d.normal(Bz, L, C, dtype=h.dtype) if up else None
+    got = lib.ssd_add_norm_bwd(h, w, dy, dh)
+    want, dw, mag, dwmag = ref.norm_bwd(h, w, dy, dh)
+    within(got["dx"], want, 200, mag, "dx")
+    within(got["dresidual"], want, 200, mag, "dresidual")
+    within(got["dweight"], dw, 400, dwmag, "dweight")
+    assert got["dx"].dtype == dy.dtype and got["dresidual"].dtype == h.dtype
+    one = lib.ssd_add_norm_bwd(h, w, dy, dh, want_dresidual=False)
+    assert one["dresidual"] is None and torch.equal(one["dx"], got["dx"]) and torch.equal(one["dweight"], got["dweight"])
+    if up:   # dh updated in place
+        keep = dh.clone()
+        two = lib.ssd_add_norm_bwd(h, w, dy, keep, want_dx=False, dresidual_out=keep)
+        assert two["dx"] is None and torch.equal(keep, got["dresidual"])
+
+
+def test_add_norm_gradients_against_differences():
+    # the library's own forward pass in fp32: a difference over 2 s carries 100 e |y| / s of rounding
+    # and s^2 of curvature; with s = 2^-7, sums of 2 x 40 outputs and their slopes within 2%
+    d = Draw(5)
+    x, r, w = d.normal(1, 2, 40), d.normal(1, 2, 40), d.normal(40, std=0.3) + 1.0
+    dy, dh = d.normal(1, 2, 40), d.normal(1, 2, 40)
+    got = lib.ssd_add_norm_bwd((x + r).contiguous(), w, dy, dh)
+
+    def loss(x, w):
+        y, _, h = lib.ssd_add_norm_fwd(x, r, w)
+        return float((y.double() * dy.double()).sum() + (h.double() * dh.double()).sum())
+
+    s = 2.0 ** -7
+    for k in (0, 7, 39):
+        bump = torch.zeros_like(x)
+        bump[0, 1, k] = s
+        num = (loss(x + bump, w) - loss(x - bump, w)) / (2 * s)
+        assert abs(num - float(got["dx"][0, 1, k])) < 0.02 * max(1.0, abs(num))
+        bw = torch.zeros_like(w)
+        bw[k] = s
+        num = (loss(x, w + bw) - loss(x, w - bw)) / (2 * s)
+        assert abs(num - float(got["dweight"][k])) < 0.02 * max(1.0, abs(num))
+
+
+# batch, tokens, channels, groups, pad, io, gate behind the norm, gate given
+GATED = [
+    (1, 1, 5, 1, 0, "bf16", False, True), (2, 3, 130, 1, 1, "bf16", True, True), (1, 4, 256, 2, 8, "fp32", False, True),
+    (3, 2, 1024, 8, 24, "bf16", True, True), (1, 7, 1111, 1, 0, "fp32", False, True), (2, 5, 384, 3, 0, "bf16", False, False),
+    (1, 1030, 5120, 1, 5456, "bf16", False, True), (2, 520, 4096, 2, 3, "bf16", False, True), (1, 2, 16384, 2, 0, "bf16", True, True),
+]
+
+
+@pytest.mark.parametrize("case", GATED, ids=str)
+def test_gated_norm_8bit(case):
+    Bz, L, C, G, pad, io, before, gate = case
+    d = Draw(2)
+    x, w = d.normal(Bz, L, C, dtype=IO[io]), d.normal(C, std=0.3) + 1.0
+    z = d.rows(Bz, L, C, pad=pad, dtype=IO[io]) if gate else None
+    y8 = lib.ssd_gated_norm_fwd_8bit(x, z, w, ngroups=G, norm_before_gate=before)
+    yr = ref.gated(x, z, w, G, before=before)
+    scaled, scale, _ = ref.blocks(flat(yr))
+    in8(y8.q, scaled, 100, "q")
+    within(y8.scale, scale, 100, scale, "scale")
+
+
+# ---- quantising ----
+
+# batch, tokens, channels, pad, io
+QUANT = [(1, 1, 1, 0, "bf16"), (1, 1, 128, 0, "fp32"), (2, 3, 127, 1, "bf16"), (1, 128, 129, 0, "fp32"), (3, 50, 260, 8, "bf16"),
+         (1, 129, 128, 3, "bf16"), (2, 200, 131, 0, "fp32"), (1, 300, 1000, 0, "bf16")]
+
+
+@pytest.mark.parametrize("tile", [False, True])
+@pytest.mark.parametrize("case", QUANT, ids=str)
+def test_quant8(case, tile):
+    Bz, L, C, pad, io = case
+    d = Draw(3)
+    x = d.rows(Bz, L, C, pad=pad, dtype=IO[io])
+    x = (x * torch.exp2(d.normal(Bz, L, 1, std=3.0).to(x.dtype))).to(x.dtype) if pad == 0 else x
+    rows, cols = lib.ssd_quant8(x, tile=tile, want_cols=True)
+    v, down = flat(f(x)), 128 if tile else 1
+    for name, got, m in (("rows", rows, v), ("cols", cols, v.T)):
+        scaled, scale, _ = ref.blocks(m, down)
+        assert got.q.shape == (x.shape[:2] if name == "rows" else (C,)) + (scaled.shape[1],)
+        in8(got.q, scaled, 1, name)
+        within(got.scale, scale, 0, scale, name + " scale")
+    bits = lambda t: t.q.view(torch.uint8)
+    alone, none = lib.ssd_quant8(x, tile=tile)
+    assert none is None and torch.equal(bits(alone), bits(rows)) and torch.equal(alone.scale, rows.scale)
+    none, alone = lib.ssd_quant8(x, tile=tile, want_rows=False, want_cols=True)
+    assert none is None and torch.equal(bits(alone), bits(cols)) and torch.equal(alone.scale, cols.scale)
+    if Bz == 1:
+        two, _ = lib.ssd_quant8(x[0], tile=tile)
+        assert two.q.shape == rows.q.shape[1:] and torch.equal(bits(two)[None], bits(rows))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quant8_extremes(dtype):
+    x = torch.zeros(6, 256, dtype=dtype, device="cuda")
+    x[1, :128] = torch.tensor([2.0 ** -126, -(2.0 ** -120)] * 64)       # below the least magnitude
+    x[2, 0], x[2, 1] = torch.finfo(dtype).max, -1.0
+    x[3, 5], x[3, 6] = float("nan"), 3.0
+    x[4, 130], x[4, 131] = float("inf"), 3.0
+    x[5] = torch.linspace(-448, 448, 256)
+    rows, cols = lib.ssd_quant8(x, want_cols=True)
+    q, s = rows.q.double().cpu(), rows.scale.double().cpu()
+    assert (q[0] == 0).all() and (s[:, 0] == np.float32(2.0 ** -100 / 448)).all()
+    assert (q[1] == 0).all() and s[0, 1] == np.float32(2.0 ** -100 / 448)     # 2^-120 448 / 2^-100 is below half of 2^-9
+    assert q[2, 0] == 448 and q[2, 1] == 0 and abs(s[0, 2] * 448 / torch.finfo(dtype).max - 1) < 1e-6
+    assert torch.isnan(q[3, 5]) and q[3, 6] == 448 and abs(s[0, 3] - 3 / 448) < 1e-9
+    assert s[1, 4] == float("inf") and torch.isnan(q[4, 130]) and q[4, 131] == 0 and s[0, 4] == s[0, 0]
+    in8(rows.q[5], ref.blocks(x[5:6])[0][0], 1, "ramp")
+    assert torch.isnan(cols.q.double()[5, 3]) and torch.isnan(cols.q.double()[130, 4])
+
+
+# ---- matrix product ----
+
+# rows, cols, depth
+PRODUCT = [(1, 1, 128), (1, 130, 256), (3, 31, 384), (16, 33, 1152), (17, 257, 128), (63, 128, 2176), (64, 129, 640),
+           (65, 32, 1280), (128, 300, 2560), (129, 384, 256), (200, 10, 4096), (257, 513, 384), (300, 1000, 1024), (513, 260, 128),
+           (1000, 770, 2176), (1024, 1024, 512), (640, 2563, 256), (2, 2000, 5120)]
+
+
+def operands(rows, cols, depth, tile, seed=0):
+    d = Draw(seed)
+    x = d.normal(rows, depth) * torch.exp2(d.normal(rows, 1, std=2.0))
+    w = d.normal(cols, depth, std=depth ** -0.5) * torch.exp2(d.normal(cols, 1, std=0.0 if tile else 2.0))
+    return lib.ssd_quant8(x)[0], lib.ssd_quant8(w, tile=tile)[0]
+
+
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("tile", [True, False])
+@pytest.mark.parametrize("size", PRODUCT, ids=str)
+def test_matmul8(size, tile, out):
+    x, w = operands(*size, tile)
+    y = lib.ssd_matmul8(x, w, out_dtype=IO[out])
+    want, mag = ref.matmul(x.q, x.scale, w.q, w.scale, tile)
+    within(y, want, ROUGH if out == "bf16" else matmul_count(size[2]), mag, "y")
+    assert torch.equal(y, lib.ssd_matmul8(x, w, out_dtype=IO[out]))
+
+
+def test_matmul8_special_values():
+    # a NaN reaches its row alone, zeros give zeros, and the scale of a zero block does not matter
+    x, w = operands(70, 150, 384, True)
+    q = x.q.view(torch.uint8).clone()
+    q[3, 200] = 0x7F
+    q[5] = 0
+    xs = x.scale.clone()
+    xs[:, 5] = 1e30
+    for dt in (torch.bfloat16, torch.float32):
+        y = lib.ssd_matmul8(lib.Tensor8(q.view(torch.float8_e4m3fn), xs), w, out_dtype=dt)
+        clean = lib.ssd_matmul8(x, w, out_dtype=dt)
+        assert torch.isnan(y[3]).all() and (y[5] == 0).all()
+        keep = [i for i in range(70) if i not in (3, 5)]
+        assert torch.equal(y[keep], clean[keep])
+
+
+def test_matmul8_leaves_the_rest_alone():
+    x, w = operands(33, 45, 256, True)
+    for dt in (torch.bfloat16, torch.float32):
+        room = torch.full((33 * 45 + 4096,), 7.0, dtype=dt, device="cuda")
+        out = room[:33 * 45].view(33, 45)
+        lib.ssd_matmul8(x, w, out_dtype=dt, out=out)
+        assert (room[33 * 45:] == 7.0).all() and torch.equal(out, lib.ssd_matmul8(x, w, out_dtype=dt))
+
+
+# ---- clipping ----
+
+def gradients(d, sizes, dtypes):
+    return [d.normal(*((n,) if isinstance(n, int) else n), dtype=IO[t]) for n, t in zip(sizes, dtypes)]
+
+
+CLIP = [
+    ([1], ["fp32"]), ([5, 0, 3], ["bf16", "fp32", "fp32"]), ([(3, 7), 8191, (2, 4096), 8193], ["bf16", "fp32", "bf16", "fp32"]),
+    ([17] * 300, ["bf16", "fp32"] * 150), ([3_000_001, 1, 70_000], ["bf16", "bf16", "fp32"]), ([0, 0], ["fp32", "bf16"]),
+    ([8192] * 1100, ["fp32"] * 1100),
+]
+
+
+@pytest.mark.parametrize("most,scale", [(1.0, 1.0), (1e9, 0.25), (float("inf"), 1.0)])
+@pytest.mark.parametrize("sizes,dtypes", CLIP, ids=lambda v: str(v)[:20])
+def test_clip_grads(sizes, dtypes, most, scale):
+    d = Draw(6)
+    g = gradients(d, sizes, dtypes)
+    size, want = ref.clip(g, most, scale)
+    outs = [torch.full_like(t, 9.0, dtype=torch.float32 if i % 2 else t.dtype) for i, t in enumerate(g)]
+    keep = [t.clone() for t in g]
+    norm = lib.ssd_clip_grads(g, most, scale=scale, out=outs)
+    assert norm.shape == () and norm.dtype == torch.float32
+    within(norm, size, 0, size, "norm")
+    assert all(torch.equal(a, b) for a, b in zip(g, keep))
+    for dt in (torch.float32, torch.bfloat16):
+        k = [i for i, o in enumerate(outs) if o.dtype == dt and o.numel()]
+        if k:
+            within(torch.cat([outs[i].reshape(-1) for i in k]), np.concatenate([want[i].reshape(-1) for i in k]), 2,
+                   np.concatenate([np.abs(want[i].reshape(-1)) for i in k]), "out")
+    # in place: the same as into tensors of the same type
+    same = [torch.empty_like(t) for t in g]
+    lib.ssd_clip_grads(g, most, scale=scale, out=same)
+    again = lib.ssd_clip_grads(g, most, scale=scale)
+    assert torch.equal(again, norm) and all(torch.equal(a, b) for a, b in zip(g, same))
+    if scale == 1.0 and most > size:
+        assert all(torch.equal(a, b) for a, b in zip(g, keep))
+
+
+def test_clip_grads_views_and_offsets():
+    # gradients and outputs packed without room between, at odd elements
+    d = Draw(7)
+    n = [13, 1, 700, 9001]
+    flat_in, flat_out = d.normal(sum(n) + 1, dtype=torch.bfloat16), torch.full((sum(n) + 9,), 5.0, device="cuda")
+    at = np.cumsum([1] + n)
+    g = [flat_in[a:a + k] for a, k in zip(at, n)]
+    o = [flat_out[a + 2:a + 2 + k] for a, k in zip(at, n)]
+    size, want = ref.clip(g, 2.0)
+    norm = lib.ssd_clip_grads(g, 2.0, out=o)
+    within(norm, size, 0, size, "norm")
+    within(flat_out[3:3 + sum(n)], np.concatenate(want), 2, np.abs(np.concatenate(want)), "out")
+    assert (flat_out[:3] == 5.0).all() and (flat_out[3 + sum(n):] == 5.0).all()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), 1e30])
+def test_clip_grads_not_finite(bad):
+    d = Draw(8)
+    g = gradients(d, [1000, 20], ["fp32", "bf16"])
+    g[0][37] = bad
+    keep = [t.clone() for t in g]
+    norm = lib.ssd_clip_grads(g, 1.0)
+    if bad == 1e30:   # its square is past fp32, the norm is not
+        assert abs(float(norm) / 1e30 - 1) < 1e-6 and abs(float(g[0][37]) - 1.0) < 1e-6
+    else:
+        assert not torch.isfinite(norm)
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(g, keep))
+
+
+# ---- together ----
+
+class Block:
+    """A second-generation block of a small model in 8 bits."""
+    heads, dim, state, width = 4, 32, 16, 4
+
+    def __init__(self, d, model=96):
+        self.model, self.inner = model, self.heads * self.dim
+        self.conv = self.inner + 2 * self.state
+        self.proj = 2 * self.inner + 2 * self.state + self.heads
+        self.w_in, self.w_out = d.normal(self.proj, model, std=model ** -0.5), d.normal(model, self.inner, std=self.inner ** -0.5)
+        self.in8, self.in8t = lib.ssd_quant8(self.w_in, tile=True, want_cols=True)
+        self.out8, self.out8t = lib.ssd_quant8(self.w_out, tile=True, want_cols=True)
+        self.cw, self.cb = d.normal(self.conv, self.width, std=0.5), d.normal(self.conv, std=0.1)
+        self.norm, self.gnorm = d.normal(model, std=0.1) + 1.0, d.normal(self.inner, std=0.1) + 1.0
+        self.A, self.D, self.bias = -d.uniform(0.5, 2.0, self.heads), d.normal(self.heads), d.normal(self.heads, std=0.3)
+
+    def parts(self, proj):
+        z, xbc, dt = proj.split((self.inner, self.conv, self.heads), 2)
+        return z, xbc, dt.float().contiguous()
+
+    def run(self, x, residual, states=None):
+        """(output, new residual); states advance in place where they are given."""
+        _, a8, h = lib.ssd_add_norm_fwd(x, residual, self.norm, want_y=False, want_8bit=True)
+        z, xbc, dt = self.parts(lib.ssd_matmul8(a8, self.in8, out_dtype=x.dtype))
+        split = (self.inner, self.state, self.state)
+        if states is None:
+            (u, B, C), _ = lib.ssd_conv_fwd(xbc, self.cw, self.cb, split=split)
+        else:
+            u, B, C = lib.ssd_conv_step(states[0], xbc, self.cw, self.cb, split=split)
+        heads = lambda t, n: t.unflatten(2, (n, -1))
+        args = (heads(u, self.heads), dt, self.A, heads(B, 1), heads(C, 1), self.D)
+        more = dict(dt_bias=self.bias, dt_softplus=True)
+        if states is None:
+            y, _ = lib.ssd_fwd(*args, 32, **more)
+        else:
+            y = lib.ssd_step(states[1], *args, **more)
+        self.last8 = lib.ssd_gated_norm_fwd_8bit(y.flatten(2), z, self.gnorm)
+        return lib.ssd_matmul8(self.last8, self.out8, out_dtype=x.dtype), h
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+def test_a_block_as_prompt_and_token_by_token(io):
+    d = Draw(10)
+    block = Block(d)
+    Bz, L = 2, 9
+    x = d.normal(Bz, L, block.model, dtype=io)
+    res = d.normal(Bz, L, block.model)
+    out, h = block.run(x, res)
+    # stage by stage in 64 bits, each from what the library left of the one before
+    assert torch.equal(h, x.float() + res)
+    _, a8, _ = lib.ssd_add_norm_fwd(x, res, block.norm, want_8bit=True)
+    p = lib.ssd_matmul8(a8, block.in8, out_dtype=io)
+    want, mag = ref.matmul(flat(a8.q), a8.scale, block.in8.q, block.in8.scale, True)
+    within(flat(p), want, ROUGH if io == torch.bfloat16 else matmul_count(128), mag, "projection")
+    # what 8 bits cost against the same product without them: each factor is off by at most half a step
+    # (or, below its normal range, 2^-10 of a scale that is at most the largest magnitude / 448)
+    full, w = ref.norm(h, block.norm), f(block.w_in)
+    err = lambda v, down: np.maximum(2.0 ** -4 * np.abs(v), 2.0 ** -10 * ref.blocks(v, down)[2][:, :v.shape[1]] / 448.0)
+    ea, ew = err(flat(full), 1), err(w, 128)
+    room = ea @ np.abs(w).T + np.abs(flat(full)) @ ew.T + ea @ ew.T
+    off = np.abs(f(flat(p)) - flat(full) @ w.T)
+    assert (off <= 1.01 * room + 2.0 ** -7 * (np.abs(flat(full)) @ np.abs(w).T)).all()
+    # token by token: the projections agree to the bit, the scan to fp32 accuracy, so that a value
+    # next to the middle of two e4m3 values may fall the other way, by a step (2^-3 of it, or 2^-9 scales)
+    block.run(x, res)
+    y8 = block.last8
+    states = [torch.zeros(Bz, block.width - 1, block.conv, dtype=io, device="cuda"),
+              torch.zeros(Bz, block.heads, block.dim, block.state, device="cuda")]
+    steps = [block.run(x[:, t:t + 1].contiguous(), res[:, t:t + 1].contiguous(), states) for t in range(L)]
+    assert torch.equal(torch.cat([s[1] for s in steps], 1), h)
+    step = np.maximum(2.0 ** -3 * np.abs(ref.widened(flat(y8.q), y8.scale)), 2.0 ** -9 * np.repeat(f(y8.scale).T, 128, 1))
+    room = step @ np.abs(ref.widened(block.out8.q, block.out8.scale, 128)).T
+    off = np.abs(f(flat(torch.cat([s[0] for s in steps], 1))) - f(flat(out)))
+    if io == torch.float32:
+        assert (off <= 1.01 * room).all()
+    else:   # outputs and states of the scan rounded to bf16 in between: only that it runs, and lands near
+        assert np.linalg.norm(off) <= 2.0 ** -3 * np.linalg.norm(f(out))
+
+
+def test_a_projections_gradients():
+    # y = x W^T: dx = dy W from the transposed tiles, dW = dy^T x from both transposed by row
+    d = Draw(11)
+    Bz, L, n, k = 2, 65, 200, 140
+    x, dy, w = d.normal(Bz, L, k, dtype=torch.bfloat16), d.normal(Bz, L, n, dtype=torch.bfloat16), d.normal(n, k)
+    x8, x8t = lib.ssd_quant8(x, want_cols=True)
+    g8, g8t = lib.ssd_quant8(dy, want_cols=True)
+    w8, w8t = lib.ssd_quant8(w, tile=True, want_cols=True)
+    dx = lib.ssd_matmul8(g8, w8t)
+    dw = lib.ssd_matmul8(g8t, x8t, out_dtype=torch.float32)
+    assert dx.shape == x.shape and dw.shape == w.shape
+    want, mag = ref.matmul(flat(g8.q), g8.scale, w8t.q, w8t.scale, True)
+    within(flat(dx), want, ROUGH, mag, "dx")
+    want, mag = ref.matmul(g8t.q, g8t.scale, x8t.q, x8t.scale, False)
+    within(dw, want, matmul_count(256), mag, "dW")
+    # against differences of the product itself, in its 8-bit values: y is linear in them
+    wq, xq = ref.widened(w8.q, w8.scale, 128)[:, :k], ref.widened(flat(x8.q), x8.scale)[:, :k]
+    assert np.allclose(ref.widened(w8t.q, w8t.scale, 128)[:, :n], wq.T)
+    gq = ref.widened(flat(g8.q), g8.scale)[:, :n]
+    loss = lambda xv: float(((xv @ wq.T) * gq).sum())
+    bump = np.zeros_like(xq)
+    bump[7, 9] = 0.5
+    num = loss(xq + bump) - loss(xq - bump)   # over 2 x 0.5
+    assert abs(num - float(dx.reshape(-1, k)[7, 9])) <= (2.0 ** -8 + 2.0 ** -13) * float((np.abs(gq) @ np.abs(wq))[7, 9]) + 1e-9
+
+
+# ---- streams, graphs, memory ----
+
+def training_step(d, fixed):
+    """A few calls in a row on fixed buffers; returns what they leave."""
+    x, res, w, dy, dh, weight, grads = fixed
+    _, a8, h = lib.ssd_add_norm_fwd(x, res, w, want_8bit=True)
+    w8, w8t = lib.ssd_quant8(weight, tile=True, want_cols=True)
+    y = lib.ssd_matmul8(a8, w8)
+    g8, g8t = lib.ssd_quant8(dy, want_cols=True)
+    dn = lib.ssd_matmul8(g8, w8t)
+    got = lib.ssd_add_norm_bwd(h, w, dn, dh)
+    outs = [torch.empty_like(g) for g in grads]
+    norm = lib.ssd_clip_grads(grads + [got["dweight"]], 1.0, out=outs + [torch.empty_like(got["dweight"])])
+    return [y, got["dx"], got["dresidual"], got["dweight"], norm] + outs
+
+
+def step_inputs(seed):
+    d = Draw(seed)
+    Bz, L, C, n = 2, 40, 192, 300
+    return [d.normal(Bz, L, C, dtype=torch.bfloat16), d.normal(Bz, L, C), d.normal(C, std=0.1) + 1.0,
+            d.normal(Bz, L, n, dtype=torch.bfloat16), d.normal(Bz, L, C), d.normal(n, C, std=C ** -0.5),
+            [d.normal(70, 33, dtype=torch.bfloat16), d.normal(9001)]]
+
+
+def copy_into(fixed, new):
+    for a, b in zip(fixed, new):
+        if isinstance(a, list):
+            copy_into(a, b)
+        else:
+            a.copy_(b)
+
+
+def test_captured_graphs_replayed():
+    # two graphs, replayed in turn with new inputs and eager work between
+    side = torch.cuda.Stream()
+    graphs, held, kept = [], [], []
+    for k in range(2):
+        fixed = step_inputs(20 + k)
+        training_step(None, fixed)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            kept.append(training_step(None, fixed))
+        graphs.append(g)
+        held.append(fixed)
+    for turn in range(3):
+        for k in range(2):
+            copy_into(held[k], step_inputs(40 + 2 * turn + k))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for k in range(2):
+            want = training_step(None, step_inputs(40 + 2 * turn + k))
+            assert all(torch.equal(a, b) for a, b in zip(kept[k], want)), (turn, k)
+
+
+def test_another_stream_and_two_at_once():
+    want = [training_step(None, step_inputs(60 + k)) for k in range(2)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [None, None]
+    inputs = [step_inputs(60 + k) for k in range(2)]
+    torch.cuda.synchronize()
+    for k, s in enumerate(streams):
+        with torch.cuda.stream(s):
+            got[k] = training_step(None, inputs[k])
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert all(torch.equal(a, b) for a, b in zip(got[k], want[k]))
+
+
+def test_offsets_past_32_bits():
+    # rows more than 2^31 elements apart
+    far = 2 ** 31 + 8 * 1000
+    store = torch.empty(far + 64 * 320, dtype=torch.bfloat16, device="cuda")
+    d = Draw(12)
+    near, w = d.normal(2, 40, 200, dtype=torch.bfloat16), d.normal(200)
+    x = store.as_strided((2, 40, 200), (far, 256, 1))
+    x.copy_(near)
+    for a, b in zip(lib.ssd_add_norm_fwd(x, None, w), lib.ssd_add_norm_fwd(near, None, w)):
+        assert (a is None and b is None) or torch.equal(a, b)
+    for a, b in zip(lib.ssd_quant8(x, want_cols=True), lib.ssd_quant8(near, want_cols=True)):
+        assert torch.equal(a.q.view(torch.uint8), b.q.view(torch.uint8)) and torch.equal(a.scale, b.scale)
+    a, b = lib.ssd_gated_norm_fwd_8bit(near, x, w), lib.ssd_gated_norm_fwd_8bit(near, near, w)
+    assert torch.equal(a.q.view(torch.uint8), b.q.view(torch.uint8)) and torch.equal(a.scale, b.scale)
+
+
+def test_rows_repeated_by_strides():
+    d = Draw(13)
+    one, w = d.normal(1, 1, 72).expand(3, 40, 72), d.normal(72)
+    near = one.contiguous()
+    assert torch.equal(lib.ssd_add_norm_fwd(one, None, w)[0], lib.ssd_add_norm_fwd(near, None, w)[0])
+    swapped = d.normal(40, 3, 72).transpose(0, 1)      # batches inside tokens
+    assert torch.equal(lib.ssd_add_norm_fwd(swapped, None, w)[0], lib.ssd_add_norm_fwd(swapped.contiguous(), None, w)[0])
+    for t in (one, swapped):
+        for a, b in zip(lib.ssd_quant8(t, want_cols=True), lib.ssd_quant8(t.contiguous(), want_cols=True)):
+            assert torch.equal(a.q.view(torch.uint8), b.q.view(torch.uint8)) and torch.equal(a.scale, b.scale)
+
+
+# ---- refusals of the binding that need GPU tensors ----
+
+def test_binding_refuses():
+    d = Draw(14)
+    x, w, r = d.normal(2, 5, 128), d.normal(128), d.normal(2, 5, 128)
+    xb = x.bfloat16()
+    a8, t8 = lib.ssd_quant8(x)[0], lib.ssd_quant8(d.normal(300, 128), tile=True)[0]
+    bad = [
+        lambda: lib.ssd_add_norm_fwd(x, r, w[:64]), lambda: lib.ssd_add_norm_fwd(x, r[:1], w), lambda: lib.ssd_add_norm_fwd(x, r, None),
+        lambda: lib.ssd_add_norm_fwd(x, r.bfloat16(), w), lambda: lib.ssd_add_norm_fwd(x.half(), None, w),
+        lambda: lib.ssd_add_norm_fwd(x, r, w, want_y=False), lambda: lib.ssd_add_norm_fwd(x, r, w, eps=-1.0),
+        lambda: lib.ssd_add_norm_fwd(x[..., ::2], None, w[:64]), lambda: lib.ssd_add_norm_fwd(x, r, w, residual_dtype=torch.bfloat16),
+        lambda: lib.ssd_add_norm_fwd(x, r.cpu(), w), lambda: lib.ssd_add_norm_fwd(x[0], None, w),
+        lambda: lib.ssd_add_norm_fwd(x, r, w, h_out=r[:1]), lambda: lib.ssd_add_norm_fwd(x, r, w, out=xb),
+        lambda: lib.ssd_add_norm_fwd(x[:, :0], None, w), lambda: lib.ssd_add_norm_fwd(torch.zeros(1, 1, 8193, device="cuda"), None, torch.zeros(8193, device="cuda")),
+        lambda: lib.ssd_add_norm_bwd(x, w, None), lambda: lib.ssd_add_norm_bwd(x, w, xb[:1]), lambda: lib.ssd_add_norm_bwd(xb, w, x),
+        lambda: lib.ssd_add_norm_bwd(x, w, x, xb), lambda: lib.ssd_add_norm_bwd(x, w, x, want_dx=False, want_dresidual=False),
+        lambda: lib.ssd_add_norm_bwd(x, w, x, workspace=torch.empty(16, device="cuda")),
+        lambda: lib.ssd_gated_norm_fwd_8bit(x, x, w, ngroups=2), lambda: lib.ssd_gated_norm_fwd_8bit(x, xb, w),
+        lambda: lib.ssd_gated_norm_fwd_8bit(x, None, None), lambda: lib.ssd_gated_norm_fwd_8bit(x, x, w, ngroups=3),
+        lambda: lib.ssd_quant8(x.half()), lambda: lib.ssd_quant8(x, want_rows=False), lambda: lib.ssd_quant8(x[0, 0]),
+        lambda: lib.ssd_quant8(x.cpu()), lambda: lib.ssd_quant8(x[..., ::2]), lambda: lib.ssd_quant8(x[:, :0]),
+        lambda: lib.ssd_matmul8(a8, a8.q), lambda: lib.ssd_matmul8(a8, lib.Tensor8(t8.q[:, :64], t8.scale)),
+        lambda: lib.ssd_matmul8(a8, lib.Tensor8(t8.q, t8.scale[:, :2])), lambda: lib.ssd_matmul8(a8, lib.Tensor8(t8.q.float(), t8.scale)),
+        lambda: lib.ssd_matmul8(lib.Tensor8(a8.q, t8.scale), t8), lambda: lib.ssd_matmul8(a8, t8, out_dtype=torch.half),
+        lambda: lib.ssd_matmul8(a8, t8, out=torch.empty(2, 5, 300, device="cuda")), lambda: lib.ssd_matmul8(a8, lib.Tensor8(t8.q.cpu(), t8.scale)),
+        lambda: lib.ssd_clip_grads([], 1.0), lambda: lib.ssd_clip_grads([x, None], 1.0), lambda: lib.ssd_clip_grads([x], 0.0),
+        lambda: lib.ssd_clip_grads([x], float("nan")), lambda: lib.ssd_clip_grads([x], 1.0, eps=-1.0), lambda: lib.ssd_clip_grads([x], 1.0, scale=0.0),
+        lambda: lib.ssd_clip_grads([x, x], 1.0), lambda: lib.ssd_clip_grads([x, x[:1]], 1.0), lambda: lib.ssd_clip_grads([x.transpose(0, 1)], 1.0),
+        lambda: lib.ssd_clip_grads([x.half()], 1.0), lambda: lib.ssd_clip_grads([x], 1.0, out=[r[:1]]), lambda: lib.ssd_clip_grads([x], 1.0, out=[]),
+        lambda: lib.ssd_clip_grads([x, r], 1.0, out=[r, x]), lambda: lib.ssd_clip_grads([x.cpu()], 1.0),
+        lambda: lib.ssd_clip_grads([x], 1.0, workspace=torch.empty(4, dtype=torch.uint8, device="cuda")),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(lib.SsdArgumentError):
+            call()
+            print("accepted", i)
+    # one gradient read twice into outputs of their own is fine
+    o = [torch.empty_like(x), torch.empty_like(x)]
+    norm = lib.ssd_clip_grads([x, x], 1.0, out=o)
+    assert torch.equal(o[0], o[1]) and float(norm) > 0
+    torch.cuda.synchronize()
+
+
+def test_options_are_taken_by_value():
+    d = Draw(15)
+    x, w, eps = d.normal(2, 3, 16), d.normal(16), torch.tensor(0.25)
+    first = lib.ssd_add_norm_fwd(x, None, w, eps=eps)[0]
+    eps.fill_(4.0)
+    assert torch.equal(first, lib.ssd_add_norm_fwd(x, None, w, eps=0.25)[0])
+    assert torch.equal(lib.ssd_add_norm_fwd(x, None, w, eps=eps)[0], lib.ssd_add_norm_fwd(x, None, w, eps=4.0)[0])
