@@ -76,8 +76,9 @@ ssd_status matmul_shape(const ssd_matmul8_problem& p) {
   return SSD_OK;
 }
 ssd_status matmul_supported(const ssd_matmul8_problem& p) {
-  if (p.rows > kMostRows || p.cols > kMostRows || p.depth > kMostRows)
-    return fail(SSD_ERR_UNSUPPORTED, "at most 2^31 - 1 rows, columns and depth");
+  // 256 rows of a tile are reached by 32-bit offsets
+  if (p.rows > kMostRows || p.cols > kMostRows || p.depth > (1 << 23))
+    return fail(SSD_ERR_UNSUPPORTED, "at most 2^31 - 1 rows and columns, and a depth of 2^23");
   if (!matmul8_grid_ok(p.rows, p.cols)) return fail(SSD_ERR_UNSUPPORTED, "grid too large for this build");
   return SSD_OK;
 }
@@ -303,7 +304,7 @@ ssd_status ssd_matmul8_workspace_size(const ssd_matmul8_problem* prob, size_t* b
     ssd_status st = matmul_shape(*prob);
     if (st == SSD_OK) st = matmul_supported(*prob);
     if (st != SSD_OK) return st;
-    *bytes = matmul8_workspace(prob->rows, prob->cols, prob->depth);
+    *bytes = matmul8_workspace(prob->rows, prob->cols, prob->depth, prob->out_dtype == SSD_BF16);
     return ok();
   });
 }
@@ -321,7 +322,7 @@ ssd_status ssd_matmul8(const ssd_matmul8_problem* prob, const void* x, const flo
       return fail(SSD_ERR_MISALIGNED, "every tensor pointer must be 16-byte aligned");
     st = matmul_supported(p);
     if (st != SSD_OK) return st;
-    const size_t need = matmul8_workspace(p.rows, p.cols, p.depth);
+    const size_t need = matmul8_workspace(p.rows, p.cols, p.depth, p.out_dtype == SSD_BF16);
     if (need > 0 && (!workspace || workspace_bytes < need))
       return fail(SSD_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace ? workspace_bytes : size_t(0),
                   need);

@@ -312,6 +312,22 @@ __device__ __forceinline__ void dma16_so(const void* base, uint32_t off, const v
       : "memory", "m0");
 }
 
+// The 4-byte load in that form.
+__device__ __forceinline__ void dma4_so(const void* base, uint32_t off, const void* lds) {
+  const uint32_t m = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+  const uint64_t b = (uint64_t)(uintptr_t)base;
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)b);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(b >> 32));
+  const uint64_t bs = ((uint64_t)hi << 32) | (uint64_t)lo;
+  asm volatile(
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dword %0, %1"
+      :
+      : "v"(off), "s"(bs), "s"(m)
+      : "memory", "m0");
+}
+
 // Wait for this wave's loads until at most n (0..3) groups of `per` vector
 // memory operations remain outstanding (the immediate must be a constant).
 // The loads above write LDS behind the compiler's back, so after the wait a
