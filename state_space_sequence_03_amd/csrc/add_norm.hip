@@ -10,8 +10,7 @@
 // tokens of dy n;  mean(t n) = r mean(t h), so one reduction gives both sums.
 //
 // Bound by HBM: every input is read once, a token's elements stay in registers between
-// the sum and the outputs.  Pieces of eight channels, NV per thread; a token is held by
-// 16 or 32 lanes, one wave, or several.
+// the sum and the outputs, in pieces of eight channels, NV per thread.
 #include "block_device.hpp"
 #include "block_host.hpp"
 
@@ -19,87 +18,102 @@ namespace ssd {
 
 enum NormForm { kAdd = 0, kGateFirst = 1, kNormFirst = 2 };
 
-// blockDim.x / tg items (a token, or a group of one) per workgroup.
+// A workgroup takes `each` tokens in a row: blockDim.x / tg of them at a time, or, with several groups,
+// as many groups of one (blockIdx.y tells which).  The next token's elements are loaded while this one's
+// are worked on, and the weights stay in registers.
 template <typename T, typename R, int NV, int FORM>
 __global__ void __launch_bounds__(512)
 block_norm_kernel(const T* __restrict__ x, Strides xs, const R* r, Strides zs,
                   const float* __restrict__ w, R* h, T* __restrict__ y,
                   unsigned char* __restrict__ q, float* __restrict__ scale, int64_t L, int64_t rows,
-                  int C, int G, float eps, int tg) {
+                  int C, int G, float eps, int tg, int each) {
   __shared__ float lds[8];
   const int S = C / G;
-  const int per = blockDim.x / tg;
-  const int64_t item = (int64_t)blockIdx.x * per + threadIdx.x / tg;
-  const int lane = threadIdx.x % tg;
-  const bool live = item < rows * G;
-  const int64_t row = live ? item / G : 0;
-  const int c0 = live ? (int)(item % G) * S : 0;
-  const T* xp = x + row_at(xs, row, L) + c0;
-  const R* rp = r;
-  if (FORM == kAdd) {
-    if (r) rp = r + row * C;
-  } else {
-    rp = r + row_at(zs, row, L) + c0;
-  }
-  float u[NV][8], other[NV][8];
-  float sum[1] = {0.0f};
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * tg + lane) * 8;
-    const int n = live ? S - c : 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) u[i][e] = other[i][e] = 0.0f;
-    if (n > 0) {
-      load8(xp + c, n, u[i]);
-      if (FORM != kAdd || r) load8(rp + c, n, other[i]);
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * tg + lane) * 8;
-    const int n = live ? S - c : 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if constexpr (FORM == kAdd) {
-        if (r) u[i][e] = to_f32(to_io<R>(u[i][e] + other[i][e]));
-      } else {
-        other[i][e] *= sigmoid_f32(other[i][e]);
-        if (FORM == kGateFirst) u[i][e] *= other[i][e];
-      }
-      sum[0] = fmaf(u[i][e], u[i][e], sum[0]);
-    }
-    if (FORM == kAdd && h && n > 0) store8(h + row * C + c, n, u[i]);
-  }
-  group_sum(sum, tg, lds);
-  const float rr = 1.0f / sqrtf(sum[0] / (float)S + eps);
+  const int slot = threadIdx.x / tg, slots = blockDim.x / tg, lane = threadIdx.x % tg;
+  const int grp = G == 1 ? 0 : blockIdx.y * slots + slot, step = G == 1 ? slots : 1;
+  const int c0 = grp * S;
+  const int64_t first = (int64_t)blockIdx.x * each;
+  const int64_t last = grp < G ? (first + each < rows ? first + each : rows) : 0;
   const int64_t P = (int64_t)(C + kBlock8 - 1) / kBlock8 * kBlock8;
   const int padded = (S + kBlock8 - 1) / kBlock8 * kBlock8;   // S itself with several groups
+  float wt[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * tg + lane) * 8;
-    const int n = live ? S - c : 0;
-    float wt[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) wt[e] = 0.0f;
-    if (n > 0) load8(w + c0 + c, n, wt);
-    if (FORM == kAdd && y && n > 0) {
-      float o[8];
+    for (int e = 0; e < 8; ++e) wt[i][e] = 0.0f;
+    if (grp < G && c < S) load8(w + c0 + c, S - c, wt[i]);
+  }
+  Raw8<T> xn[NV];
+  Raw8<R> rn[NV];
+  auto load = [&](int64_t row) {
+    const T* xp = x + row_at(xs, row, L) + c0;
+    const R* rp = FORM != kAdd ? r + row_at(zs, row, L) + c0 : r ? r + row * C : nullptr;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = u[i][e] * rr * wt[e];
-      store8(y + row * C + c, n, o);
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tg + lane) * 8;
+      if (c < S) {
+        xn[i] = raw8(xp + c, S - c);
+        if (FORM != kAdd || r) rn[i] = raw8(rp + c, S - c);
+      }
     }
-    if (q) {
-      // y / m does not depend on r: what is quantised is y / r, and r joins the scale.
-      double t[8];
+  };
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    xn[i] = Raw8<T>{};
+    rn[i] = Raw8<R>{};
+  }
+  const int64_t mine = first + (G == 1 ? slot : 0);
+  if (mine < last) load(mine);
+  for (int k = 0; k < each; k += step) {   // as often in every thread: the sums have barriers
+    const int64_t row = mine + k;
+    const bool live = row < last;
+    float u[NV][8], gate[FORM == kAdd ? 1 : NV][8];
+    float sum[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tg + lane) * 8;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        t[e] = (double)u[i][e] * (double)wt[e];
-        if (FORM == kNormFirst) t[e] *= (double)other[i][e];
+        u[i][e] = xn[i][e];
+        if constexpr (FORM == kAdd) {
+          if (r) u[i][e] = to_f32(to_io<R>(u[i][e] + rn[i][e]));
+        } else {
+          const float z = rn[i][e];
+          gate[i][e] = z * sigmoid_f32(z);
+          if (FORM == kGateFirst) u[i][e] *= gate[i][e];
+        }
+        sum[0] = fmaf(u[i][e], u[i][e], sum[0]);
       }
-      const double m = fmax(most_of_16(most_of(t)) * (double)rr, (double)kLeast8);
-      if (live && c < padded) {
-        *reinterpret_cast<uint2*>(q + row * P + c0 + c) = pack8(t, (double)kMost8 * (double)rr / m);
-        if (lane % 16 == 0) scale[(int64_t)((c0 + c) / kBlock8) * rows + row] = (float)(m / (double)kMost8);
+      if (FORM == kAdd && h && live && c < S) store8(h + row * C + c, S - c, u[i]);
+    }
+    if (row + step < last) load(row + step);
+    group_sum(sum, tg, lds);
+    const float rr = 1.0f / sqrtf(sum[0] / (float)S + eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tg + lane) * 8;
+      if (FORM == kAdd && y && live && c < S) {
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = u[i][e] * rr * wt[i][e];
+        store8(y + row * C + c, S - c, o);
+      }
+      if (q) {
+        // y / m does not depend on r: what is quantised is y / r, and r joins the scale.
+        double t[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float we = wt[i][e];
+          asm volatile("" : "+v"(we));   // widened here, not kept in 64 bits from token to token
+          t[e] = (double)u[i][e] * (double)we;
+          if constexpr (FORM == kNormFirst) t[e] *= (double)gate[i][e];
+        }
+        const double m = fmax(most_of_16(most_of(t)) * (double)rr, (double)kLeast8);
+        if (live && c < padded) {
+          *reinterpret_cast<uint2*>(q + row * P + c0 + c) = pack8(t, (double)kMost8 * (double)rr / m);
+          if (lane % 16 == 0) scale[(int64_t)((c0 + c) / kBlock8) * rows + row] = (float)(m / (double)kMost8);
+        }
       }
     }
   }
@@ -181,21 +195,52 @@ add_norm_reduce_kernel(const float* __restrict__ part, int64_t n, int64_t C, flo
 namespace {
 
 struct ItemGrid {
-  int tg, nv, threads;
+  int tg, nv, threads, each;   // threads per item and workgroup, pieces per thread, tokens per workgroup
+  int64_t sets;                // of groups
 };
 
-// 16 or 32 lanes hold an item of up to 32 pieces; beyond that whole waves.
-ItemGrid item_grid(int64_t items, int64_t S) {
+// Pieces of 8 channels, padded to whole blocks.  16 or 32 lanes hold an item of up to 32; beyond that:
+//   the addition, which waits for memory alone, takes as many waves as give each thread one piece (two
+//   past 512), and one token for each: 16384 x 2560 to 8 bits 93 us; 2 pieces 95, 3 pieces and half the
+//   threads 100, 5 pieces in one wave 109; four tokens in a row 94, sixteen 100;
+//   gates also keep the vector ALU busy: 1, 2, 4 or 8 waves (three or five leave a SIMD with less:
+//   16384 x 5120, 320 threads of 2 pieces 144 us), the fewest idle lanes first (128 threads of 5 pieces
+//   104, 256 of 3 111), and as many tokens in a row as make one round of workgroups, up to 16 (128 of 5
+//   pieces: one token 131, eight 121, sixteen 104; 16384 x 2048 in 128 of 2: one 50, eight 43, sixteen 52).
+ItemGrid item_grid(int64_t rows, int64_t S, int64_t G, bool gate) {
+  constexpr int kWavesPerSimd[6] = {0, 6, 4, 3, 3, 2};   // of the gated kernels, by their registers
   ItemGrid g;
   const int pieces = (int)((S + kBlock8 - 1) / kBlock8 * (kBlock8 / 8));
+  const bool many = gate && rows * G >= 1024;
   if (pieces <= 32) {
     g.tg = pieces;
-  } else {
-    const int most = items < 1024 ? 2 : 4;
+  } else if (!many) {
+    const int most = pieces > 512 ? 2 : 1;
     g.tg = (pieces + kWave * most - 1) / (kWave * most) * kWave;
+  } else {
+    g.tg = 0;
+    for (int tg = 512; tg >= kWave; tg /= 2) {
+      const int nv = (pieces + tg - 1) / tg;
+      if (nv > 5 || (nv == 1 && tg > kWave)) continue;
+      if (g.tg == 0 || tg * nv < g.tg * g.nv) {
+        g.tg = tg;
+        g.nv = nv;
+      }
+    }
   }
   g.nv = (pieces + g.tg - 1) / g.tg;
-  g.threads = g.tg >= 256 ? g.tg : 256 / g.tg * g.tg;
+  int slots = g.tg >= 256 || many ? (g.tg < kWave ? 256 / g.tg : 1) : 256 / g.tg;
+  if (many && g.tg == kWave) slots = 4;
+  g.threads = g.tg * slots;
+  g.sets = G == 1 ? 1 : (G + slots - 1) / slots;
+  const int step = G == 1 ? slots : 1;
+  g.each = step;
+  if (many) {
+    const int64_t groups = 256 * (int64_t)(4 * kWavesPerSimd[g.nv] * kWave / g.threads) / g.sets;   // at once
+    int64_t each = groups > 0 ? (rows + groups - 1) / groups : 16 * step;
+    each = (each + step - 1) / step * step;
+    g.each = (int)(each < 16 * step ? each : 16 * step);
+  }
   return g;
 }
 
@@ -208,8 +253,9 @@ int64_t stripes_of(int64_t rows) { return rows < kStripes ? rows : kStripes; }
 int64_t block_norm_limit() { return 8192; }
 
 int block_norm_grid_ok(int64_t batch, int64_t L, int64_t C, int64_t G) {
-  const ItemGrid g = item_grid(1, C / G);
-  return C <= (1 << 24) && (__int128)batch * L * G * g.tg + 512 < (int64_t(1) << 32);
+  if (C > (1 << 24) || batch > INT32_MAX / L) return 0;
+  const ItemGrid g = item_grid(1, C / G, G, false);   // one token for each workgroup: the most
+  return (__int128)batch * L * 512 < (int64_t(1) << 32) && g.sets <= 65535;
 }
 
 size_t add_norm_bwd_workspace(int64_t rows, int64_t C) {
@@ -218,20 +264,22 @@ size_t add_norm_bwd_workspace(int64_t rows, int64_t C) {
 
 template <typename T, typename R, int FORM>
 static hipError_t block_norm_f(const BlockNormArgs& a, hipStream_t stream) {
-  const int64_t rows = a.batch * a.L, items = rows * a.G;
-  const ItemGrid g = item_grid(items, a.C / a.G);
-  const int64_t per = g.threads / g.tg;
+  const int64_t rows = a.batch * a.L;
+  const ItemGrid g = item_grid(rows, a.C / a.G, a.G, FORM != kAdd);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)((items + per - 1) / per)), dim3(g.threads), 0, stream,
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((rows + g.each - 1) / g.each), (unsigned)g.sets), dim3(g.threads), 0, stream,
                        static_cast<const T*>(a.x), Strides{a.xs[0], a.xs[1]},
                        static_cast<const R*>(a.r), Strides{a.zs[0], a.zs[1]}, a.w,
                        static_cast<R*>(a.h), static_cast<T*>(a.y), a.q, a.scale, a.L, rows, (int)a.C,
-                       (int)a.G, a.eps, g.tg);
+                       (int)a.G, a.eps, g.tg, g.each);
   };
   if (g.nv == 1) go(block_norm_kernel<T, R, 1, FORM>);
   else if (g.nv == 2) go(block_norm_kernel<T, R, 2, FORM>);
-  else if (g.nv == 3) go(block_norm_kernel<T, R, 3, FORM>);
-  else go(block_norm_kernel<T, R, 4, FORM>);
+  else if constexpr (FORM != kAdd) {
+    if (g.nv == 3) go(block_norm_kernel<T, R, 3, FORM>);
+    else if (g.nv == 4) go(block_norm_kernel<T, R, 4, FORM>);
+    else go(block_norm_kernel<T, R, 5, FORM>);
+  }
   return hipGetLastError();
 }
 

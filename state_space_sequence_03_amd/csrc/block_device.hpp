@@ -14,6 +14,41 @@ constexpr float kLeast8 = 7.888609052210118e-31f;   // 2^-100: a block's least m
 typedef bf16 bf16x8_any __attribute__((ext_vector_type(8), aligned(2)));
 typedef float floatx4_any __attribute__((ext_vector_type(4), aligned(4)));
 
+// The same held unconverted, for rows loaded ahead.
+template <typename T> struct Raw8;
+template <> struct Raw8<bf16> {
+  bf16x8 v;
+  __device__ __forceinline__ float operator[](int e) const { return static_cast<float>(v[e]); }
+};
+template <> struct Raw8<float> {
+  floatx4 a, b;
+  __device__ __forceinline__ float operator[](int e) const { return e < 4 ? a[e] : b[e - 4]; }
+};
+__device__ __forceinline__ Raw8<bf16> raw8(const bf16* p, int n) {
+  Raw8<bf16> r;
+  if (n >= 8) {
+    r.v = *reinterpret_cast<const bf16x8_any*>(p);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) r.v[e] = e < n ? p[e] : static_cast<bf16>(0.0f);
+  }
+  return r;
+}
+__device__ __forceinline__ Raw8<float> raw8(const float* p, int n) {
+  Raw8<float> r;
+  if (n >= 8) {
+    r.a = *reinterpret_cast<const floatx4_any*>(p);
+    r.b = *reinterpret_cast<const floatx4_any*>(p + 4);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      r.a[e] = e < n ? p[e] : 0.0f;
+      r.b[e] = e + 4 < n ? p[e + 4] : 0.0f;
+    }
+  }
+  return r;
+}
+
 // The first `n` of the eight elements at p (all of them where n >= 8), zeros behind them.
 __device__ __forceinline__ void load8(const bf16* p, int n, float (&v)[8]) {
   if (n >= 8) {
