@@ -3,7 +3,7 @@
 //
 // Over the C channels of a token:  h = x + residual, rounded to the residual's type;
 // r = (mean(h^2) + eps)^(-1/2);  y = w h r.  In 8 bits, per block of 128 channels:
-// m = max |y|, q = e4m3(y 448 / m), scale = m / 448, from h and w with no rounding of y between.
+// m = max |y|, q = e4m3(y 448 / m), scale = m / 448, with no rounding of y between.
 // Gated, in each of G groups, with s(z) = z sigmoid(z):  u = x s(z) or x,  y = w u r or
 // w u r s(z).
 // Gradients, with n = h r and t = w dy:  dh' = dh + r (t - n mean(t n)),  dw = sum over
@@ -100,19 +100,20 @@ block_norm_kernel(const T* __restrict__ x, Strides xs, const R* r, Strides zs,
         store8(y + row * C + c, S - c, o);
       }
       if (q) {
-        // y / m does not depend on r: what is quantised is y / r, and r joins the scale.
-        double t[8];
+        // y / m does not depend on r: what is quantised is t = y / r, in two parts, and r joins the scale.
+        float t[8], rest[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          float we = wt[i][e];
-          asm volatile("" : "+v"(we));   // widened here, not kept in 64 bits from token to token
-          t[e] = (double)u[i][e] * (double)we;
-          if constexpr (FORM == kNormFirst) t[e] *= (double)gate[i][e];
+          const float v = FORM == kNormFirst ? u[i][e] * gate[FORM == kNormFirst ? i : 0][e] : u[i][e];
+          t[e] = v * wt[i][e];
+          rest[e] = fmaf(v, wt[i][e], -t[e]);
+          if constexpr (FORM == kNormFirst)
+            rest[e] = fmaf(fmaf(u[i][e], gate[i][e], -v), wt[i][e], rest[e]);
         }
-        const double m = fmax(most_of_16(most_of(t)) * (double)rr, (double)kLeast8);
+        const float m = fmaxf(most_of_16(most_of(t)), kLeast8 / rr);
         if (live && c < padded) {
-          *reinterpret_cast<uint2*>(q + row * P + c0 + c) = pack8(t, (double)kMost8 * (double)rr / m);
-          if (lane % 16 == 0) scale[(int64_t)((c0 + c) / kBlock8) * rows + row] = (float)(m / (double)kMost8);
+          *reinterpret_cast<uint2*>(q + row * P + c0 + c) = pack8(t, rest, m);
+          if (lane % 16 == 0) scale[(int64_t)((c0 + c) / kBlock8) * rows + row] = m * rr / kMost8;
         }
       }
     }

@@ -124,35 +124,53 @@ __device__ __forceinline__ float most_of_16(float m) {
   return m;
 }
 
-// Eight values times `by` as e4m3, to nearest even: v 448 / m is at most 448 (1 + 2^-23),
-// which rounds to 448, so nothing has to be cut off.  The products are formed in 64 bits and
-// rounded to fp32 in front of the conversion, so a value falls on the wrong side of the middle
-// between two e4m3 values only within half a step of fp32 of it; 64-bit operations run at the
-// rate of fp32 ones here, and the kernels wait for memory.
-__device__ __forceinline__ uint2 pack8(const double (&v)[8], double by) {
+// 448 / m in two parts, to about 2^-44 of it: the hardware reciprocal (of m / 448, which stays normal) and
+// what it leaves of 448.  `bits` of them in the first part.  An infinite m gives 0.
+struct Inverse8 {
+  float hi, lo;
+};
+template <bool SHORT> __device__ __forceinline__ Inverse8 inverse8(float m) {
+  const float r = __builtin_amdgcn_rcpf(m * (1.0f / kMost8));
+  Inverse8 by;
+  by.hi = SHORT ? __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, r) & 0xffffff00u) : r;
+  const float lo = fmaf(-by.hi, m, kMost8) * (r * (1.0f / kMost8));
+  by.lo = by.hi == 0.0f ? 0.0f : lo;
+  return by;
+}
+
+// v 448 / m as e4m3, to nearest even, for eight values: at most 448 (1 + 2^-23), which rounds to 448, so
+// nothing has to be cut off.  The products are rounded once, to fp32, in front of the conversion, so a value
+// falls on the wrong side of the middle between two e4m3 values only within half a step of fp32 of it.  A
+// bf16 value times the 16 bits of a short first part is exact; others carry their rounding error along.
+__device__ __forceinline__ uint2 convert8(const float (&p)[8]) {
   uint2 r;
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32((float)(v[0] * by), (float)(v[1] * by), 0, false);
-  r.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32((float)(v[2] * by), (float)(v[3] * by), w, true);
-  w = __builtin_amdgcn_cvt_pk_fp8_f32((float)(v[4] * by), (float)(v[5] * by), 0, false);
-  r.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32((float)(v[6] * by), (float)(v[7] * by), w, true);
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(p[0], p[1], 0, false);
+  r.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(p[2], p[3], w, true);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(p[4], p[5], 0, false);
+  r.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(p[6], p[7], w, true);
   return r;
 }
-__device__ __forceinline__ uint2 pack8(const float (&v)[8], double by) {
-  double d[8];
+template <typename T> __device__ __forceinline__ uint2 pack8(const float (&v)[8], float m) {
+  constexpr bool kShort = sizeof(T) == 2;
+  const Inverse8 by = inverse8<kShort>(m);
+  float p[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) d[e] = (double)v[e];
-  return pack8(d, by);
+  for (int e = 0; e < 8; ++e) {
+    const float h = v[e] * by.hi;
+    p[e] = kShort ? fmaf(v[e], by.lo, h) : h + fmaf(v[e], by.lo, fmaf(v[e], by.hi, -h));
+  }
+  return convert8(p);
 }
-__device__ __forceinline__ double most_of(const double (&v)[8]) {
-  double m = 0.0;
+// The same of values v + rest.
+__device__ __forceinline__ uint2 pack8(const float (&v)[8], const float (&rest)[8], float m) {
+  const Inverse8 by = inverse8<false>(m);
+  float p[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) m = fmax(m, fabs(v[e]));
-  return m;
-}
-__device__ __forceinline__ double most_of_16(double m) {
-#pragma unroll
-  for (int off = 8; off >= 1; off >>= 1) m = fmax(m, __shfl_xor(m, off, 16));
-  return m;
+  for (int e = 0; e < 8; ++e) {
+    const float h = v[e] * by.hi;
+    p[e] = h + fmaf(rest[e], by.hi, fmaf(v[e], by.lo, fmaf(v[e], by.hi, -h)));
+  }
+  return convert8(p);
 }
 
 }  // namespace ssd

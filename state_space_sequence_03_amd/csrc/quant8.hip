@@ -56,7 +56,7 @@ quant_tile_kernel(const T* __restrict__ x, Strides xs, unsigned char* __restrict
       float m = tile_most;
       if constexpr (!TILE) m = fmaxf(most_of_16(most_of(v[i])), kLeast8);
       if (row < rows) {
-        *reinterpret_cast<uint2*>(q + row * nc * kBlock8 + c) = pack8(v[i], (double)kMost8 / (double)m);
+        *reinterpret_cast<uint2*>(q + row * nc * kBlock8 + c) = pack8<T>(v[i], m);
         if (!TILE && pc == 0) scale[tc * rows + row] = m / kMost8;
       }
     }
@@ -90,7 +90,7 @@ quant_tile_kernel(const T* __restrict__ x, Strides xs, unsigned char* __restrict
     for (int i = 0; i < 8; ++i) col[i] = v[i][e];
     // Column k's 16 pieces lie in places permuted by pc = k / 8, so the 64 lanes of a write
     // touch every bank alike; the permutation keeps pairs of pieces together.
-    turned[k * 16 + (pr ^ pc)] = pack8(col, (double)kMost8 / (double)m);
+    turned[k * 16 + (pr ^ pc)] = pack8<T>(col, m);
   }
   __syncthreads();
 #pragma unroll
@@ -119,7 +119,7 @@ quant_rows_kernel(const T* __restrict__ x, Strides xs, unsigned char* __restrict
   for (int e = 0; e < 8; ++e) v[e] = 0.0f;
   if (c < C) load8(x + row_at(xs, row, L) + c, (int)(C - c < 8 ? C - c : 8), v);
   const float m = fmaxf(most_of_16(most_of(v)), kLeast8);
-  *reinterpret_cast<uint2*>(q + row * nc * kBlock8 + c) = pack8(v, (double)kMost8 / (double)m);
+  *reinterpret_cast<uint2*>(q + row * nc * kBlock8 + c) = pack8<T>(v, m);
   if (threadIdx.x % 16 == 0) scale[b * rows + row] = m / kMost8;
 }
 
