@@ -48,15 +48,33 @@ __device__ __forceinline__ double block_sum(double v) {
   return (waves[0] + waves[1]) + (waves[2] + waves[3]);
 }
 
+// f(position, raw values, how many of them count) for every eighth element of a thread's share of n,
+// with kAhead loads on their way at a time.
+constexpr int kAhead = 4;
+template <typename T, typename F>
+__device__ __forceinline__ void each_piece(const T* g, int64_t n, F f) {
+  constexpr int64_t kStep = 8 * 256;
+  int64_t i = 8 * (int64_t)threadIdx.x;
+  for (; i + (kAhead - 1) * kStep + 8 <= n; i += kAhead * kStep) {
+    Raw8<T> v[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) v[k] = raw8(g + i + k * kStep, 8);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) f(i + k * kStep, v[k], 8);
+  }
+  for (; i < n; i += kStep) {
+    const int m = (int)(n - i < 8 ? n - i : 8);
+    f(i, raw8(g + i, m), m);
+  }
+}
+
 template <typename T>
 __device__ __forceinline__ double squares(const T* g, int64_t n) {
   double s[2] = {0.0, 0.0};
-  for (int64_t i = 8 * threadIdx.x; i < n; i += 8 * 256) {
-    float v[8];
-    load8(g + i, (int)(n - i < 8 ? n - i : 8), v);
+  each_piece(g, n, [&](int64_t, const Raw8<T>& v, int) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[e % 2] = fma((double)v[e], (double)v[e], s[e % 2]);
-  }
+  });
   return s[0] + s[1];
 }
 
@@ -86,14 +104,12 @@ __global__ void __launch_bounds__(256) clip_parts_kernel(const double* part, int
 
 template <typename T, typename O>
 __device__ __forceinline__ void scale_chunk(const T* g, O* out, int64_t n, float by) {
-  for (int64_t i = 8 * threadIdx.x; i < n; i += 8 * 256) {
-    const int m = (int)(n - i < 8 ? n - i : 8);
+  each_piece(g, n, [&](int64_t i, const Raw8<T>& r, int m) {
     float v[8];
-    load8(g + i, m, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= by;
+    for (int e = 0; e < 8; ++e) v[e] = r[e] * by;
     store8(out + i, m, v);
-  }
+  });
 }
 
 __global__ void __launch_bounds__(256)
@@ -104,8 +120,9 @@ clip_scale_kernel(const Tensors t, const double* __restrict__ part, int64_t part
   double c = scale;
   if (norm < INFINITY) c *= fmin(1.0, most / (norm + eps));   // false for NaN
   const float by = (float)c;
-  const int k = tensor_of(t, blockIdx.x);
-  const int64_t chunk = 8 * (int64_t)t.chunk8, at = (blockIdx.x - t.first[k]) * chunk;
+  const int b = gridDim.x - 1 - blockIdx.x;   // the last chunks first: they may still be in a cache
+  const int k = tensor_of(t, b);
+  const int64_t chunk = 8 * (int64_t)t.chunk8, at = (b - t.first[k]) * chunk;
   const int64_t n = t.n[k] - at < chunk ? t.n[k] - at : chunk;
   if (by == 1.0f && t.out[k] == t.grad[k]) return;
   const bf16* gb = static_cast<const bf16*>(t.grad[k]) + at;

@@ -27,18 +27,25 @@ quant_tile_kernel(const T* __restrict__ x, Strides xs, unsigned char* __restrict
   const int t = threadIdx.x, pr = t / 16, pc = t % 16;
   const int64_t c = c0 + 8 * pc;
   const int n = c < C ? (int)(C - c < 8 ? C - c : 8) : 0;
-  float v[8][8];
+  Raw8<T> v[8];   // in the registers of its own type, widened where it is used
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t row = r0 + 8 * pr + i;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[i][e] = 0.0f;
-    if (n > 0 && row < rows) load8(x + row_at(xs, row, L) + c, n, v[i]);
+    v[i] = Raw8<T>{};
+    if (n > 0 && row < rows) v[i] = raw8(x + row_at(xs, row, L) + c, n);
   }
+  auto row_of = [&](int i, float (&o)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] = v[i][e];
+  };
   float tile_most = 0.0f;
   if constexpr (TILE) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) tile_most = fmaxf(tile_most, most_of(v[i]));
+    for (int i = 0; i < 8; ++i) {
+      float o[8];
+      row_of(i, o);
+      tile_most = fmaxf(tile_most, most_of(o));
+    }
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) tile_most = fmaxf(tile_most, __shfl_xor(tile_most, off, kWave));
     if (t % kWave == 0) col_most[t / kWave][0] = tile_most;
@@ -53,10 +60,11 @@ quant_tile_kernel(const T* __restrict__ x, Strides xs, unsigned char* __restrict
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t row = r0 + 8 * pr + i;
-      float m = tile_most;
-      if constexpr (!TILE) m = fmaxf(most_of_16(most_of(v[i])), kLeast8);
+      float m = tile_most, o[8];
+      row_of(i, o);
+      if constexpr (!TILE) m = fmaxf(most_of_16(most_of(o)), kLeast8);
       if (row < rows) {
-        *reinterpret_cast<uint2*>(q + row * nc * kBlock8 + c) = pack8<T>(v[i], m);
+        *reinterpret_cast<uint2*>(q + row * nc * kBlock8 + c) = pack8<T>(o, m);
         if (!TILE && pc == 0) scale[tc * rows + row] = m / kMost8;
       }
     }
