@@ -307,25 +307,36 @@ def ssd_matmul8(x: Tensor8, w: Tensor8, *, out_dtype: torch.dtype = torch.bfloat
 # ------------------------------------------------------------------------- clipping
 
 def _clip_list(grads, out, dev) -> array:
-    """The ssd_grad entries, four words each."""
-    words = array("q")
-    outs = grads if out is None else out
-    for g, o in zip(grads, outs):
-        try:
-            kind, to, n = _IO[g.dtype], _IO[o.dtype], g.numel()
-            if g.get_device() == dev == o.get_device() and g.is_contiguous() and o.is_contiguous() and o.shape == g.shape:
-                words.extend((g.data_ptr(), o.data_ptr(), n, kind | to << 32))
-                continue
-        except (AttributeError, KeyError):
-            pass
+    """The ssd_grad entries, four words each.  (A call costs its tensors' marshalling: one look at each property.)"""
+    words = []
+    add, io = words.extend, _IO
+    try:
+        if out is None:
+            for g in grads:
+                kind, at = io[g.dtype], g.data_ptr()
+                if g.get_device() != dev or not g.is_contiguous():
+                    raise KeyError
+                add((at, at, g.numel(), kind | kind << 32))
+        else:
+            for g, o in zip(grads, out):
+                n = g.numel()
+                if g.get_device() != dev or o.get_device() != dev or not g.is_contiguous() or not o.is_contiguous() \
+                        or o.numel() != n:
+                    raise KeyError
+                add((g.data_ptr(), o.data_ptr(), n, io[g.dtype] | io[o.dtype] << 32))
+        return array("q", words)
+    except (AttributeError, KeyError, RuntimeError):
+        pass
+    for g, o in zip(grads, grads if out is None else out):
         for t, name in ((g, "grads"), (o, "out")):
             if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != dev:
                 raise SsdArgumentError(1, "%s must be GPU tensors on one device" % name)
             _io(t.dtype, name)
             if not t.is_contiguous():
                 raise SsdArgumentError(2, "%s must be contiguous" % name)
-        raise SsdArgumentError(2, "out must have the shapes of grads")
-    return words
+        if o.numel() != g.numel():
+            raise SsdArgumentError(2, "out must have the sizes of grads")
+    raise SsdArgumentError(1, "grads must be GPU tensors with memory of their own")
 
 
 @functools.lru_cache(maxsize=1024)

@@ -120,7 +120,7 @@ block_norm_kernel(const T* __restrict__ x, Strides xs, const R* r, Strides zs,
   }
 }
 
-// A workgroup takes rows first, first + stride, ... and keeps its sums of dw in
+// A workgroup takes rows first, first + stride, ..., the next one loaded ahead, and keeps its sums of dw in
 // registers; it leaves one row of part sums [C] in the workspace.
 template <typename T, typename R, int NV>
 __global__ void __launch_bounds__(512)
@@ -137,19 +137,36 @@ add_norm_bwd_kernel(const R* h, const float* __restrict__ w, const T* __restrict
     for (int e = 0; e < 8; ++e) wt[i][e] = dw[i][e] = 0.0f;
     if (c < C) load8(w + c, C - c, wt[i]);
   }
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-    float u[NV][8], g[NV][8], up[NV][8];
+  Raw8<R> hn[NV], un[NV];   // the next row, loaded while this one is worked on
+  Raw8<T> gn[NV];
+  auto load = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tg + lane) * 8;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) u[i][e] = g[i][e] = up[i][e] = 0.0f;
       if (c < C) {
-        load8(h + row * C + c, C - c, u[i]);
-        load8(dy + row * C + c, C - c, g[i]);
-        if (dh) load8(dh + row * C + c, C - c, up[i]);
+        hn[i] = raw8(h + row * C + c, C - c);
+        gn[i] = raw8(dy + row * C + c, C - c);
+        if (dh) un[i] = raw8(dh + row * C + c, C - c);
       }
     }
+  };
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    hn[i] = un[i] = Raw8<R>{};
+    gn[i] = Raw8<T>{};
+  }
+  if (blockIdx.x < rows) load(blockIdx.x);
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    float u[NV][8], g[NV][8], up[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        u[i][e] = hn[i][e];
+        g[i][e] = gn[i][e];
+        up[i][e] = un[i][e];
+      }
+    if (row + gridDim.x < rows) load(row + gridDim.x);
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -245,8 +262,22 @@ ItemGrid item_grid(int64_t rows, int64_t S, int64_t G, bool gate) {
   return g;
 }
 
-constexpr int kStripes = 1024;
-int64_t stripes_of(int64_t rows) { return rows < kStripes ? rows : kStripes; }
+// The gradients: one piece per thread up to 512 of them, and as many workgroups as give each CU 256
+// threads or one workgroup: more only make more part sums (8192 x 2560 in 256 of 320 threads 66 us, 512 73,
+// 1024 82; 40960 x 512 in 1024 of 64 threads 74, 512 104, 2048 88).
+struct BwdGrid {
+  int nv, threads;
+  int64_t stripes;
+};
+BwdGrid bwd_grid(int64_t rows, int64_t C) {
+  BwdGrid g;
+  const int pieces = (int)((C + 7) / 8);
+  g.nv = pieces > 512 ? 2 : 1;
+  g.threads = (pieces + g.nv * kWave - 1) / (g.nv * kWave) * kWave;
+  g.stripes = 256 * (g.threads < 256 ? 256 / g.threads : 1);
+  if (g.stripes > rows) g.stripes = rows;
+  return g;
+}
 
 }  // namespace
 
@@ -260,7 +291,7 @@ int block_norm_grid_ok(int64_t batch, int64_t L, int64_t C, int64_t G) {
 }
 
 size_t add_norm_bwd_workspace(int64_t rows, int64_t C) {
-  return size_t(stripes_of(rows)) * C * sizeof(float);
+  return size_t(bwd_grid(rows, C).stripes) * C * sizeof(float);
 }
 
 template <typename T, typename R, int FORM>
@@ -296,23 +327,20 @@ hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t stream) {
 
 template <typename T, typename R>
 static hipError_t add_norm_bwd_t(const AddNormBwdArgs& a, hipStream_t stream) {
-  const int pieces = (int)((a.C + 7) / 8);
-  const int nv = pieces > 512 ? 2 : 1;
-  const int threads = (pieces + nv * kWave - 1) / (nv * kWave) * kWave;
-  const int64_t stripes = stripes_of(a.rows);
+  const BwdGrid g = bwd_grid(a.rows, a.C);
   float* part = static_cast<float*>(a.workspace);
   auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)stripes), dim3(threads), 0, stream,
+    hipLaunchKernelGGL(kernel, dim3((unsigned)g.stripes), dim3(g.threads), 0, stream,
                        static_cast<const R*>(a.h), a.w, static_cast<const T*>(a.dy),
                        static_cast<const R*>(a.dh), static_cast<T*>(a.dx), static_cast<R*>(a.dres),
                        part, a.rows, (int)a.C, a.eps);
   };
-  if (nv == 1) go(add_norm_bwd_kernel<T, R, 1>);
+  if (g.nv == 1) go(add_norm_bwd_kernel<T, R, 1>);
   else go(add_norm_bwd_kernel<T, R, 2>);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(add_norm_reduce_kernel, dim3((unsigned)((a.C + 31) / 32)), dim3(256), 0, stream,
-                     part, stripes, a.C, a.dw);
+                     part, g.stripes, a.C, a.dw);
   return hipGetLastError();
 }
 
