@@ -147,13 +147,13 @@ namespace {
 struct ClipPlan {
   int64_t chunk, parts;
 };
-// Chunks so that a large list takes about 8192 workgroups, a small one at least
+// Chunks so that a large list takes about 4096 workgroups (241 M gradients 410 us; 8192: 418, 2048: 430), a small one at least
 // kLeastChunk elements each.
 ClipPlan clip_plan(const ssd_grad* g, int64_t n) {
   int64_t total = 0;
   for (int64_t i = 0; i < n; ++i) total += g[i].elements;
   ClipPlan p;
-  p.chunk = total / 8192 / 8 * 8;
+  p.chunk = total / 4096 / 8 * 8;
   if (p.chunk < kLeastChunk) p.chunk = kLeastChunk;
   p.parts = 0;
   for (int64_t i = 0; i < n; ++i) p.parts += (g[i].elements + p.chunk - 1) / p.chunk;
