@@ -217,14 +217,10 @@ matmul8_kernel(const unsigned char* __restrict__ x, const float* __restrict__ xs
   auto rows8 = [&](const unsigned char* base, uint32_t last, int piece, unsigned char* to) {
     dma16_so(base, min(from + (uint32_t)(8 * piece) * (uint32_t)K, last), to + piece * 1024);
   };
-  // Each wave's columns fall into a lower and an upper half; a block comes in two parts.
-  auto load_half = [&](int b, int half) {
-    const unsigned char* base = wb + min(b, blocks - 1) * kBlock8;
-#pragma unroll
-    for (int i = 0; i < kHalfN; ++i) {
-      const int l = wave + kWaves * i;
-      rows8(base, last_n, l / NT * 2 * NT + half * NT + l % NT, lds + (b % 2) * kBuffer);
-    }
+  // Each wave's columns fall into a lower and an upper half.  The i-th piece of one, of this wave's:
+  auto load_half = [&](int b, int half, int i) {
+    const int l = wave + kWaves * i;
+    rows8(wb + min(b, blocks - 1) * kBlock8, last_n, l / NT * 2 * NT + half * NT + l % NT, lds + (b % 2) * kBuffer);
   };
   // The scales of a block, 64 by each wave (more than once where there are more waves than that).
   const int wtiles = (N + kBlock8 - 1) / kBlock8;
@@ -236,15 +232,19 @@ matmul8_kernel(const unsigned char* __restrict__ x, const float* __restrict__ xs
   sbase += b0 * srow;
   const int sleft = (int)(for_m ? M - m0 : TILE ? wtiles - n0 / kBlock8 : N - n0);
   const uint32_t sat = 4 * min(64 * (for_m ? spart : spart - BM / 64) + lane, sleft - 1);
-  auto load_rest = [&](int b) {
+  // The rows of x, the scales and the lower half: the i-th of kFirst loads.
+  constexpr int kFirst = kPiecesM + 1 + kHalfN;
+  auto load_first = [&](int b, int i) {
     unsigned char* to = lds + (b % 2) * kBuffer;
-    const unsigned char* base = xb + min(b, blocks - 1) * kBlock8;
-#pragma unroll
-    for (int i = 0; i < kPiecesM; ++i) rows8(base, last_m, wave + kWaves * i, to + BN * kBlock8);
-    dma4_so(sbase + min(b, blocks - 1) * srow, sat, to + (BN + BM) * kBlock8 + 256 * spart);
+    if (i < kPiecesM)
+      rows8(xb + min(b, blocks - 1) * kBlock8, last_m, wave + kWaves * i, to + BN * kBlock8);
+    else if (i == kPiecesM)
+      dma4_so(sbase + min(b, blocks - 1) * srow, sat, to + (BN + BM) * kBlock8 + 256 * spart);
+    else
+      load_half(b, 0, i - kPiecesM - 1);
   };
   // Waits until every wave's loads but those of the latest `kAhead` have arrived, and its LDS reads are done.
-  constexpr int kAhead = kPiecesM + 1 + 2 * kHalfN;
+  constexpr int kAhead = kFirst + kHalfN;
   auto arrived = [&](floatx4& behind) {   // behind the work that gives `behind`
     asm volatile("s_waitcnt vmcnt(%1) lgkmcnt(0)" : "+v"(behind) : "n"(kAhead) : "memory");
     __builtin_amdgcn_s_barrier();
@@ -285,12 +285,13 @@ matmul8_kernel(const unsigned char* __restrict__ x, const float* __restrict__ xs
   // 8-bit operands are read into the registers that products take them from; operands to be
   // widened wait as they are.
   constexpr bool kWide = !std::is_same<Frag, intx8>::value;
-  load_rest(0);
-  load_half(0, 0);
-  load_half(0, 1);
-  load_rest(1);
-  load_half(1, 0);
-  load_half(1, 1);
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) load_first(b, i);
+#pragma unroll
+    for (int i = 0; i < (b == 0 ? kHalfN : 1); ++i) load_half(b, 1, i);
+  }
   arrived(acc[0][0]);
   intx8 an = read_n(0, 0), cn[MT];
 #pragma unroll
@@ -320,17 +321,18 @@ matmul8_kernel(const unsigned char* __restrict__ x, const float* __restrict__ xs
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       a = Frag8<O>::of(an);
-      if (i + 1 == NT / 2) {
-        arrived(acc[NT / 2 - 2][0]);
-        load_rest(b + 2);
-        load_half(b + 2, 0);
-      }
-      if (i + 1 < NT) {
-        an = read_n(b, i + 1);
-      } else {
-        arrived(acc[NT - 2][0]);
-        an = read_n(b + 1, 0);
-        load_half(b + 2, 1);
+      if (i + 1 == NT / 2) arrived(acc[NT / 2 - 2][0]);
+      if (i + 1 == NT) arrived(acc[NT - 2][0]);
+      an = i + 1 < NT ? read_n(b, i + 1) : read_n(b + 1, 0);
+      // loads, a few between any two reads: many in a row would hold the wave up
+      if (i + 1 >= NT / 2 && i + 1 < NT) {
+        constexpr int kEach = (kFirst + NT / 2 - 1) / (NT / 2);
+        const int g = i + 1 - NT / 2;
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+          if (g * kEach + k < kFirst) load_first(b + 2, g * kEach + k);
+      } else if (i + 1 < kHalfN) {
+        load_half(b + 1, 1, i + 1);
       }
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
@@ -344,6 +346,7 @@ matmul8_kernel(const unsigned char* __restrict__ x, const float* __restrict__ xs
 #pragma unroll
     for (int t = NT * MT - kLag; t < NT * MT; ++t) add(t);
     read_scales(b + 1);
+    load_half(b + 2, 1, 0);
     // the order of the above, which the scheduler is held to: reads, one product, the sums of an earlier one
     constexpr int kSums = (TILE ? 4 : 8) + (kWide ? 16 / MT : 0);
 #pragma unroll
@@ -356,6 +359,8 @@ matmul8_kernel(const unsigned char* __restrict__ x, const float* __restrict__ xs
   }
   // The tile of y goes through LDS, so that whole rows of a wave's columns are stored: 16 bytes a lane,
   // 256 in a row.  Rows lie 16 bytes further apart than they are long, and their pieces in all banks.
+  // The largest tiles, which are taken where y is larger than the caches, are stored past them (16384 x
+  // 10576 x 2560: 417 us in place of 448).
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();   // no load is on its way to LDS, and nothing is read from it any more
   asm volatile("" ::: "memory");
@@ -378,7 +383,8 @@ matmul8_kernel(const unsigned char* __restrict__ x, const float* __restrict__ xs
       typedef Y PieceAny __attribute__((ext_vector_type(16 / sizeof(Y)), aligned(sizeof(Y))));
       const Piece v = *reinterpret_cast<const Piece*>(from_lds);
       if (n + kEach <= N) {
-        *reinterpret_cast<PieceAny*>(to) = v;
+        if constexpr (NT * MT > 16) __builtin_nontemporal_store(v, reinterpret_cast<PieceAny*>(to));
+        else *reinterpret_cast<PieceAny*>(to) = v;
       } else {
 #pragma unroll
         for (int e = 0; e < kEach; ++e)
@@ -419,27 +425,31 @@ struct Matmul8Plan {
   int parts, each;   // of the depth
 };
 
-// How a product is computed (bf16 results, us; a block is 128 of the depth):
-//   up to 16 rows, each wave its own blocks, straight from memory: 1 x 10576 x 2560 7.1, tiles of 128 x 64 11
-//   tiles of 128 columns x 64 rows up to three for each CU: 512 x 10576 x 2560 24.0, of 128 rows 25.1,
-//     2048 x 2560 x 5120 41.4 against 43.4
-//   of 256 x 256 from two for each CU: 4096 x 10576 x 2560 140, of 128 x 128 153; with fewer it is the other
-//     way: 2048 x 10576 x 2560 79 against 74
-//   fp32 results take twice the registers for operands: tiles of 128 x 128 and 128 x 64 alone
+// How a product is computed (us, bf16 results unless said):
+//   up to 16 rows, each wave its own blocks, straight from memory: 1 x 10576 x 2560 7.1, in tiles of 64 x 64 9
+//   tiles of 256 x 256 from 160 of them: 1024 x 10576 x 2560 39, of 128 x 128 42; 4096 x 2560 x 5120 64 and 70,
+//     8192 x 2560 x 5120 (320 tiles) 123 and 120, 16384 x 2560 x 5120 198 and 232
+//   of 128 x 128 from 160 of them: 256 x 10576 x 2560 15.2, of 64 x 64 16.4; 1024 x 2560 x 5120 26 and 28, but
+//     512 x 2560 x 5120 (80 tiles) 26 and 18.  fp32 results take twice the registers for their operands, and
+//     these tiles at most.
+//   few tiles of 64 x 64: the depth is split between workgroups as long as CUs are free and a part has ten
+//     blocks (fp32 results take the matrix cores longer: three workgroups for each CU, six blocks): 128 x 2560
+//     x 5120 14.8, in three 11.6, in six 13.0; 200 x 1000 x 16384 40, in four 16.6; 64 x 640 x 1280 5.1, in two
+//     6.5; fp32 128 x 2560 x 5120 26.6, in six 15.6
 Matmul8Plan matmul8_plan(int64_t M, int64_t N, int64_t K, int out_bf16) {
-  const int64_t tn = (N + 127) / 128, t64 = (M + 63) / 64 * tn, t256 = (M + 255) / 256 * ((N + 255) / 256);
+  const auto tiles = [&](int64_t t) { return (M + t - 1) / t * ((N + t - 1) / t); };
   const int64_t blocks = K / kBlock8;
   Matmul8Plan p;
   p.parts = 1;
   p.each = (int)blocks;
   if (M <= 16) p.form = kFew;
-  else if (t64 <= 768) p.form = kTile64;
-  else if (out_bf16 && t256 >= 512) p.form = kTile256;
-  else p.form = kTile128;
+  else if (out_bf16 && tiles(256) >= 160) p.form = kTile256;
+  else if (tiles(128) >= 160) p.form = kTile128;
+  else p.form = kTile64;
   if (p.form == kTile64) {
-    // few tiles: the depth is split until every CU has work, into parts of at least 8 blocks
-    int64_t parts = 256 / t64;
-    if (parts > blocks / 8) parts = blocks / 8;
+    int64_t parts = (out_bf16 ? 256 : 768) / tiles(64);
+    const int64_t most = blocks / (out_bf16 ? 10 : 6);
+    if (parts > most) parts = most;
     if (parts > 1) {
       p.each = (int)((blocks + parts - 1) / parts);
       p.parts = (int)((blocks + p.each - 1) / p.each);
@@ -455,9 +465,9 @@ size_t matmul8_workspace(int64_t M, int64_t N, int64_t K, int out_bf16) {
   return p.parts > 1 ? size_t(p.parts) * M * N * sizeof(float) : 0;
 }
 
-// The smallest tiles, 16 columns x 16 rows (up to 16 rows) or 128 x 64, of 512 threads at most.
+// The smallest tiles, 16 columns x 16 rows (up to 16 rows) or 64 x 64, of 512 threads at most.
 int matmul8_grid_ok(int64_t M, int64_t N) {
-  const __int128 tiles = M <= 16 ? (N + 15) / 16 : (__int128)((N + 127) / 128) * ((M + 63) / 64);
+  const __int128 tiles = M <= 16 ? (N + 15) / 16 : (__int128)((N + 63) / 64) * ((M + 63) / 64);
   return tiles * 512 < (int64_t(1) << 32);
 }
 
@@ -494,9 +504,9 @@ static hipError_t matmul8_o(const Matmul8Args& a, hipStream_t stream) {
   if (p.form == kTile128) return tiles<O, O, 4, 4, 2, 2, TILE>(a, p, y, stream);
   if constexpr (sizeof(O) == 2)
     if (p.form == kTile256) return tiles<O, O, 8, 4, 2, 4, TILE>(a, p, y, stream);
-  if (p.parts == 1) return tiles<O, O, 4, 2, 2, 2, TILE>(a, p, y, stream);
+  if (p.parts == 1) return tiles<O, O, 4, 1, 1, 4, TILE>(a, p, y, stream);
   float* part = static_cast<float*>(a.workspace);
-  const hipError_t e = tiles<O, float, 4, 2, 2, 2, TILE>(a, p, part, stream);
+  const hipError_t e = tiles<O, float, 4, 1, 1, 4, TILE>(a, p, part, stream);
   if (e != hipSuccess) return e;
   const int64_t n = a.M * a.N;
   hipLaunchKernelGGL(matmul8_join_kernel<O>, dim3((unsigned)((n + 1023) / 1024)), dim3(256), 0, stream, part, p.parts, n, y);
