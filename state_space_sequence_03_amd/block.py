@@ -107,6 +107,16 @@ def _new8(like, lead, depth: int, scales: int) -> Tensor8:
     return Tensor8(like.new_empty(tuple(lead) + (kb * 128,), dtype=_E4M3), like.new_empty((kb, scales), dtype=_F32))
 
 
+def _output(wanted: bool, out, name: str, like, shape, dtype, dev: int):
+    """An output (the caller's, checked, or a new one) and its pointer; None, None where it is not wanted."""
+    if not wanted:
+        return None, None
+    if out is None:
+        out = like.new_empty(shape, dtype=dtype)
+        return out, out.data_ptr()
+    return out, _plain(out, name, dtype, shape, dev)
+
+
 # ---------------------------------------------------------------- residual and norm
 
 def make_add_norm_problem(batch, seqlen, channels, eps, io_dtype, residual_dtype) -> ssd_add_norm_problem:
@@ -148,17 +158,15 @@ def ssd_add_norm_fwd(x: torch.Tensor, residual: Optional[torch.Tensor], weight: 
     if not (want_y or want_8bit):
         raise SsdArgumentError(10, "want_y or want_8bit must be set")
     prob = _add_norm_problem(*shape, float(eps), _io_code(x), _io(res, "residual"))
-    y = h = y8 = None
-    if want_y:
-        y = out if out is not None else x.new_empty(shape)
-    if want_h:
-        h = h_out if h_out is not None else x.new_empty(shape, dtype=res)
+    src = _rows(x, "x", io, shape, dev)
+    rp, wp = _plain(residual, "residual", res, shape, dev), _plain(weight, "weight", _F32, (shape[2],), dev)
+    y, yp = _output(want_y, out, "out", x, shape, io, dev)
+    h, hp = _output(want_h, h_out, "h_out", x, shape, res, dev)
+    y8, qp, sp = None, None, None
     if want_8bit:
         y8 = _new8(x, shape[:2], shape[2], shape[0] * shape[1])
-    _launch(lib.ssd_add_norm_fwd, dev, prob, *_rows(x, "x", io, shape, dev),
-            _plain(residual, "residual", res, shape, dev), _plain(weight, "weight", _F32, (shape[2],), dev),
-            _plain(h, "h_out", res, shape, dev), _plain(y, "out", io, shape, dev),
-            None if y8 is None else y8.q.data_ptr(), None if y8 is None else y8.scale.data_ptr())
+        qp, sp = y8.q.data_ptr(), y8.scale.data_ptr()
+    _launch(lib.ssd_add_norm_fwd, dev, prob, *src, rp, wp, hp, yp, qp, sp)
     return y, y8, h
 
 
@@ -186,14 +194,11 @@ def ssd_add_norm_bwd(h: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor,
     key = shape + (float(eps), _io(io, "dy"), _io_code(h))
     ptrs = (_plain(h, "h", res, shape, dev), _plain(weight, "weight", _F32, (shape[2],), dev),
             _plain(dy, "dy", io, shape, dev), _plain(dh, "dh", res, shape, dev))
-    dx = dy.new_empty(shape) if want_dx else None
-    dres = None
-    if want_dresidual:
-        dres = dresidual_out if dresidual_out is not None else h.new_empty(shape)
+    dx, dxp = _output(want_dx, None, "dx", dy, shape, io, dev)
+    dres, drp = _output(want_dresidual, dresidual_out, "dresidual_out", h, shape, res, dev)
     dw = weight.new_empty((shape[2],))
     ws, ws_bytes, held = _scratch(h, workspace, _add_norm_bwd_bytes(*key) if workspace is None else 0, dev)
-    _launch(lib.ssd_add_norm_bwd, dev, _add_norm_problem(*key), *ptrs, None if dx is None else dx.data_ptr(),
-            _plain(dres, "dresidual_out", res, shape, dev), dw.data_ptr(), ws, ws_bytes)
+    _launch(lib.ssd_add_norm_bwd, dev, _add_norm_problem(*key), *ptrs, dxp, drp, dw.data_ptr(), ws, ws_bytes)
     return {"dx": dx, "dresidual": dres, "dweight": dw}
 
 
@@ -268,15 +273,17 @@ def ssd_matmul8_workspace_size(prob: ssd_matmul8_problem) -> int:
     return _size(load_library().ssd_matmul8_workspace_size, prob)
 
 
-def _operand(t, name: str):
+def _operand(t, name: str, dev: Optional[int]):
+    """(q, its shape, its pointer, scale) of an 8-bit operand."""
     if not isinstance(t, tuple) or len(t) != 2:
         raise SsdArgumentError(1, "%s must be a Tensor8" % name)
     q = t[0]
     if not isinstance(q, torch.Tensor) or not q.is_cuda:
         raise SsdArgumentError(1, "%s.q must be a GPU tensor" % name)
-    if q.dim() < 2 or q.shape[-1] % 128 != 0:
+    shape = q.shape
+    if len(shape) < 2 or shape[-1] % 128 != 0:
         raise SsdArgumentError(2, "%s.q must be [..., depth] with a depth padded to whole blocks of 128" % name)
-    return q, t[1]
+    return q, shape, _plain(q, name + ".q", _E4M3, shape, q.get_device() if dev is None else dev), t[1]
 
 
 def ssd_matmul8(x: Tensor8, w: Tensor8, *, out_dtype: torch.dtype = torch.bfloat16,
@@ -284,23 +291,21 @@ def ssd_matmul8(x: Tensor8, w: Tensor8, *, out_dtype: torch.dtype = torch.bfloat
     """y = x w^T of 8-bit operands.  x is by row, q [..., depth]; w is by tile or by row, q
     [cols, depth].  Returns y [..., cols] in out_dtype."""
     lib = load_library()
-    (xq, xs), (wq, ws) = _operand(x, "x"), _operand(w, "w")
-    dev, depth, lead = xq.get_device(), xq.shape[-1], tuple(xq.shape[:-1])
-    rows = 1
-    for n in lead:
-        rows *= n
-    if wq.dim() != 2 or wq.shape[1] != depth:
-        raise SsdArgumentError(2, "w.q must be [cols, %d], got %s" % (depth, list(wq.shape)))
-    cols, kb = wq.shape[0], depth // 128
-    tile = isinstance(ws, torch.Tensor) and ws.shape == (kb, _blocks(cols))
+    xq, shape, xp, xs = _operand(x, "x", None)
+    dev, depth, lead = xq.get_device(), shape[-1], shape[:-1]
+    rows = lead.numel()
+    _, wshape, wp, ws = _operand(w, "w", dev)
+    if len(wshape) != 2 or wshape[1] != depth:
+        raise SsdArgumentError(2, "w.q must be [cols, %d], got %s" % (depth, list(wshape)))
+    cols, kb = wshape[0], depth // 128
+    tiles = (kb, _blocks(cols))
+    tile = isinstance(ws, torch.Tensor) and ws.shape == tiles
     prob, need = _matmul8_problem(rows, cols, depth, tile, _io(out_dtype, "out_dtype"))
-    ptrs = (_plain(xq, "x.q", _E4M3, xq.shape, dev), _plain(xs, "x.scale", _F32, (kb, rows), dev),
-            _plain(wq, "w.q", _E4M3, wq.shape, dev),
-            _plain(ws, "w.scale", _F32, (kb, _blocks(cols)) if tile else (kb, cols), dev))
-    y = out if out is not None else xq.new_empty(lead + (cols,), dtype=out_dtype)
-    yp = _plain(y, "out", out_dtype, lead + (cols,), dev)
+    xsp = _plain(xs, "x.scale", _F32, (kb, rows), dev)
+    wsp = _plain(ws, "w.scale", _F32, tiles if tile else (kb, cols), dev)
+    y, yp = _output(True, out, "out", xq, tuple(lead) + (cols,), out_dtype, dev)
     mem, mem_bytes, held = _scratch(xq, workspace, need if workspace is None else 0, dev)
-    _launch(lib.ssd_matmul8, dev, prob, *ptrs, yp, mem, mem_bytes)
+    _launch(lib.ssd_matmul8, dev, prob, xp, xsp, wp, wsp, yp, mem, mem_bytes)
     return y
 
 

@@ -128,6 +128,8 @@ GATED = [
     (1, 1, 5, 1, 0, "bf16", False, True), (2, 3, 130, 1, 1, "bf16", True, True), (1, 4, 256, 2, 8, "fp32", False, True),
     (3, 2, 1024, 8, 24, "bf16", True, True), (1, 7, 1111, 1, 0, "fp32", False, True), (2, 5, 384, 3, 0, "bf16", False, False),
     (1, 1030, 5120, 1, 5456, "bf16", False, True), (2, 520, 4096, 2, 3, "bf16", False, True), (1, 2, 16384, 2, 0, "bf16", True, True),
+    (1, 1100, 130, 1, 1, "bf16", False, True), (2, 600, 256, 2, 0, "fp32", False, True), (3, 400, 1300, 1, 0, "bf16", True, True),
+    (1, 1029, 3000, 1, 8, "bf16", False, True), (1, 1200, 8192, 1, 0, "fp32", True, True), (5, 300, 1024, 8, 0, "bf16", False, False),
 ]
 
 
@@ -199,7 +201,9 @@ def test_quant8_extremes(dtype):
 # rows, cols, depth
 PRODUCT = [(1, 1, 128), (1, 130, 256), (3, 31, 384), (16, 33, 1152), (17, 257, 128), (63, 128, 2176), (64, 129, 640),
            (65, 32, 1280), (128, 300, 2560), (129, 384, 256), (200, 10, 4096), (257, 513, 384), (300, 1000, 1024), (513, 260, 128),
-           (1000, 770, 2176), (1024, 1024, 512), (640, 2563, 256), (2, 2000, 5120)]
+           (1000, 770, 2176), (1024, 1024, 512), (640, 2563, 256), (2, 2000, 5120),
+           # tiles of 128 x 128 and of 256 x 256 with ragged ends, of one block and more
+           (1500, 1701, 384), (1409, 1793, 128), (2600, 4101, 128), (2561, 4097, 640)]
 
 
 def operands(rows, cols, depth, tile, seed=0):
