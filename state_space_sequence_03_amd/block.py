@@ -108,11 +108,13 @@ def _new8(like, lead, depth: int, scales: int) -> Tensor8:
 
 
 def _output(wanted: bool, out, name: str, like, shape, dtype, dev: int):
-    """An output (the caller's, checked, or a new one) and its pointer; None, None where it is not wanted."""
+    """An output (the caller's, checked, or a new one) and its pointer; None, None where it is not wanted.
+    `like` is on its device; a contiguous one of its shape and type is the quickest to make it from."""
     if not wanted:
         return None, None
     if out is None:
-        out = like.new_empty(shape, dtype=dtype)
+        same = like.dtype is dtype and like.shape == shape and like.is_contiguous()
+        out = torch.empty_like(like) if same else like.new_empty(shape, dtype=dtype)
         return out, out.data_ptr()
     return out, _plain(out, name, dtype, shape, dev)
 
@@ -161,7 +163,7 @@ def ssd_add_norm_fwd(x: torch.Tensor, residual: Optional[torch.Tensor], weight: 
     src = _rows(x, "x", io, shape, dev)
     rp, wp = _plain(residual, "residual", res, shape, dev), _plain(weight, "weight", _F32, (shape[2],), dev)
     y, yp = _output(want_y, out, "out", x, shape, io, dev)
-    h, hp = _output(want_h, h_out, "h_out", x, shape, res, dev)
+    h, hp = _output(want_h, h_out, "h_out", x if residual is None else residual, shape, res, dev)
     y8, qp, sp = None, None, None
     if want_8bit:
         y8 = _new8(x, shape[:2], shape[2], shape[0] * shape[1])
@@ -196,7 +198,7 @@ def ssd_add_norm_bwd(h: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor,
             _plain(dy, "dy", io, shape, dev), _plain(dh, "dh", res, shape, dev))
     dx, dxp = _output(want_dx, None, "dx", dy, shape, io, dev)
     dres, drp = _output(want_dresidual, dresidual_out, "dresidual_out", h, shape, res, dev)
-    dw = weight.new_empty((shape[2],))
+    dw = torch.empty_like(weight)
     ws, ws_bytes, held = _scratch(h, workspace, _add_norm_bwd_bytes(*key) if workspace is None else 0, dev)
     _launch(lib.ssd_add_norm_bwd, dev, _add_norm_problem(*key), *ptrs, dxp, drp, dw.data_ptr(), ws, ws_bytes)
     return {"dx": dx, "dresidual": dres, "dweight": dw}
@@ -292,8 +294,8 @@ def ssd_matmul8(x: Tensor8, w: Tensor8, *, out_dtype: torch.dtype = torch.bfloat
     [cols, depth].  Returns y [..., cols] in out_dtype."""
     lib = load_library()
     xq, shape, xp, xs = _operand(x, "x", None)
-    dev, depth, lead = xq.get_device(), shape[-1], shape[:-1]
-    rows = lead.numel()
+    dev, depth, lead = xq.get_device(), shape[-1], tuple(shape[:-1])
+    rows = shape.numel() // depth if depth else 0
     _, wshape, wp, ws = _operand(w, "w", dev)
     if len(wshape) != 2 or wshape[1] != depth:
         raise SsdArgumentError(2, "w.q must be [cols, %d], got %s" % (depth, list(wshape)))
@@ -303,7 +305,7 @@ def ssd_matmul8(x: Tensor8, w: Tensor8, *, out_dtype: torch.dtype = torch.bfloat
     prob, need = _matmul8_problem(rows, cols, depth, tile, _io(out_dtype, "out_dtype"))
     xsp = _plain(xs, "x.scale", _F32, (kb, rows), dev)
     wsp = _plain(ws, "w.scale", _F32, tiles if tile else (kb, cols), dev)
-    y, yp = _output(True, out, "out", xq, tuple(lead) + (cols,), out_dtype, dev)
+    y, yp = _output(True, out, "out", xq, lead + (cols,), out_dtype, dev)
     mem, mem_bytes, held = _scratch(xq, workspace, need if workspace is None else 0, dev)
     _launch(lib.ssd_matmul8, dev, prob, xp, xsp, wp, wsp, yp, mem, mem_bytes)
     return y
