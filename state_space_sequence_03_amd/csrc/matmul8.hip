@@ -425,37 +425,51 @@ struct Matmul8Plan {
   int parts, each;   // of the depth
 };
 
-// How a product is computed (us, bf16 results unless said):
-//   up to 16 rows, each wave its own blocks, straight from memory: 1 x 10576 x 2560 7.1, in tiles of 64 x 64 9
-//   tiles of 256 x 256 from 160 of them: 1024 x 10576 x 2560 39, of 128 x 128 42; 4096 x 2560 x 5120 64 and 70,
-//     8192 x 2560 x 5120 (320 tiles) 123 and 120, 16384 x 2560 x 5120 198 and 232
-//   of 128 x 128 from 160 of them: 256 x 10576 x 2560 15.2, of 64 x 64 16.4; 1024 x 2560 x 5120 26 and 28, but
-//     512 x 2560 x 5120 (80 tiles) 26 and 18.  fp32 results take twice the registers for their operands, and
-//     these tiles at most.
-//   few tiles of 64 x 64: the depth is split between workgroups as long as CUs are free and a part has ten
-//     blocks (fp32 results take the matrix cores longer: three workgroups for each CU, six blocks): 128 x 2560
-//     x 5120 14.8, in three 11.6, in six 13.0; 200 x 1000 x 16384 40, in four 16.6; 64 x 640 x 1280 5.1, in two
-//     6.5; fp32 128 x 2560 x 5120 26.6, in six 15.6
+// How a product is computed.  Up to 16 rows, each wave takes its own blocks straight from memory (1 x 10576 x
+// 2560 7.1 us, in tiles of 64 x 64 9).  Beyond that the form and the parts of the depth whose time, by what was
+// measured, is the least.  With c tiles (times parts) for each CU, a step of 128 in the depth takes (us)
+//                 bf16 results                          fp32 results
+//   64 x 64       0.33, and 0.26 (c - 1) more past one   0.65, 0.42
+//   128 x 128     0.65, 0.72                             1.30, 1.15
+//   256 x 256     1.7, 1.9 ceil(c) past 180 tiles        (their operands take twice the registers)
+// a launch 3, and a split depth 3 more and the parts' way through memory at 4.5 TB/s.  Measured against it:
+//   512 x 2560 x 5120 in tiles of 64 18.8 (18.8), of 128 25.8 (29); 256 x 10576 x 2560 16.4 (18), 15.2 (16);
+//   2048 x 10576 x 2560 in tiles of 128 73 (76), of 256 74 (79); 4096 x 10576 x 2560 146 (151), 117 (117);
+//   128 x 2560 x 5120 whole 14.8 (16), in three parts 11.6 (12.5); fp32 1111 x 770 x 2176 whole 14.4 (14), in two
+//   17 (17); fp32 1500 x 1500 x 16384 in tiles of 128 whole 162 (169), in four parts 106 (104).
 Matmul8Plan matmul8_plan(int64_t M, int64_t N, int64_t K, int out_bf16) {
-  const auto tiles = [&](int64_t t) { return (M + t - 1) / t * ((N + t - 1) / t); };
   const int64_t blocks = K / kBlock8;
-  Matmul8Plan p;
-  p.parts = 1;
-  p.each = (int)blocks;
-  if (M <= 16) p.form = kFew;
-  else if (out_bf16 && tiles(256) >= 160) p.form = kTile256;
-  else if (tiles(128) >= 160) p.form = kTile128;
-  else p.form = kTile64;
-  if (p.form == kTile64) {
-    int64_t parts = (out_bf16 ? 256 : 768) / tiles(64);
-    const int64_t most = blocks / (out_bf16 ? 10 : 6);
-    if (parts > most) parts = most;
-    if (parts > 1) {
-      p.each = (int)((blocks + parts - 1) / parts);
-      p.parts = (int)((blocks + p.each - 1) / p.each);
+  Matmul8Plan best{kFew, 1, (int)blocks};
+  if (M <= 16) return best;
+  const auto tiles = [&](int64_t t) { return (double)((M + t - 1) / t) * (double)((N + t - 1) / t); };
+  const double cells = (double)M * (double)N;
+  double least = 0.0;
+  const auto consider = [&](Matmul8Form form, double step_one, double step_more, double count) {
+    for (int parts = 1; parts <= 16; ++parts) {
+      const int64_t each = (blocks + parts - 1) / parts;
+      if (parts > 1 && (form == kTile256 || each < 4 || parts * cells * sizeof(float) > (1 << 28))) break;
+      const double c = count * parts / 256.0;
+      const double step = form == kTile256 ? (count <= 180 ? step_one : step_more * (double)(int64_t)((count + 255) / 256))
+                                           : step_one + (c > 1.0 ? step_more * (c - 1.0) : 0.0);
+      double t = 3.0 + step * (double)each;
+      if (parts > 1) t += 3.0 + cells * (8.0 * parts + (out_bf16 ? 2.0 : 4.0)) / 4.5e6;
+      if (least == 0.0 || t < least) {
+        least = t;
+        best.form = form;
+        best.each = (int)each;
+        best.parts = (int)((blocks + each - 1) / each);
+      }
     }
+  };
+  if (out_bf16) {
+    consider(kTile64, 0.33, 0.26, tiles(64));
+    consider(kTile128, 0.65, 0.72, tiles(128));
+    consider(kTile256, 1.7, 1.9, tiles(256));
+  } else {
+    consider(kTile64, 0.65, 0.42, tiles(64));
+    consider(kTile128, 1.30, 1.15, tiles(128));
   }
-  return p;
+  return best;
 }
 
 }  // namespace
@@ -501,12 +515,13 @@ static hipError_t matmul8_o(const Matmul8Args& a, hipStream_t stream) {
   const Matmul8Plan p = matmul8_plan(a.M, a.N, a.K, a.out_bf16);
   O* y = static_cast<O*>(a.y);
   if (p.form == kFew) return few<O, 1, 1>(a, stream);
-  if (p.form == kTile128) return tiles<O, O, 4, 4, 2, 2, TILE>(a, p, y, stream);
   if constexpr (sizeof(O) == 2)
     if (p.form == kTile256) return tiles<O, O, 8, 4, 2, 4, TILE>(a, p, y, stream);
-  if (p.parts == 1) return tiles<O, O, 4, 1, 1, 4, TILE>(a, p, y, stream);
+  if (p.parts == 1)
+    return p.form == kTile128 ? tiles<O, O, 4, 4, 2, 2, TILE>(a, p, y, stream) : tiles<O, O, 4, 1, 1, 4, TILE>(a, p, y, stream);
   float* part = static_cast<float*>(a.workspace);
-  const hipError_t e = tiles<O, float, 4, 1, 1, 4, TILE>(a, p, part, stream);
+  const hipError_t e = p.form == kTile128 ? tiles<O, float, 4, 4, 2, 2, TILE>(a, p, part, stream)
+                                          : tiles<O, float, 4, 1, 1, 4, TILE>(a, p, part, stream);
   if (e != hipSuccess) return e;
   const int64_t n = a.M * a.N;
   hipLaunchKernelGGL(matmul8_join_kernel<O>, dim3((unsigned)((n + 1023) / 1024)), dim3(256), 0, stream, part, p.parts, n, y);
