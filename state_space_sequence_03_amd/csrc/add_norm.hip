@@ -120,25 +120,30 @@ block_norm_kernel(const T* __restrict__ x, Strides xs, const R* r, Strides zs,
   }
 }
 
-// A workgroup takes rows first, first + stride, ..., the next one loaded ahead, and keeps its sums of dw in
+// A workgroup takes blockDim.x / tg rows at a time, the next ones loaded ahead, and keeps its sums of dw in
 // registers; it leaves one row of part sums [C] in the workspace.
 template <typename T, typename R, int NV>
 __global__ void __launch_bounds__(512)
 add_norm_bwd_kernel(const R* h, const float* __restrict__ w, const T* __restrict__ dy, const R* dh,
                     T* __restrict__ dx, R* dres, float* __restrict__ part, int64_t rows, int C,
-                    float eps) {
+                    float eps, int tg) {
   __shared__ float lds[16];
-  const int tg = blockDim.x, lane = threadIdx.x;
+  __shared__ float joined[2048];   // several rows at a time have at most 256 threads of 8 channels each
+  const int slot = threadIdx.x / tg, slots = blockDim.x / tg, lane = threadIdx.x % tg;
+  const int64_t step = (int64_t)gridDim.x * slots, mine = (int64_t)blockIdx.x * slots + slot;
+  const int64_t turns = (rows + step - 1) / step;   // as many in every thread: the sums have barriers
   float wt[NV][8], dw[NV][8];
+  Raw8<R> hn[NV], un[NV];
+  Raw8<T> gn[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * tg + lane) * 8;
 #pragma unroll
     for (int e = 0; e < 8; ++e) wt[i][e] = dw[i][e] = 0.0f;
     if (c < C) load8(w + c, C - c, wt[i]);
+    hn[i] = un[i] = Raw8<R>{};
+    gn[i] = Raw8<T>{};
   }
-  Raw8<R> hn[NV], un[NV];   // the next row, loaded while this one is worked on
-  Raw8<T> gn[NV];
   auto load = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -150,23 +155,20 @@ add_norm_bwd_kernel(const R* h, const float* __restrict__ w, const T* __restrict
       }
     }
   };
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    hn[i] = un[i] = Raw8<R>{};
-    gn[i] = Raw8<T>{};
-  }
-  if (blockIdx.x < rows) load(blockIdx.x);
-  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+  if (mine < rows) load(mine);
+  for (int64_t k = 0; k < turns; ++k) {
+    const int64_t row = mine + k * step;
+    const bool live = row < rows;
     float u[NV][8], g[NV][8], up[NV][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         u[i][e] = hn[i][e];
-        g[i][e] = gn[i][e];
+        g[i][e] = live ? gn[i][e] : 0.0f;   // past the last row: nothing for dw
         up[i][e] = un[i][e];
       }
-    if (row + gridDim.x < rows) load(row + gridDim.x);
+    if (row + step < rows) load(row + step);
     float sum[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
@@ -177,27 +179,44 @@ add_norm_bwd_kernel(const R* h, const float* __restrict__ w, const T* __restrict
       }
     group_sum(sum, tg, lds);
     const float r = 1.0f / sqrtf(sum[0] / (float)C + eps);
-    const float k = r * (sum[1] / (float)C);   // mean(t n)
+    const float m = r * (sum[1] / (float)C);   // mean(t n)
+    if (live) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = (i * tg + lane) * 8;
-      float o[8];
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * tg + lane) * 8;
+        float o[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float n = u[i][e] * r;
-        dw[i][e] = fmaf(g[i][e], n, dw[i][e]);
-        o[e] = fmaf(r, g[i][e] * wt[i][e] - n * k, up[i][e]);
-      }
-      if (c < C) {
-        if (dx) store8(dx + row * C + c, C - c, o);
-        if (dres) store8(dres + row * C + c, C - c, o);
+        for (int e = 0; e < 8; ++e) {
+          const float n = u[i][e] * r;
+          dw[i][e] = fmaf(g[i][e], n, dw[i][e]);
+          o[e] = fmaf(r, g[i][e] * wt[i][e] - n * m, up[i][e]);
+        }
+        if (c < C) {
+          if (dx) store8(dx + row * C + c, C - c, o);
+          if (dres) store8(dres + row * C + c, C - c, o);
+        }
       }
     }
   }
+  if (slots == 1) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * tg + lane) * 8;
-    if (c < C) store8(part + (int64_t)blockIdx.x * C + c, C - c, dw[i]);
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tg + lane) * 8;
+      if (c < C) store8(part + (int64_t)blockIdx.x * C + c, C - c, dw[i]);
+    }
+    return;
+  }
+  if constexpr (NV == 1) {   // the rows side by side, added in order
+    for (int q = 0; q < slots; ++q) {
+      if (slot == q)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int c = lane * 8 + e;
+          joined[c] = q == 0 ? dw[0][e] : joined[c] + dw[0][e];
+        }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x; c < C; c += blockDim.x) part[(int64_t)blockIdx.x * C + c] = joined[c];
   }
 }
 
@@ -262,20 +281,27 @@ ItemGrid item_grid(int64_t rows, int64_t S, int64_t G, bool gate) {
   return g;
 }
 
-// The gradients: one piece per thread up to 512 of them, and as many workgroups as give each CU 256
-// threads or one workgroup: more only make more part sums (8192 x 2560 in 256 of 320 threads 66 us, 512 73,
-// 1024 82; 40960 x 512 in 1024 of 64 threads 74, 512 104, 2048 88).
+// The gradients: one piece per thread up to 512 of them, two beyond; small rows side by side in workgroups of
+// up to 512 threads; and workgroups until 20 KB of inputs are on their way to each CU, at most 1280 threads:
+// more only make more part sums (8192 x 2560 with an fp32 residual, one workgroup per CU 66 us, two 73,
+// four 82; one row of 128 channels at a time, 145388 x 128 in bf16 181 us, 32 at a time 39).
 struct BwdGrid {
-  int nv, threads;
+  int nv, tg, threads;
   int64_t stripes;
 };
-BwdGrid bwd_grid(int64_t rows, int64_t C) {
+BwdGrid bwd_grid(int64_t rows, int64_t C, int bf16, int res_bf16) {
   BwdGrid g;
   const int pieces = (int)((C + 7) / 8);
   g.nv = pieces > 512 ? 2 : 1;
-  g.threads = (pieces + g.nv * kWave - 1) / (g.nv * kWave) * kWave;
-  g.stripes = 256 * (g.threads < 256 ? 256 / g.threads : 1);
-  if (g.stripes > rows) g.stripes = rows;
+  g.tg = pieces <= 16 ? 16 : pieces <= 32 ? 32 : (pieces + g.nv * kWave - 1) / (g.nv * kWave) * kWave;
+  const int slots = g.tg <= 256 ? 512 / g.tg : 1;
+  g.threads = g.tg * slots;
+  const int64_t bytes = ((bf16 ? 2 : 4) + (res_bf16 ? 4 : 8)) * C * slots;
+  int64_t each = (20 * 1024 + bytes - 1) / bytes;
+  if (each * g.threads > 1280) each = 1280 / g.threads;
+  g.stripes = 256 * each;
+  const int64_t most = (rows + slots - 1) / slots;
+  if (g.stripes > most) g.stripes = most;
   return g;
 }
 
@@ -290,8 +316,8 @@ int block_norm_grid_ok(int64_t batch, int64_t L, int64_t C, int64_t G) {
   return (__int128)batch * L * 512 < (int64_t(1) << 32) && g.sets <= 65535;
 }
 
-size_t add_norm_bwd_workspace(int64_t rows, int64_t C) {
-  return size_t(bwd_grid(rows, C).stripes) * C * sizeof(float);
+size_t add_norm_bwd_workspace(int64_t rows, int64_t C, int bf16, int res_bf16) {
+  return size_t(bwd_grid(rows, C, bf16, res_bf16).stripes) * C * sizeof(float);
 }
 
 template <typename T, typename R, int FORM>
@@ -327,13 +353,13 @@ hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t stream) {
 
 template <typename T, typename R>
 static hipError_t add_norm_bwd_t(const AddNormBwdArgs& a, hipStream_t stream) {
-  const BwdGrid g = bwd_grid(a.rows, a.C);
+  const BwdGrid g = bwd_grid(a.rows, a.C, a.bf16, a.res_bf16);
   float* part = static_cast<float*>(a.workspace);
   auto go = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)g.stripes), dim3(g.threads), 0, stream,
                        static_cast<const R*>(a.h), a.w, static_cast<const T*>(a.dy),
                        static_cast<const R*>(a.dh), static_cast<T*>(a.dx), static_cast<R*>(a.dres),
-                       part, a.rows, (int)a.C, a.eps);
+                       part, a.rows, (int)a.C, a.eps, g.tg);
   };
   if (g.nv == 1) go(add_norm_bwd_kernel<T, R, 1>);
   else go(add_norm_bwd_kernel<T, R, 2>);

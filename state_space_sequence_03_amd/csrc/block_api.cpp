@@ -178,7 +178,8 @@ ssd_status ssd_add_norm_bwd_workspace_size(const ssd_add_norm_problem* prob, siz
     ssd_status st = add_norm_shape(*prob);
     if (st == SSD_OK) st = add_norm_supported(*prob);
     if (st != SSD_OK) return st;
-    *bytes = add_norm_bwd_workspace(prob->batch * prob->seqlen, prob->channels);
+    *bytes = add_norm_bwd_workspace(prob->batch * prob->seqlen, prob->channels, prob->io_dtype == SSD_BF16,
+                                    prob->residual_dtype == SSD_BF16);
     return ok();
   });
 }
@@ -200,7 +201,7 @@ ssd_status ssd_add_norm_bwd(const ssd_add_norm_problem* prob, const void* h, con
     AddNormBwdArgs a{};
     a.rows = p.batch * p.seqlen;
     a.C = p.channels;
-    const size_t need = add_norm_bwd_workspace(a.rows, a.C);
+    const size_t need = add_norm_bwd_workspace(a.rows, a.C, p.io_dtype == SSD_BF16, p.residual_dtype == SSD_BF16);
     if (workspace_bytes < need)
       return fail(SSD_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
     a.eps = p.eps;

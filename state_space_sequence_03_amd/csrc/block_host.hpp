@@ -41,7 +41,7 @@ struct AddNormBwdArgs {
   void* workspace;
 };
 hipError_t launch_add_norm_bwd(const AddNormBwdArgs& a, hipStream_t stream);
-size_t add_norm_bwd_workspace(int64_t rows, int64_t C);
+size_t add_norm_bwd_workspace(int64_t rows, int64_t C, int bf16, int res_bf16);
 
 struct Quant8Args {
   int64_t batch, L, C;
