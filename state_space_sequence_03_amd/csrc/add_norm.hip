@@ -242,7 +242,7 @@ struct ItemGrid {
 //   threads 100, 5 pieces in one wave 109; four tokens in a row 94, sixteen 100;
 //   gates also keep the vector ALU busy: 1, 2, 4 or 8 waves (three or five leave a SIMD with less:
 //   16384 x 5120, 320 threads of 2 pieces 144 us), the fewest idle lanes first (128 threads of 5 pieces
-//   104, 256 of 3 111), and as many tokens in a row as make one round of workgroups, up to 16 (128 of 5
+//   104, 256 of 3 111), and as many tokens in a row, up to 16, as make whole rounds of workgroups (128 of 5
 //   pieces: one token 131, eight 121, sixteen 104; 16384 x 2048 in 128 of 2: one 50, eight 43, sixteen 52).
 ItemGrid item_grid(int64_t rows, int64_t S, int64_t G, bool gate) {
   constexpr int kWavesPerSimd[6] = {0, 6, 4, 3, 3, 2};   // of the gated kernels, by their registers
@@ -274,9 +274,13 @@ ItemGrid item_grid(int64_t rows, int64_t S, int64_t G, bool gate) {
   g.each = step;
   if (many) {
     const int64_t groups = 256 * (int64_t)(4 * kWavesPerSimd[g.nv] * kWave / g.threads) / g.sets;   // at once
-    int64_t each = groups > 0 ? (rows + groups - 1) / groups : 16 * step;
-    each = (each + step - 1) / step * step;
-    g.each = (int)(each < 16 * step ? each : 16 * step);
+    if (groups > 0) {
+      const int64_t rounds = (rows + groups * 16 * step - 1) / (groups * 16 * step);
+      const int64_t each = (rows + groups * rounds - 1) / (groups * rounds);
+      g.each = (int)((each + step - 1) / step * step);
+    } else {
+      g.each = 16 * step;
+    }
   }
   return g;
 }
