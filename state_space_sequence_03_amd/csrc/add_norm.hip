@@ -100,19 +100,18 @@ block_norm_kernel(const T* __restrict__ x, Strides xs, const R* r, Strides zs,
         store8(y + row * C + c, S - c, o);
       }
       if (q) {
-        // y / m does not depend on r: what is quantised is t = y / r, in two parts, and r joins the scale.
+        // y / m does not depend on r: what is quantised is t = y / r, and r joins the scale.  Behind a gate,
+        // whose own roundings are of the size of its product's, t is one number; else it is two.
         float t[8], rest[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float v = FORM == kNormFirst ? u[i][e] * gate[FORM == kNormFirst ? i : 0][e] : u[i][e];
-          t[e] = v * wt[i][e];
-          rest[e] = fmaf(v, wt[i][e], -t[e]);
-          if constexpr (FORM == kNormFirst)
-            rest[e] = fmaf(fmaf(u[i][e], gate[i][e], -v), wt[i][e], rest[e]);
+          t[e] = u[i][e] * wt[i][e];
+          if constexpr (FORM == kAdd) rest[e] = fmaf(u[i][e], wt[i][e], -t[e]);
+          if constexpr (FORM == kNormFirst) t[e] *= gate[i][e];
         }
         const float m = fmaxf(most_of_16(most_of(t)), kLeast8 / rr);
         if (live && c < padded) {
-          *reinterpret_cast<uint2*>(q + row * P + c0 + c) = pack8(t, rest, m);
+          *reinterpret_cast<uint2*>(q + row * P + c0 + c) = FORM == kAdd ? pack8(t, rest, m) : pack8<float>(t, m);
           if (lane % 16 == 0) scale[(int64_t)((c0 + c) / kBlock8) * rows + row] = m * rr / kMost8;
         }
       }
