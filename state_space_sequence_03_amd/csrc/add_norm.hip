@@ -10,7 +10,11 @@
 // tokens of dy n;  mean(t n) = r mean(t h), so one reduction gives both sums.
 //
 // Bound by HBM: every input is read once, a token's elements stay in registers between
-// the sum and the outputs, in pieces of eight channels, NV per thread.
+// the sum and the outputs, in pieces of eight channels, NV per thread.  The gates (an exp2
+// and a reciprocal per element, quarter rate) keep the vector ALU busy beside it.
+// bf16 with an fp32 residual, 2 x 8192 x 2560 to 8 bits 87 us (5.3 TB/s of the 5.07 that a
+// large copy reaches: more is read than written), gradients over 2 x 4096 66 us (5.1 TB/s, 5 of
+// them part sums); gated norm of 2 x 8192 x 5120 to 8 bits 101 us (4.2 TB/s).
 #include "block_device.hpp"
 #include "block_host.hpp"
 

@@ -5,7 +5,9 @@
 // even, scale = m / 448.  A block is 128 elements of a row (of a column, for the transposed
 // form), or a tile of 128 x 128 that both forms share.
 //
-// Bound by HBM: each element is read once and written once or twice as a byte.
+// Bound by HBM: each element is read once and written once or twice as a byte.  2 x 4096 x 5120
+// bf16 both ways 41 us (4.1 TB/s of the 5.07 that a large copy reaches), rows alone 29 us; an fp32
+// weight of 10576 x 2560 by tiles, both ways, 33 us (4.9 TB/s).
 #include "block_device.hpp"
 #include "block_host.hpp"
 
@@ -13,7 +15,8 @@ namespace ssd {
 
 // A workgroup of 256 threads takes a tile of 128 x 128; thread t holds the patch of rows
 // 8 (t / 16) .. + 8 and columns 8 (t % 16) .. + 8, so that 16 lanes read whole rows of the
-// tile, and eight rows of a column are one 8-byte piece of the transposed form.
+// tile, and eight rows of a column are one 8-byte piece of the transposed form.  Held as it was
+// read, a bf16 patch takes 32 registers and six waves fit a SIMD (widened: 64, four, 48 us for 42).
 template <typename T, bool TILE>
 __global__ void __launch_bounds__(256)
 quant_tile_kernel(const T* __restrict__ x, Strides xs, unsigned char* __restrict__ q,
