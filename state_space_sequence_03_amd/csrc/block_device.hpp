@@ -125,7 +125,7 @@ __device__ __forceinline__ float most_of_16(float m) {
 }
 
 // 448 / m in two parts, to about 2^-44 of it: the hardware reciprocal (of m / 448, which stays normal) and
-// what it leaves of 448.  `bits` of them in the first part.  An infinite m gives 0.
+// what it leaves of 448.  SHORT: 16 bits in the first part.  An infinite m gives 0.
 struct Inverse8 {
   float hi, lo;
 };
