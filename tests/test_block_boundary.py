@@ -10,6 +10,7 @@ import torch
 
 import state_space_sequence_03_amd as lib
 from state_space_sequence_03_amd import block, layer
+from test_boundary import LLVM, device_disassembly, device_functions
 from test_host_asan import CLANG_RT, HIPCC, _instrumented, _run_child
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -246,3 +247,48 @@ def test_host_code_under_asan(tmp_path):
                    capture_output=True, text=True)
     assert _instrumented(so)
     _run_child(["tests/test_block_boundary.py"], {"LD_PRELOAD": CLANG_RT[-1], "SSD_LIBRARY": so})
+
+
+# ---- the built device code ----
+
+@pytest.mark.skipif(not os.path.exists("%s/llvm-objdump" % LLVM), reason="ROCm LLVM tools not installed")
+@pytest.mark.parametrize("obj", ["add_norm.o", "quant8.o", "matmul8.o", "clip.o"])
+def test_device_code(so, obj, tmp_path):
+    # M0 is written for the direct-to-LDS loads alone, each write followed by its load; nothing is written
+    # through the scalar data cache, no packed fp32 operation is there, and no register goes to memory
+    # (spilled ones would be vector memory operations that the products' waits do not count)
+    insts = device_disassembly(obj, tmp_path)
+    assert insts, "no device code found"
+    for k, ins in enumerate(insts):
+        op = ins.split()[0] if ins else ""
+        assert not re.match(r"s_(store|atomic|buffer_store|buffer_atomic|scratch_store|dcache_wb|dcache_discard)", op), ins
+        assert not re.match(r"v_pk_(add|mul|fma)_f32", op) and not op.startswith("scratch_"), ins
+        fields = [f.strip() for f in ins[len(op):].split(",")]
+        if fields and fields[0] == "m0" and op.startswith("s_"):
+            nxt = [i for i in insts[k + 1:k + 3] if not i.startswith("s_nop")]
+            assert nxt and nxt[0].startswith("global_load_lds"), (obj, ins, insts[k + 1:k + 3])
+    if obj == "matmul8.o":
+        assert any(i.startswith("global_load_lds_dwordx4") for i in insts) and not any(i.startswith("s_bfe_i64") for i in insts)
+
+
+@pytest.mark.skipif(not os.path.exists("%s/llvm-objdump" % LLVM), reason="ROCm LLVM tools not installed")
+def test_products_wait_for_counted_loads(so, tmp_path):
+    # The loop of the tiled products waits for all but a counted number of its latest loads: two waits in a
+    # block of the depth, with kFirst + kHalfN loads between two of the same kind.  Every other vector memory
+    # operation of the kernel lies behind the loop (the stores of y), so that the counts hold.
+    funcs = {f: i for f, i in device_functions("matmul8.o", tmp_path).items() if "14matmul8_kernel" in f}
+    # <results, y, NT, MT, WN, WM, by tile>: loads of a block for one wave
+    loads = {"Li8ELi4ELi2ELi4E": 2 * 4 // 2 + 1 + 2 * (8 // 4), "Li4ELi4ELi2ELi2E": 2 * 4 // 2 + 1 + 2 * (4 // 2),
+             "Li4ELi1ELi1ELi4E": 2 * 1 // 1 + 1 + 2 * (4 // 4)}
+    seen = set()
+    for name, insts in funcs.items():
+        kind = next(k for k in loads if k in name)
+        seen.add(kind)
+        waits = [k for k, i in enumerate(insts) if re.match(r"s_waitcnt vmcnt\(%d\) lgkmcnt\(0\)" % loads[kind], i)]
+        assert len(waits) == 3, (name, len(waits))          # in front of the loop, and two in it
+        lds = [k for k, i in enumerate(insts) if i.startswith("global_load_lds")]
+        others = [k for k, i in enumerate(insts) if re.match(r"(global|flat|buffer)_(load|store)", i) and k not in lds]
+        assert min(others) > max(lds), name
+        in_loop = [k for k in lds if k > waits[0]]
+        assert len(in_loop) == loads[kind], (name, len(in_loop))
+    assert seen == set(loads)
