@@ -116,12 +116,23 @@ __device__ __forceinline__ float most_of(const float (&v)[8]) {
   for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
   return m;
 }
-// The largest over the lanes that share `lane / 16`, in all of them: a block of 128 in
-// pieces of eight.
-__device__ __forceinline__ float most_of_16(float m) {
-#pragma unroll
-  for (int off = 8; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 16));
+// The largest over the lanes that share `lane / 16`, in all of them: a block of 128 in pieces of eight.
+// Rotations of the 16 lanes ride on the max itself; numbers >= 0 are in the order of their bits.
+__device__ __forceinline__ uint32_t most_of_16(uint32_t m) {
+  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x128, 0xf, 0xf, true));   // by 8
+  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x124, 0xf, 0xf, true));
+  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x122, 0xf, 0xf, true));
+  m = max(m, (uint32_t)__builtin_amdgcn_mov_dpp((int)m, 0x121, 0xf, 0xf, true));   // by 1
   return m;
+}
+__device__ __forceinline__ float most_of_16(float m) {
+  return __builtin_bit_cast(float, most_of_16(__builtin_bit_cast(uint32_t, m)));
+}
+
+// m / 448 for 2^-100 <= m, correctly rounded: the quotient by the reciprocal, and what it leaves of m joined to it.
+__device__ __forceinline__ float scale_of(float m) {
+  const float s = m * (1.0f / kMost8), left = fmaf(-s, kMost8, m);
+  return m < __builtin_inff() ? fmaf(left, 1.0f / kMost8, s) : m;
 }
 
 // 448 / m in two parts, to about 2^-44 of it: the hardware reciprocal (of m / 448, which stays normal) and
@@ -143,16 +154,14 @@ template <bool SHORT> __device__ __forceinline__ Inverse8 inverse8(float m) {
 // falls on the wrong side of the middle between two e4m3 values only within half a step of fp32 of it.  A
 // bf16 value times the 16 bits of a short first part is exact; others carry their rounding error along.
 __device__ __forceinline__ uint2 convert8(const float (&p)[8]) {
-  uint2 r;
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(p[0], p[1], 0, false);
-  r.x = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(p[2], p[3], w, true);
-  w = __builtin_amdgcn_cvt_pk_fp8_f32(p[4], p[5], 0, false);
-  r.y = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(p[6], p[7], w, true);
-  return r;
+  auto four = [&](int i) {   // the first pair's registers take the other half of the word: any value will do
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(p[i], p[i + 1], __builtin_bit_cast(int, p[i]), false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(p[i + 2], p[i + 3], w, true);
+  };
+  return make_uint2(four(0), four(4));
 }
-template <typename T> __device__ __forceinline__ uint2 pack8(const float (&v)[8], float m) {
-  constexpr bool kShort = sizeof(T) == 2;
-  const Inverse8 by = inverse8<kShort>(m);
+template <typename T> __device__ __forceinline__ uint2 pack8(const float (&v)[8], Inverse8 by) {
+  constexpr bool kShort = sizeof(T) == 2;   // `by` is short too
   float p[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
@@ -160,6 +169,9 @@ template <typename T> __device__ __forceinline__ uint2 pack8(const float (&v)[8]
     p[e] = kShort ? fmaf(v[e], by.lo, h) : h + fmaf(v[e], by.lo, fmaf(v[e], by.hi, -h));
   }
   return convert8(p);
+}
+template <typename T> __device__ __forceinline__ uint2 pack8(const float (&v)[8], float m) {
+  return pack8<T>(v, inverse8<sizeof(T) == 2>(m));
 }
 // The same of values v + rest.
 __device__ __forceinline__ uint2 pack8(const float (&v)[8], const float (&rest)[8], float m) {

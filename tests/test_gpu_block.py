@@ -196,6 +196,37 @@ def test_quant8_extremes(dtype):
     assert torch.isnan(cols.q.double()[5, 3]) and torch.isnan(cols.q.double()[130, 4])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quant8_tile_leaves_nan_out(dtype):
+    d = Draw(31)
+    x = d.normal(140, 260).to(dtype)
+    x[7, 9], x[7, 10], x[131, 3], x[20, 200] = float("nan"), -float("nan"), float("nan"), float("-inf")
+    for rows, cols in (lib.ssd_quant8(x, tile=True, want_cols=True), lib.ssd_quant8(x, want_cols=True)):
+        for got, m in ((rows, x), (cols, x.t())):
+            q, bad = got.q.double()[:, :m.shape[1]], torch.isnan(m)
+            assert torch.isnan(q[bad]).all()
+            assert not torch.isnan(q[~bad & ~torch.isinf(m)]).any()
+    rows, cols = lib.ssd_quant8(x, tile=True, want_cols=True)
+    v = x.double().cpu().nan_to_num(nan=0.0)
+    for r in range(2):
+        for c in range(3):
+            most = v[128 * r:128 * r + 128, 128 * c:128 * c + 128].abs().max()
+            assert rows.scale[c, r] == cols.scale[r, c] == (most / 448).float()
+
+
+@pytest.mark.parametrize("length", [1, 3, 7, 8, 9, 130])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_quant8_short_sequences(length, dtype):
+    """Patches of rows that run over the ends of sequences, with strides of their own."""
+    d = Draw(32 + length)
+    x = d.normal(37, length + 2, 150).to(dtype)[::2, 1:length + 1, :131]
+    flat_x = x.reshape(-1, 131).contiguous()
+    for tile in (False, True):
+        for got, want in zip(lib.ssd_quant8(x, tile=tile, want_cols=True), lib.ssd_quant8(flat_x, tile=tile, want_cols=True)):
+            assert torch.equal(got.q.flatten(0, -2).view(torch.uint8), want.q.view(torch.uint8))
+            assert torch.equal(got.scale, want.scale)
+
+
 # ---- matrix product ----
 
 # rows, cols, depth
