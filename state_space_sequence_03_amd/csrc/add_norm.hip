@@ -14,7 +14,7 @@
 // and a reciprocal per element, quarter rate) keep the vector ALU busy beside it.
 // bf16 with an fp32 residual, 2 x 8192 x 2560 to 8 bits 87 us (5.3 TB/s of the 5.07 that a
 // large copy reaches: more is read than written), gradients over 2 x 4096 66 us (5.1 TB/s, 5 of
-// them part sums); gated norm of 2 x 8192 x 5120 to 8 bits 101 us (4.2 TB/s).
+// them part sums); gated norm of 2 x 8192 x 5120 to 8 bits 90 us (4.7 TB/s).
 #include "block_device.hpp"
 #include "block_host.hpp"
 
@@ -93,7 +93,7 @@ block_norm_kernel(const T* __restrict__ x, Strides xs, const R* r, Strides zs,
     }
     if (row + step < last) load(row + step);
     group_sum(sum, tg, lds);
-    const float rr = 1.0f / sqrtf(sum[0] / (float)S + eps);
+    const float root = sqrtf(sum[0] / (float)S + eps), rr = 1.0f / root;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tg + lane) * 8;
@@ -113,10 +113,10 @@ block_norm_kernel(const T* __restrict__ x, Strides xs, const R* r, Strides zs,
           if constexpr (FORM == kAdd) rest[e] = fmaf(u[i][e], wt[i][e], -t[e]);
           if constexpr (FORM == kNormFirst) t[e] *= gate[i][e];
         }
-        const float m = fmaxf(most_of_16(most_of(t)), kLeast8 / rr);
+        const float m = fmaxf(most_of_16(most_of(t)), kLeast8 * root);
         if (live && c < padded) {
-          *reinterpret_cast<uint2*>(q + row * P + c0 + c) = FORM == kAdd ? pack8(t, rest, m) : pack8<float>(t, m);
-          if (lane % 16 == 0) scale[(int64_t)((c0 + c) / kBlock8) * rows + row] = m * rr / kMost8;
+          *reinterpret_cast<uint2*>(q + row * P + c0 + c) = FORM == kAdd ? pack8(t, rest, m) : pack8_once(t, m);
+          if (lane % 16 == 0) scale[(int64_t)((c0 + c) / kBlock8) * rows + row] = scale_of(m * rr);
         }
       }
     }
@@ -243,12 +243,11 @@ struct ItemGrid {
 //   the addition, which waits for memory alone, takes as many waves as give each thread one piece (two
 //   past 512), and one token for each: 16384 x 2560 to 8 bits 93 us; 2 pieces 95, 3 pieces and half the
 //   threads 100, 5 pieces in one wave 109; four tokens in a row 94, sixteen 100;
-//   gates also keep the vector ALU busy: 1, 2, 4 or 8 waves (three or five leave a SIMD with less:
-//   16384 x 5120, 320 threads of 2 pieces 144 us), the fewest idle lanes first (128 threads of 5 pieces
-//   104, 256 of 3 111), and as many tokens in a row, up to 16, as make whole rounds of workgroups (128 of 5
-//   pieces: one token 131, eight 121, sixteen 104; 16384 x 2048 in 128 of 2: one 50, eight 43, sixteen 52).
+//   gates also keep the vector ALU busy: 1, 2, 4 or 8 waves (three or five leave a SIMD with less) of up to
+//   three pieces per thread, the fewest idle lanes first (256 threads of 3 pieces 92 us, 128 of 5 95, 512 of 2
+//   114, 320 of 2 105), and two tokens in a row: more of them make whole rounds of workgroups that load, compute
+//   and store in step (256 of 3: four 90, but 16384 x 8 x 512 70 in place of 67, 2048 x 5120 17 in place of 16).
 ItemGrid item_grid(int64_t rows, int64_t S, int64_t G, bool gate) {
-  constexpr int kWavesPerSimd[6] = {0, 6, 4, 3, 3, 2};   // of the gated kernels, by their registers
   ItemGrid g;
   const int pieces = (int)((S + kBlock8 - 1) / kBlock8 * (kBlock8 / 8));
   const bool many = gate && rows * G >= 1024;
@@ -261,7 +260,7 @@ ItemGrid item_grid(int64_t rows, int64_t S, int64_t G, bool gate) {
     g.tg = 0;
     for (int tg = 512; tg >= kWave; tg /= 2) {
       const int nv = (pieces + tg - 1) / tg;
-      if (nv > 5 || (nv == 1 && tg > kWave)) continue;
+      if (nv > 3 || (nv == 1 && tg > kWave)) continue;
       if (g.tg == 0 || tg * nv < g.tg * g.nv) {
         g.tg = tg;
         g.nv = nv;
@@ -273,18 +272,7 @@ ItemGrid item_grid(int64_t rows, int64_t S, int64_t G, bool gate) {
   if (many && g.tg == kWave) slots = 4;
   g.threads = g.tg * slots;
   g.sets = G == 1 ? 1 : (G + slots - 1) / slots;
-  const int step = G == 1 ? slots : 1;
-  g.each = step;
-  if (many) {
-    const int64_t groups = 256 * (int64_t)(4 * kWavesPerSimd[g.nv] * kWave / g.threads) / g.sets;   // at once
-    if (groups > 0) {
-      const int64_t rounds = (rows + groups * 16 * step - 1) / (groups * 16 * step);
-      const int64_t each = (rows + groups * rounds - 1) / (groups * rounds);
-      g.each = (int)((each + step - 1) / step * step);
-    } else {
-      g.each = 16 * step;
-    }
-  }
+  g.each = (G == 1 ? slots : 1) * (many ? 2 : 1);
   return g;
 }
 
@@ -341,9 +329,7 @@ static hipError_t block_norm_f(const BlockNormArgs& a, hipStream_t stream) {
   if (g.nv == 1) go(block_norm_kernel<T, R, 1, FORM>);
   else if (g.nv == 2) go(block_norm_kernel<T, R, 2, FORM>);
   else if constexpr (FORM != kAdd) {
-    if (g.nv == 3) go(block_norm_kernel<T, R, 3, FORM>);
-    else if (g.nv == 4) go(block_norm_kernel<T, R, 4, FORM>);
-    else go(block_norm_kernel<T, R, 5, FORM>);
+    go(block_norm_kernel<T, R, 3, FORM>);
   }
   return hipGetLastError();
 }

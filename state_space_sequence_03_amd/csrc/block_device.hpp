@@ -173,6 +173,15 @@ template <typename T> __device__ __forceinline__ uint2 pack8(const float (&v)[8]
 template <typename T> __device__ __forceinline__ uint2 pack8(const float (&v)[8], float m) {
   return pack8<T>(v, inverse8<sizeof(T) == 2>(m));
 }
+// The same of values with roundings of their own: by 448 / m in fp32, which adds half a step or less to them.
+__device__ __forceinline__ uint2 pack8_once(const float (&v)[8], float m) {
+  const Inverse8 by = inverse8<false>(m);
+  const float one = by.hi + by.lo;
+  float p[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) p[e] = v[e] * one;
+  return convert8(p);
+}
 // The same of values v + rest.
 __device__ __forceinline__ uint2 pack8(const float (&v)[8], const float (&rest)[8], float m) {
   const Inverse8 by = inverse8<false>(m);
