@@ -15,6 +15,8 @@
 // scaling into the sums 45; a library's product of the same operands with one scale for all 425 us;
 // the card's best rate there, at 8192 x 8192 x 8192, 2.84 PFLOP/s).  Few rows are bound by the
 // weight's way from memory: one row, 10576 x 2560, 7.1 us, 3.8 TB/s.
+#include <cmath>
+#include <initializer_list>
 #include <type_traits>
 
 #include "block_device.hpp"
@@ -330,7 +332,7 @@ matmul8_kernel(const unsigned char* __restrict__ x, const float* __restrict__ xs
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       a = Frag8<O>::of(an);
-      if (i + 1 == NT / 2) arrived(acc[NT / 2 - 2][0]);
+      if (i + 1 == NT / 2) arrived(acc[NT / 2 > 2 ? NT / 2 - 2 : 0][0]);
       if (i + 1 == NT) arrived(acc[NT - 2][0]);
       an = i + 1 < NT ? read_n(b, i + 1) : read_n(b + 1, 0);
       // loads, a few between any two reads: many in a row would hold the wave up
@@ -411,6 +413,7 @@ matmul8_join_kernel(const float* __restrict__ part, int parts, int64_t n, O* __r
   if (i >= n) return;
   const int left = (int)(n - i < 4 ? n - i : 4);
   floatx4 s = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
   for (int p = 0; p < parts; ++p) {
     const float* q = part + p * n + i;
     if (left == 4) {
@@ -436,16 +439,19 @@ struct Matmul8Plan {
 
 // How a product is computed.  Up to 16 rows, each wave takes its own blocks straight from memory (1 x 10576 x
 // 2560 7.1 us, in tiles of 64 x 64 9).  Beyond that the form and the parts of the depth whose time, by what was
-// measured, is the least.  With c tiles (times parts) for each CU, a step of 128 in the depth takes (us)
-//                 bf16 results                          fp32 results
-//   64 x 64       0.33, and 0.26 (c - 1) more past one   0.65, 0.42
-//   128 x 128     0.65, 0.72                             1.30, 1.15
-//   256 x 256     1.7, 1.9 ceil(c) past 180 tiles        (their operands take twice the registers)
-// a launch 3, and a split depth 3 more and the parts' way through memory at 4.5 TB/s.  Measured against it:
-//   512 x 2560 x 5120 in tiles of 64 18.8 (18.8), of 128 25.8 (29); 256 x 10576 x 2560 16.4 (18), 15.2 (16);
-//   2048 x 10576 x 2560 in tiles of 128 73 (76), of 256 74 (79); 4096 x 10576 x 2560 146 (151), 117 (117);
-//   128 x 2560 x 5120 whole 14.8 (16), in three parts 11.6 (12.5); fp32 1111 x 770 x 2176 whole 14.4 (14), in two
-//   17 (17); fp32 1500 x 1500 x 16384 in tiles of 128 whole 162 (169), in four parts 106 (104).
+// measured, is the least.  A step of 128 in the depth takes a CU (us) for as many tiles (times parts) as it has, at
+// most those that fit it at once, and again for those behind them:
+//                 bf16 results                 fp32 results
+//   64 x 64       0.33, 0.42, 0.60, 0.80       0.49, 0.70, 0.98, 1.25  (64 x 16 a wave, not 32 x 32: 0.65, 1.07)
+//   128 x 128     0.70, 1.10                   1.33, 1.95
+//   256 x 256     1.9 (1.7 on up to 180 CUs)   (their operands take twice the registers)
+// a launch 3, and a split depth 3 more, 0.15 for each part, and the parts' way through memory at 4.5 TB/s.
+// Measured against it:
+//   512 x 2560 x 5120 in tiles of 64 19.6 (19.8), of 128 29 (31); 256 x 10576 x 2560 16.9 (15), 17.3 (17);
+//   2048 x 2560 x 5120 47 (48), 43 (47); 2048 x 10576 x 2560 in tiles of 128 73 (69), of 256 79 (79);
+//   4096 x 10576 x 2560 146 (127), 117 (117); 128 x 2560 x 5120 whole 15.6 (16), in three parts 12.4 (13);
+//   fp32 1111 x 770 x 2176 whole 11.7 (11), in two 16 (16); fp32 1500 x 1500 x 16384 in tiles of 128 whole 163
+//   (173), in three parts 92 (104).
 Matmul8Plan matmul8_plan(int64_t M, int64_t N, int64_t K, int out_bf16) {
   const int64_t blocks = K / kBlock8;
   Matmul8Plan best{kFew, 1, (int)blocks};
@@ -453,15 +459,15 @@ Matmul8Plan matmul8_plan(int64_t M, int64_t N, int64_t K, int out_bf16) {
   const auto tiles = [&](int64_t t) { return (double)((M + t - 1) / t) * (double)((N + t - 1) / t); };
   const double cells = (double)M * (double)N;
   double least = 0.0;
-  const auto consider = [&](Matmul8Form form, double step_one, double step_more, double count) {
+  const auto consider = [&](Matmul8Form form, double count, std::initializer_list<double> steps) {
     for (int parts = 1; parts <= 16; ++parts) {
       const int64_t each = (blocks + parts - 1) / parts;
       if (parts > 1 && (form == kTile256 || each < 4 || parts * cells * sizeof(float) > (1 << 28))) break;
-      const double c = count * parts / 256.0;
-      const double step = form == kTile256 ? (count <= 180 ? step_one : step_more * (double)(int64_t)((count + 255) / 256))
-                                           : step_one + (c > 1.0 ? step_more * (c - 1.0) : 0.0);
+      const double c = std::ceil(count * parts / 256.0), rounds = std::floor(c / (double)steps.size());
+      const int rest = (int)(c - rounds * (double)steps.size());
+      const double step = rounds * steps.end()[-1] + (rest ? steps.begin()[rest - 1] : 0.0);
       double t = 3.0 + step * (double)each;
-      if (parts > 1) t += 3.0 + cells * (8.0 * parts + (out_bf16 ? 2.0 : 4.0)) / 4.5e6;
+      if (parts > 1) t += 3.0 + 0.15 * parts + cells * (8.0 * parts + (out_bf16 ? 2.0 : 4.0)) / 4.5e6;
       if (least == 0.0 || t < least) {
         least = t;
         best.form = form;
@@ -471,12 +477,12 @@ Matmul8Plan matmul8_plan(int64_t M, int64_t N, int64_t K, int out_bf16) {
     }
   };
   if (out_bf16) {
-    consider(kTile64, 0.33, 0.26, tiles(64));
-    consider(kTile128, 0.65, 0.72, tiles(128));
-    consider(kTile256, 1.7, 1.9, tiles(256));
+    consider(kTile64, tiles(64), {0.33, 0.42, 0.60, 0.80});
+    consider(kTile128, tiles(128), {0.70, 1.10});
+    consider(kTile256, tiles(256), {tiles(256) <= 180 ? 1.7 : 1.9});
   } else {
-    consider(kTile64, 0.65, 0.42, tiles(64));
-    consider(kTile128, 1.30, 1.15, tiles(128));
+    consider(kTile64, tiles(64), {0.49, 0.70, 0.98, 1.25});
+    consider(kTile128, tiles(128), {1.33, 1.95});
   }
   return best;
 }
@@ -527,10 +533,10 @@ static hipError_t matmul8_o(const Matmul8Args& a, hipStream_t stream) {
   if constexpr (sizeof(O) == 2)
     if (p.form == kTile256) return tiles<O, O, 8, 4, 2, 4, TILE>(a, p, y, stream);
   if (p.parts == 1)
-    return p.form == kTile128 ? tiles<O, O, 4, 4, 2, 2, TILE>(a, p, y, stream) : tiles<O, O, 4, 1, 1, 4, TILE>(a, p, y, stream);
+    return p.form == kTile128 ? tiles<O, O, 4, 4, 2, 2, TILE>(a, p, y, stream) : tiles<O, O, 2, 2, 2, 2, TILE>(a, p, y, stream);
   float* part = static_cast<float*>(a.workspace);
   const hipError_t e = p.form == kTile128 ? tiles<O, float, 4, 4, 2, 2, TILE>(a, p, part, stream)
-                                          : tiles<O, float, 4, 1, 1, 4, TILE>(a, p, part, stream);
+                                          : tiles<O, float, 2, 2, 2, 2, TILE>(a, p, part, stream);
   if (e != hipSuccess) return e;
   const int64_t n = a.M * a.N;
   hipLaunchKernelGGL(matmul8_join_kernel<O>, dim3((unsigned)((n + 1023) / 1024)), dim3(256), 0, stream, part, p.parts, n, y);

@@ -279,7 +279,7 @@ def test_products_wait_for_counted_loads(so, tmp_path):
     funcs = {f: i for f, i in device_functions("matmul8.o", tmp_path).items() if "14matmul8_kernel" in f}
     # <results, y, NT, MT, WN, WM, by tile>: loads of a block for one wave
     loads = {"Li8ELi4ELi2ELi4E": 2 * 4 // 2 + 1 + 2 * (8 // 4), "Li4ELi4ELi2ELi2E": 2 * 4 // 2 + 1 + 2 * (4 // 2),
-             "Li4ELi1ELi1ELi4E": 2 * 1 // 1 + 1 + 2 * (4 // 4)}
+             "Li2ELi2ELi2ELi2E": 2 * 2 // 2 + 1 + 2 * (2 // 2)}
     seen = set()
     for name, insts in funcs.items():
         kind = next(k for k in loads if k in name)
