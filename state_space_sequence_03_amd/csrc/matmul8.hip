@@ -438,7 +438,9 @@ struct Matmul8Plan {
 };
 
 // How a product is computed.  Up to 16 rows, each wave takes its own blocks straight from memory (1 x 10576 x
-// 2560 7.1 us, in tiles of 64 x 64 9).  Beyond that the form and the parts of the depth whose time, by what was
+// 2560 7.1 us, in tiles of 64 x 64 9; more of them on their way at once change nothing), and up to 32 where one
+// workgroup for each CU does and the depth is not large (32 x 2560 x 5120 9.7, in tiles 10.2; 20 x 4096 x 5120 8.5,
+// 11.6; but 32 x 4096 x 8192 13.7, 13.0; 32 x 10576 x 2560 13.2, 9.6).  Beyond that the form and the parts of the depth whose time, by what was
 // measured, is the least.  A step of 128 in the depth takes a CU (us) for as many tiles (times parts) as it has, at
 // most those that fit it at once, and again for those behind them:
 //                 bf16 results                 fp32 results
@@ -455,7 +457,7 @@ struct Matmul8Plan {
 Matmul8Plan matmul8_plan(int64_t M, int64_t N, int64_t K, int out_bf16) {
   const int64_t blocks = K / kBlock8;
   Matmul8Plan best{kFew, 1, (int)blocks};
-  if (M <= 16) return best;
+  if (M <= 16 || (M <= 32 && N <= 4096 && K <= 5120)) return best;
   const auto tiles = [&](int64_t t) { return (double)((M + t - 1) / t) * (double)((N + t - 1) / t); };
   const double cells = (double)M * (double)N;
   double least = 0.0;
@@ -529,7 +531,7 @@ template <typename O, bool TILE>
 static hipError_t matmul8_o(const Matmul8Args& a, hipStream_t stream) {
   const Matmul8Plan p = matmul8_plan(a.M, a.N, a.K, a.out_bf16);
   O* y = static_cast<O*>(a.y);
-  if (p.form == kFew) return few<O, 1, 1>(a, stream);
+  if (p.form == kFew) return a.M <= 16 ? few<O, 1, 1>(a, stream) : few<O, 1, 2>(a, stream);
   if constexpr (sizeof(O) == 2)
     if (p.form == kTile256) return tiles<O, O, 8, 4, 2, 4, TILE>(a, p, y, stream);
   if (p.parts == 1)

@@ -233,6 +233,7 @@ def test_quant8_short_sequences(length, dtype):
 PRODUCT = [(1, 1, 128), (1, 130, 256), (3, 31, 384), (16, 33, 1152), (17, 257, 128), (63, 128, 2176), (64, 129, 640),
            (65, 32, 1280), (128, 300, 2560), (129, 384, 256), (200, 10, 4096), (257, 513, 384), (300, 1000, 1024), (513, 260, 128),
            (1000, 770, 2176), (1024, 1024, 512), (640, 2563, 256), (2, 2000, 5120),
+           (32, 100, 1152), (31, 4096, 640), (32, 4097, 256), (20, 33, 5248), (29, 1, 5120),
            # tiles of 128 x 128 and of 256 x 256 with ragged ends, of one block and more
            (1500, 1701, 384), (1409, 1793, 128), (2559, 4095, 128), (2559, 4093, 640)]
 
