@@ -6,7 +6,7 @@
 // form), or a tile of 128 x 128 that both forms share.
 //
 // Bound by HBM: each element is read once and written once or twice as a byte.  2 x 4096 x 5120
-// bf16 both ways 38 us (4.5 TB/s of the 5.07 that a large copy reaches), rows alone 27 us; an fp32
+// bf16 both ways 39 us (4.3 TB/s of the 5.07 that a large copy reaches), rows alone 27 us; an fp32
 // weight of 10576 x 2560 by tiles, both ways, 33 us (4.9 TB/s).
 #include "block_device.hpp"
 #include "block_host.hpp"
@@ -59,7 +59,7 @@ template <> struct Bits8<float> {
 // read, a bf16 patch takes 32 registers and eight waves fit a SIMD (widened, an earlier form had four, 48 us for 42).
 // The vector ALU is busy for half of the time that the memory takes, so whatever belongs to a row or a column
 // (a scale, a column's inverse) is computed once, magnitudes are compared as integers, and addresses are counted
-// on from row to row: 38 us in place of 41.  Stores past the caches took 37, and the product that reads them 6 more.
+// on from row to row: 39 us in place of 41.  Stores past the caches took 37, and the product that reads them 6 more.
 template <typename T, bool TILE>
 __global__ void __launch_bounds__(256)
 quant_tile_kernel(const T* __restrict__ x, Strides xs, unsigned char* __restrict__ q,
