@@ -136,23 +136,23 @@ __device__ __forceinline__ float scale_of(float m) {
 }
 
 // 448 / m in two parts, to about 2^-44 of it: the hardware reciprocal (of m / 448, which stays normal) and
-// what it leaves of 448.  SHORT: 16 bits in the first part.  An infinite m gives 0.
+// what it leaves of 448.  An infinite m gives 0.
 struct Inverse8 {
   float hi, lo;
 };
-template <bool SHORT> __device__ __forceinline__ Inverse8 inverse8(float m) {
-  const float r = __builtin_amdgcn_rcpf(m * (1.0f / kMost8));
+__device__ __forceinline__ Inverse8 inverse8(float m) {
   Inverse8 by;
-  by.hi = SHORT ? __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, r) & 0xffffff00u) : r;
-  const float lo = fmaf(-by.hi, m, kMost8) * (r * (1.0f / kMost8));
+  by.hi = __builtin_amdgcn_rcpf(m * (1.0f / kMost8));
+  const float lo = fmaf(-by.hi, m, kMost8) * (by.hi * (1.0f / kMost8));
   by.lo = by.hi == 0.0f ? 0.0f : lo;
   return by;
 }
 
 // v 448 / m as e4m3, to nearest even, for eight values: at most 448 (1 + 2^-23), which rounds to 448, so
-// nothing has to be cut off.  The products are rounded once, to fp32, in front of the conversion, so a value
-// falls on the wrong side of the middle between two e4m3 values only within half a step of fp32 of it.  A
-// bf16 value times the 16 bits of a short first part is exact; others carry their rounding error along.
+// nothing has to be cut off.  What the second part adds goes into the fma with the first, so the sum is
+// rounded once, to fp32, in front of the conversion, and a value falls on the wrong side of the middle between
+// two e4m3 values only within half a step of fp32 of it.  (Written as a product and additions of what it lost, the
+// compiler contracts the last of them with the product, and the loss counts twice.)
 __device__ __forceinline__ uint2 convert8(const float (&p)[8]) {
   auto four = [&](int i) {   // the first pair's registers take the other half of the word: any value will do
     const int w = __builtin_amdgcn_cvt_pk_fp8_f32(p[i], p[i + 1], __builtin_bit_cast(int, p[i]), false);
@@ -160,22 +160,16 @@ __device__ __forceinline__ uint2 convert8(const float (&p)[8]) {
   };
   return make_uint2(four(0), four(4));
 }
-template <typename T> __device__ __forceinline__ uint2 pack8(const float (&v)[8], Inverse8 by) {
-  constexpr bool kShort = sizeof(T) == 2;   // `by` is short too
+__device__ __forceinline__ uint2 pack8(const float (&v)[8], Inverse8 by) {
   float p[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float h = v[e] * by.hi;
-    p[e] = kShort ? fmaf(v[e], by.lo, h) : h + fmaf(v[e], by.lo, fmaf(v[e], by.hi, -h));
-  }
+  for (int e = 0; e < 8; ++e) p[e] = fmaf(v[e], by.hi, v[e] * by.lo);
   return convert8(p);
 }
-template <typename T> __device__ __forceinline__ uint2 pack8(const float (&v)[8], float m) {
-  return pack8<T>(v, inverse8<sizeof(T) == 2>(m));
-}
+__device__ __forceinline__ uint2 pack8(const float (&v)[8], float m) { return pack8(v, inverse8(m)); }
 // The same of values with roundings of their own: by 448 / m in fp32, which adds half a step or less to them.
 __device__ __forceinline__ uint2 pack8_once(const float (&v)[8], float m) {
-  const Inverse8 by = inverse8<false>(m);
+  const Inverse8 by = inverse8(m);
   const float one = by.hi + by.lo;
   float p[8];
 #pragma unroll
@@ -184,13 +178,10 @@ __device__ __forceinline__ uint2 pack8_once(const float (&v)[8], float m) {
 }
 // The same of values v + rest.
 __device__ __forceinline__ uint2 pack8(const float (&v)[8], const float (&rest)[8], float m) {
-  const Inverse8 by = inverse8<false>(m);
+  const Inverse8 by = inverse8(m);
   float p[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float h = v[e] * by.hi;
-    p[e] = h + fmaf(rest[e], by.hi, fmaf(v[e], by.lo, fmaf(v[e], by.hi, -h)));
-  }
+  for (int e = 0; e < 8; ++e) p[e] = fmaf(v[e], by.hi, fmaf(rest[e], by.hi, v[e] * by.lo));
   return convert8(p);
 }
 

@@ -127,7 +127,7 @@ quant_tile_kernel(const T* __restrict__ x, Strides xs, unsigned char* __restrict
     if (t % kWave == 0) col_most[t / kWave][0] = most;
     __syncthreads();
     most = fmaxf(fmaxf(fmaxf(col_most[0][0], col_most[1][0]), fmaxf(col_most[2][0], col_most[3][0])), kLeast8);
-    tile_by = inverse8<sizeof(T) == 2>(most);
+    tile_by = inverse8(most);
     if (t == 0) {
       if (q) scale[tc * nr + tr] = scale_of(most);
       if (qt) scale_t[tr * nc + tc] = scale_of(most);
@@ -145,10 +145,10 @@ quant_tile_kernel(const T* __restrict__ x, Strides xs, unsigned char* __restrict
       Inverse8 by = tile_by;
       if constexpr (!TILE) {
         const float m = fmaxf(Bits::value(most_of_16(row_bits[i])), kLeast8);
-        by = inverse8<sizeof(T) == 2>(m);
+        by = inverse8(m);
         mine = pc == i ? m : mine;
       }
-      if (i < high) *reinterpret_cast<uint2*>(to) = pack8<T>(o, by);
+      if (i < high) *reinterpret_cast<uint2*>(to) = pack8(o, by);
       to += pitch;
     }
     if (!TILE && pc < 8 && pc < high) scale[tc * rows + r0 + 8 * pr + pc] = scale_of(mine);
@@ -171,7 +171,7 @@ quant_tile_kernel(const T* __restrict__ x, Strides xs, unsigned char* __restrict
     __syncthreads();
     if (t < kBlock8) {
       const float m = fmaxf(fmaxf(fmaxf(col_most[0][t], col_most[1][t]), fmaxf(col_most[2][t], col_most[3][t])), kLeast8);
-      col_by[t] = inverse8<sizeof(T) == 2>(m);
+      col_by[t] = inverse8(m);
       if (c0 + t < C) scale_t[tr * C + c0 + t] = scale_of(m);
     }
     __syncthreads();
@@ -184,7 +184,7 @@ quant_tile_kernel(const T* __restrict__ x, Strides xs, unsigned char* __restrict
     for (int i = 0; i < 8; ++i) col[i] = v[i][e];
     // Column k's 16 pieces lie in places permuted by pc = k / 8, so the 64 lanes of a write
     // touch every bank alike; the permutation keeps pairs of pieces together.
-    turned[k * 16 + (pr ^ pc)] = pack8<T>(col, TILE ? tile_by : col_by[k]);
+    turned[k * 16 + (pr ^ pc)] = pack8(col, TILE ? tile_by : col_by[k]);
   }
   __syncthreads();
   unsigned char* to = qt + (c0 + t / 8) * nr * kBlock8 + r0 + 16 * (t % 8);
@@ -215,7 +215,7 @@ quant_rows_kernel(const T* __restrict__ x, Strides xs, unsigned char* __restrict
   for (int e = 0; e < 8; ++e) v[e] = 0.0f;
   if (c < C) load8(x + row_at(xs, row, L) + c, (int)(C - c < 8 ? C - c : 8), v);
   const float m = fmaxf(most_of_16(most_of(v)), kLeast8);
-  *reinterpret_cast<uint2*>(q + row * nc * kBlock8 + c) = pack8<T>(v, m);
+  *reinterpret_cast<uint2*>(q + row * nc * kBlock8 + c) = pack8(v, m);
   if (threadIdx.x % 16 == 0) scale[b * rows + row] = scale_of(m);
 }
 

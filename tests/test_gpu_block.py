@@ -604,3 +604,78 @@ def test_options_are_taken_by_value():
     eps.fill_(4.0)
     assert torch.equal(first, lib.ssd_add_norm_fwd(x, None, w, eps=0.25)[0])
     assert torch.equal(lib.ssd_add_norm_fwd(x, None, w, eps=eps)[0], lib.ssd_add_norm_fwd(x, None, w, eps=4.0)[0])
+
+
+# ---- 8-bit values beside the middles ----
+
+def beside_middles(m, steps=2):
+    """fp32 values up to `steps` steps to either side of every middle of two e4m3 values of a block whose
+    magnitude is m."""
+    mid = (ref.E4M3[:-1] + ref.E4M3[1:]) / 2 * (m / ref.MOST)
+    near = mid.astype(np.float32)
+    out = [near]
+    for side in (0.0, np.inf):
+        v = near
+        for _ in range(steps):
+            v = np.nextafter(v, np.float32(side), dtype=np.float32)
+            out.append(v)
+    v = np.concatenate(out)
+    return np.concatenate([v, -v])
+
+
+def middles_matrix(m):
+    """128 x 128 of such values, with a magnitude of m in every row and column."""
+    v = beside_middles(m)
+    x = np.resize(v, (128, 128))
+    x[0], x[:, 0] = m, -m
+    return torch.from_numpy(x)
+
+
+@pytest.mark.parametrize("m", [1.0, 448.0, 1.7, 3.3e-4, 2.0 ** -100, 1.9 * 2.0 ** -99, 2.3e9, 3.0e38])
+def test_quant8_beside_middles(m):
+    # 448 / m in two parts is off by 2^-44 of it (2^-31 where the second is subnormal, m past 2^104), its product with v by
+    # half a step of fp32: d = 1.01 e.  By rows alone, by rows and transposed, by tiles.
+    x = middles_matrix(np.float32(m)).cuda()
+    v = f(x)
+    in8(lib.ssd_quant8(x)[0].q, ref.blocks(v)[0], 1, "rows alone")
+    for tile in (False, True):
+        rows, cols = lib.ssd_quant8(x, tile=tile, want_cols=True)
+        in8(rows.q, ref.blocks(v, 128 if tile else 1)[0], 1, "rows")
+        in8(cols.q, ref.blocks(v.T, 128 if tile else 1)[0], 1, "cols")
+
+
+@pytest.mark.parametrize("m", [1.0, 1.7, 3.3e-4, 1e-12, 3e8])
+def test_add_norm_8bit_beside_middles(m):
+    # a weight of 1: h is what is quantised, and its largest is exact (1 e); any weight: the block's magnitude is a
+    # product rounded to fp32 (2 e)
+    x = middles_matrix(np.float32(m)).cuda()[None]
+    w = torch.ones(128, device="cuda")
+    y8 = lib.ssd_add_norm_fwd(x, None, w, want_y=False, want_8bit=True)[1]
+    in8(y8.q, ref.blocks(flat(ref.norm(x, w)))[0], 1, "q")
+    w = Draw(41).uniform(0.5, 2.0, 128)
+    w[0] = 2.0
+    x = (x.double() / w * 2.0).float()
+    y8 = lib.ssd_add_norm_fwd(x, None, w, want_y=False, want_8bit=True)[1]
+    in8(y8.q, ref.blocks(flat(ref.norm(x, w)))[0], 2, "q, any weight")
+
+
+def test_quant8_of_bf16_is_exact():
+    # with v and m of 8 bits, v 448 / m is the middle of two e4m3 values or at least 2^-13 of it away from every one: to
+    # nearest, ties to even, of the exact quotient (in 64 bits one rounding of v 448, which is exact, by m)
+    most = np.arange(128, 256) / 128.0
+    near = (np.arange(128, 256)[:, None] / 128.0 * 2.0 ** -np.arange(20)[None]).reshape(-1)
+    rows = []
+    for m in most:
+        v = near[near <= m]
+        v = np.resize(np.concatenate([v, -v]), (-(-2 * len(v) // 127), 127))
+        rows.append(np.concatenate([np.full((len(v), 1), m), v], 1))
+    v = np.concatenate(rows)
+    x = torch.from_numpy(v).bfloat16().cuda()
+    assert np.array_equal(f(x), v)
+    want = ref.nearest8(v * ref.MOST / np.abs(v).max(1, keepdims=True))
+    ties = sum(np.isin(np.abs(v * ref.MOST) / np.abs(v).max(1, keepdims=True), (ref.E4M3[:-1] + ref.E4M3[1:]) / 2).reshape(-1))
+    assert ties > 1000
+    for got in (lib.ssd_quant8(x)[0].q, lib.ssd_quant8(x, want_cols=True)[0].q):
+        assert np.array_equal(f(got), want)
+    xt = x.t().contiguous()
+    assert np.array_equal(f(lib.ssd_quant8(xt, want_rows=False, want_cols=True)[1].q), want)
