@@ -93,7 +93,19 @@ block_norm_kernel(const T* __restrict__ x, Strides xs, const R* r, Strides zs,
     }
     if (row + step < last) load(row + step);
     group_sum(sum, tg, lds);
-    const float root = sqrtf(sum[0] / (float)S + eps), rr = 1.0f / root;
+    float root = sqrtf(sum[0] / (float)S + eps), rr = 1.0f / root;
+    if (q && root < 0x1p-9f) {
+      // Far below 1 (with an eps below 2^-18) t, and with it the least magnitude of a block, would leave the range in
+      // which 448 / m is finite and values are normal; brought to [1, 2) by a power of two, which changes no digit.
+      const uint32_t power = __builtin_bit_cast(uint32_t, root) >> 23;   // biased; 0 for a root of 0 alone
+      const float up = __builtin_bit_cast(float, (254 - power) << 23);
+      root *= up;
+      rr = 1.0f / root;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[i][e] *= up;
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tg + lane) * 8;

@@ -679,3 +679,60 @@ def test_quant8_of_bf16_is_exact():
         assert np.array_equal(f(got), want)
     xt = x.t().contiguous()
     assert np.array_equal(f(lib.ssd_quant8(xt, want_rows=False, want_cols=True)[1].q), want)
+
+
+# ---- zeros behind a norm in 8 bits ----
+
+def zeros_and_tiny(d, C, eps, io):
+    """Tokens of zeros (with an eps), of blocks of zeros, and of small and tiny values."""
+    h = d.normal(12, C)
+    h[1:4] *= torch.tensor([1e-3, 1e-8, 1e-15], device="cuda")[:, None]
+    h[:4, 128:256] = 0.0
+    h[4], h[5] = 0.0, 0.0
+    h[4, 7], h[5, 300] = 3e-9, 1.0
+    if eps > 0:
+        h[6], h[8] = 0.0, h[8] * 1e-30
+        h[7] *= 1e-37
+        h[7, :128] = 0.0
+    return h.to(io)[None].contiguous()
+
+
+def check_zeros(y8, yr, count):
+    # behind the least magnitude the root of the mean does not drop out of the quantised value: 100 e more
+    scaled, scale, m = ref.blocks(flat(yr))
+    floor = m <= ref.LEAST * 1.001
+    in8(y8.q, scaled, np.where(floor, count + 100, count), "q")
+    within(y8.scale, scale, 100, scale, "scale")
+    got = f(y8.q).reshape(scaled.shape)
+    assert (got[scaled == 0] == 0).all() and (scaled.reshape(len(scaled), -1, 128) == 0).all(2).any()
+
+
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("eps", [1e-5, 1e-12, 0.0])
+@pytest.mark.parametrize("C", [384, 2600])
+def test_add_norm_8bit_of_zeros(C, eps, io):
+    d = Draw(42)
+    h, w = zeros_and_tiny(d, C, eps, io), d.normal(C, std=0.3) + 1.0
+    for weight in (w, torch.where(torch.arange(C, device="cuda") // 128 == 2, 0.0, w)):
+        y, y8, _ = lib.ssd_add_norm_fwd(h, None, weight, eps=eps, want_8bit=True)
+        yr = ref.norm(h, weight, eps)
+        within(y, yr, 100, np.abs(yr), "y")
+        check_zeros(y8, yr, 2)
+
+
+@pytest.mark.parametrize("before", [False, True])
+@pytest.mark.parametrize("io", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("eps", [1e-5, 1e-12, 0.0])
+@pytest.mark.parametrize("C,groups", [(384, 1), (384, 3), (2600, 1)])
+def test_gated_norm_8bit_of_zeros(C, groups, eps, io, before):
+    d = Draw(43)
+    x, z, w = zeros_and_tiny(d, C, eps, io), d.normal(1, 12, C).to(io), d.normal(C, std=0.3) + 1.0
+    z[0, 9, 256:] = 0.0
+    z[0, 10, 128:256] = -200.0       # its sigmoid is 0 in fp32, and the value below half of the least e4m3 one in 64 bits
+    if groups == 3:                  # with eps 0 a group has to have a value that is not 0
+        x = torch.where(x == 0, torch.tensor(1e-9, device="cuda").to(io), x) if eps == 0 else x
+        z = torch.where((z == 0) | (z == -200.0), torch.ones_like(z), z) if eps == 0 else z
+        w[128:256] = 0.0
+    for gate in (z, None):
+        y8 = lib.ssd_gated_norm_fwd_8bit(x, gate, w, ngroups=groups, eps=eps, norm_before_gate=before)
+        check_zeros(y8, ref.gated(x, gate, w, groups, eps, before), 100)
