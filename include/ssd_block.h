@@ -160,8 +160,9 @@ ssd_status ssd_matmul8(const ssd_matmul8_problem* prob, const void* x, const flo
  *     norm = grad_scale sqrt(sum g^2)
  *     c    = grad_scale min(1, max_norm / (norm + eps)), grad_scale where norm is not finite
  *     out  = g c
- * The sum is 64-bit; c is rounded to fp32, and out once to its type.  A caller that
- * skips a step whose norm is not finite finds that in `norm`.
+ * The sum is 64-bit; c is rounded to fp32, and out once to its type.  Whether the norm is
+ * finite goes by its rounding to fp32, which is what `norm` holds: a caller that skips a step
+ * whose norm is not finite finds that there.
  */
 typedef struct {
   const void* grad;  /* contiguous, aligned to its element */

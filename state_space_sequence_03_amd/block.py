@@ -367,8 +367,8 @@ def ssd_clip_grads(grads: Sequence[torch.Tensor], max_norm: float, *, scale: flo
     fp32 tensor of no axes on their device (before clipping, after ``scale``).
 
     Every gradient is multiplied by scale min(1, max_norm / (norm + eps)) with norm = scale
-    sqrt(sum of all squares); by ``scale`` alone where the norm is not finite, or with max_norm
-    infinite.  Contiguous bf16 and fp32 tensors in any mixture; ``out`` may have other dtypes
+    sqrt(sum of all squares); by ``scale`` alone where the norm that is returned is not finite, or
+    with max_norm infinite.  Contiguous bf16 and fp32 tensors in any mixture; ``out`` may have other dtypes
     than ``grads`` (bf16 gradients into an optimizer's fp32 buffer)."""
     lib = load_library()
     grads = list(grads)

@@ -1,7 +1,7 @@
 // clip.hip -- the global norm over many gradients, and clipping by it.
 //
 //     norm = s sqrt(sum g^2),  out = g s min(1, most / (norm + eps))   (s alone where the
-//     norm is not finite)
+//     norm, rounded to fp32, is not finite)
 //
 // Bound by HBM: every gradient is read twice, since no factor is known before the last
 // one has been read, and written once: 241 M bf16 gradients into fp32 411 us, 1.93 GB at
@@ -119,7 +119,7 @@ clip_scale_kernel(const Tensors t, const double* __restrict__ part, int64_t part
   const double norm = scale * sqrt(parts_sum(part, parts));
   if (first_launch && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
   double c = scale;
-  if (norm < INFINITY) c *= fmin(1.0, most / (norm + eps));   // false for NaN
+  if ((float)norm < INFINITY) c *= fmin(1.0, most / (norm + eps));   // finite as it is reported; false for NaN
   const float by = (float)c;
   const int b = gridDim.x - 1 - blockIdx.x;   // the last chunks first: they may still be in a cache
   const int k = tensor_of(t, b);

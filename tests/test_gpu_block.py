@@ -736,3 +736,19 @@ def test_gated_norm_8bit_of_zeros(C, groups, eps, io, before):
     for gate in (z, None):
         y8 = lib.ssd_gated_norm_fwd_8bit(x, gate, w, ngroups=groups, eps=eps, norm_before_gate=before)
         check_zeros(y8, ref.gated(x, gate, w, groups, eps, before), 100)
+
+
+# ---- clipping past fp32 ----
+
+def test_clip_grads_norm_past_fp32():
+    # between fp32's largest and the 64-bit range the norm that is returned is infinite: the scale alone is applied
+    big = torch.full((4,), 3e38, device="cuda")
+    for out in (None, [torch.empty(4, device="cuda")], [torch.empty(4, dtype=torch.bfloat16, device="cuda")]):
+        for scale in (1.0, 0.5):   # norms 6e38 and 3e38
+            g = [big.clone()]
+            norm = lib.ssd_clip_grads(g, 1.0, scale=scale, out=out)
+            got = (g if out is None else out)[0].double().cpu()
+            if scale == 1.0:
+                assert norm == float("inf") and torch.equal(got, big.to((g if out is None else out)[0].dtype).double().cpu())
+            else:   # 0.5 / 3e38 is subnormal in fp32: off by half a step of 2^-149
+                assert abs(float(norm) / 3e38 - 1) < 1e-6 and (abs(got - 0.5) <= 0.5 * 2.0 ** -8 * (out is not None) + 1e-6).all()
