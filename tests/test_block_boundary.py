@@ -179,6 +179,39 @@ def test_matmul8_pointers():
     assert size_of("ssd_matmul8_workspace_size", MP())[0] == OK
 
 
+def test_products_of_every_form_are_tested(tmp_path):
+    # every form of the plan, its depth whole and split, for results in bf16 and in fp32, has sizes among those that
+    # the GPU tests run (by tile and by row each)
+    from test_gpu_block import PRODUCT, PRODUCT_128
+    src = tmp_path / "plan.cpp"
+    src.write_text('#include <cstdio>\n#include "matmul8_plan.hpp"\n'
+                   'int main() {\n  long long m, n, k;\n  int bf16;\n'
+                   '  while (std::scanf("%lld %lld %lld %d", &m, &n, &k, &bf16) == 4) {\n'
+                   '    const ssd::Matmul8Plan p = ssd::matmul8_plan(m, n, k, bf16);\n'
+                   '    std::printf("%d %d %d\\n", (int)p.form, p.parts, p.each);\n  }\n}\n')
+    exe = str(tmp_path / "plan")
+    csrc = os.path.join(ROOT, "state_space_sequence_03_amd", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-Wall", "-Werror", "-I" + csrc, str(src), "-o", exe], check=True)
+    cases = [(size, bf16) for size in PRODUCT + PRODUCT_128 for bf16 in (0, 1)]
+    text = "".join("%d %d %d %d\n" % (size + (bf16,)) for size, bf16 in cases)
+    out = subprocess.run([exe], input=text, capture_output=True, text=True, check=True).stdout.split("\n")[:-1]
+    seen = {}
+    for (size, bf16), line in zip(cases, out):
+        form, parts, each = (int(v) for v in line.split())
+        blocks = size[2] // 128
+        assert (parts - 1) * each < blocks <= parts * each, (size, line)
+        # the library's own plan: its workspace holds the parts
+        need = 4 * parts * size[0] * size[1] if parts > 1 else 0
+        assert size_of("ssd_matmul8_workspace_size", MP(*size, out=bf16)) == (OK, need), (size, line)
+        seen.setdefault((["few", 64, 128, 256][form], parts > 1, bf16), []).append(size)
+    want = {("few", False, b) for b in (0, 1)} | {(t, split, b) for t in (64, 128) for split in (False, True) for b in (0, 1)}
+    assert set(seen) == want | {(256, False, 1)}, sorted(seen, key=str)
+    # more than one block of the depth, and ends of both sides inside a tile, in every one of the tiled forms
+    for (form, split, _), sizes in seen.items():
+        if form != "few":
+            assert any(k > 128 for _, _, k in sizes) and any(m % form and n % form for m, n, _ in sizes), (form, split, sizes)
+
+
 # ---- clipping ----
 
 def clip(items, n=None, most=1.0, eps=1e-6, scale=1.0, reserved=0, norm=PTR << 8, ws=PTR << 9, ws_bytes=BIG, none=None):

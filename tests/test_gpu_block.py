@@ -752,3 +752,23 @@ def test_clip_grads_norm_past_fp32():
                 assert norm == float("inf") and torch.equal(got, big.to((g if out is None else out)[0].dtype).double().cpu())
             else:   # 0.5 / 3e38 is subnormal in fp32: off by half a step of 2^-149
                 assert abs(float(norm) / 3e38 - 1) < 1e-6 and (abs(got - 0.5) <= 0.5 * 2.0 ** -8 * (out is not None) + 1e-6).all()
+
+
+# ---- every tile of the plan ----
+
+# Sizes of the forms and splits that PRODUCT leaves out, as csrc/matmul8_plan.hpp has it (test_block_boundary.py asks it):
+# tiles of 128 x 128, of the whole depth and of parts of it, for results in bf16 and in fp32
+PRODUCT_128 = [(1921, 1537, 128), (1793, 2049, 640), (1090, 1025, 8192), (2049, 3001, 128), (2049, 3001, 384), (1090, 1793, 8192)]
+
+
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("tile", [True, False])
+@pytest.mark.parametrize("size", PRODUCT_128, ids=str)
+def test_matmul8_tiles_of_128(size, tile, out):
+    x, w = operands(*size, tile)
+    n = size[0] * size[1]
+    room = torch.full((n + 8192,), 7.0, dtype=IO[out], device="cuda")
+    y = lib.ssd_matmul8(x, w, out_dtype=IO[out], out=room[:n].view(size[:2]))
+    want, mag = ref.matmul(x.q, x.scale, w.q, w.scale, tile)
+    within(y, want, ROUGH if out == "bf16" else matmul_count(size[2]), mag, "y")
+    assert (room[n:] == 7.0).all() and torch.equal(y, lib.ssd_matmul8(x, w, out_dtype=IO[out]))
