@@ -69,8 +69,9 @@ typedef struct {
  *   h        : [batch, seqlen, channels] residual dtype, or NULL; may be `residual`.
  *   y        : [batch, seqlen, channels] io dtype, or NULL.
  *   q, scale : the 8-bit y by row (rows = batch * seqlen, depth = channels), or both NULL.
- * One of y and q at least.  Errors: UNSUPPORTED for more than 8192 channels, or sizes past a
- * launch's 2^32 threads. */
+ * One of y and q at least.  Errors: UNSUPPORTED for more than 8192 channels or 2^31 - 1 tokens, or
+ * sizes past a launch's 2^32 threads: a token of up to 128 channels takes 16, of up to 256 takes 32,
+ * beyond that at most 64 for each 512 channels. */
 ssd_status ssd_add_norm_fwd(const ssd_add_norm_problem* prob, const void* x,
                             const ssd_strides* x_strides, const void* residual,
                             const float* weight, void* h, void* y, void* q, float* scale,
@@ -85,14 +86,16 @@ ssd_status ssd_add_norm_bwd_workspace_size(const ssd_add_norm_problem* prob, siz
  *   dresidual : [batch, seqlen, channels] residual dtype, or NULL; may be `dh`.  The same
  *               gradient as dx, rounded to its own type.
  *   dweight   : [channels] fp32.
- * One of dx and dresidual at least. */
+ * One of dx and dresidual at least.  Errors: UNSUPPORTED for more than 8192 channels or 2^31 - 1
+ * tokens. */
 ssd_status ssd_add_norm_bwd(const ssd_add_norm_problem* prob, const void* h, const float* weight,
                             const void* dy, const void* dh, void* dx, void* dresidual,
                             float* dweight, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ssd_gated_norm_fwd with the output in 8 bits, by row (rows = batch * seqlen, depth =
  * channels).  Errors beside those of ssd_gated_norm_fwd: UNSUPPORTED for more than one
- * group whose channels are not whole blocks of 128. */
+ * group whose channels are not whole blocks of 128, and past ssd_add_norm_fwd's limits of tokens
+ * and threads (a group's channels in place of a token's). */
 ssd_status ssd_gated_norm_fwd_8bit(const ssd_gated_norm_problem* prob, const void* x,
                                    const void* z, const ssd_strides* z_strides,
                                    const float* weight, void* q, float* scale, void* stream);

@@ -317,10 +317,12 @@ BwdGrid bwd_grid(int64_t rows, int64_t C, int bf16, int res_bf16) {
 // 512 threads hold 2 x 8 elements each.
 int64_t block_norm_limit() { return 8192; }
 
-int block_norm_grid_ok(int64_t batch, int64_t L, int64_t C, int64_t G) {
+// Rows are counted in 31 bits, and the launch has fewer than 2^32 threads along its first axis.
+int block_norm_grid_ok(int64_t batch, int64_t L, int64_t C, int64_t G, int gate) {
   if (C > (1 << 24) || batch > INT32_MAX / L) return 0;
-  const ItemGrid g = item_grid(1, C / G, G, false);   // one token for each workgroup: the most
-  return (__int128)batch * L * 512 < (int64_t(1) << 32) && g.sets <= 65535;
+  const int64_t rows = batch * L;
+  const ItemGrid g = item_grid(rows, C / G, G, gate != 0);
+  return (rows + g.each - 1) / g.each * g.threads < (int64_t(1) << 32) && g.sets <= 65535;
 }
 
 size_t add_norm_bwd_workspace(int64_t rows, int64_t C, int bf16, int res_bf16) {

@@ -38,11 +38,13 @@ ssd_status add_norm_shape(const ssd_add_norm_problem& p) {
   if (!(p.eps >= 0.0f) || std::isinf(p.eps)) return fail(SSD_ERR_BAD_VALUE, "eps must be finite and >= 0");
   return SSD_OK;
 }
-ssd_status add_norm_supported(const ssd_add_norm_problem& p) {
+// `launch`: of the forward pass, whose workgroups grow with the tokens (those of the gradients do not).
+ssd_status add_norm_supported(const ssd_add_norm_problem& p, bool launch) {
   if (p.channels > block_norm_limit())
     return fail(SSD_ERR_UNSUPPORTED, "at most %lld channels (got %lld)", (long long)block_norm_limit(),
                 (long long)p.channels);
-  if (!block_norm_grid_ok(p.batch, p.seqlen, p.channels, 1))
+  if (p.batch > kMostRows / p.seqlen) return fail(SSD_ERR_UNSUPPORTED, "at most 2^31 - 1 tokens");
+  if (launch && !block_norm_grid_ok(p.batch, p.seqlen, p.channels, 1, 0))
     return fail(SSD_ERR_UNSUPPORTED, "grid too large for this build");
   return SSD_OK;
 }
@@ -151,7 +153,7 @@ ssd_status ssd_add_norm_fwd(const ssd_add_norm_problem* prob, const void* x,
       return fail(SSD_ERR_MISALIGNED, "x must have the alignment of its element");
     if (!aligned16(residual, weight, h, y, q, scale))
       return fail(SSD_ERR_MISALIGNED, "every other tensor pointer must be 16-byte aligned");
-    st = add_norm_supported(p);
+    st = add_norm_supported(p, true);
     if (st != SSD_OK) return st;
     a.batch = p.batch;
     a.L = p.seqlen;
@@ -176,7 +178,7 @@ ssd_status ssd_add_norm_bwd_workspace_size(const ssd_add_norm_problem* prob, siz
   return guarded([&] {
     if (!prob || !bytes) return fail(SSD_ERR_NULL_POINTER, "prob and bytes must not be NULL");
     ssd_status st = add_norm_shape(*prob);
-    if (st == SSD_OK) st = add_norm_supported(*prob);
+    if (st == SSD_OK) st = add_norm_supported(*prob, false);
     if (st != SSD_OK) return st;
     *bytes = add_norm_bwd_workspace(prob->batch * prob->seqlen, prob->channels, prob->io_dtype == SSD_BF16,
                                     prob->residual_dtype == SSD_BF16);
@@ -196,7 +198,7 @@ ssd_status ssd_add_norm_bwd(const ssd_add_norm_problem* prob, const void* h, con
     if (st != SSD_OK) return st;
     if (!aligned16(h, weight, dy, dh, dx, dresidual, dweight, workspace))
       return fail(SSD_ERR_MISALIGNED, "every tensor pointer must be 16-byte aligned");
-    st = add_norm_supported(p);
+    st = add_norm_supported(p, false);
     if (st != SSD_OK) return st;
     AddNormBwdArgs a{};
     a.rows = p.batch * p.seqlen;
@@ -244,7 +246,7 @@ ssd_status ssd_gated_norm_fwd_8bit(const ssd_gated_norm_problem* prob, const voi
     if (p.ngroups > 1 && p.channels / p.ngroups % 128 != 0)
       return fail(SSD_ERR_UNSUPPORTED, "the channels of several groups must be whole blocks of 128 (got %lld)",
                   (long long)(p.channels / p.ngroups));
-    if (!block_norm_grid_ok(p.batch, p.seqlen, p.channels, p.ngroups))
+    if (!block_norm_grid_ok(p.batch, p.seqlen, p.channels, p.ngroups, z != nullptr))
       return fail(SSD_ERR_UNSUPPORTED, "grid too large for this build");
     a.batch = p.batch;
     a.L = p.seqlen;

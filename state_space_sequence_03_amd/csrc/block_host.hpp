@@ -26,7 +26,7 @@ struct BlockNormArgs {
   float* scale;
 };
 hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t stream);
-int block_norm_grid_ok(int64_t batch, int64_t L, int64_t C, int64_t G);
+int block_norm_grid_ok(int64_t batch, int64_t L, int64_t C, int64_t G, int gate);
 int64_t block_norm_limit();
 
 struct AddNormBwdArgs {

@@ -126,6 +126,18 @@ def test_gated_norm_8bit():
     assert call(seqlen=2 ** 40) == UNSUP
 
 
+def test_norms_refuse_what_their_own_launch_cannot_hold():
+    # forwards 16 threads for a token of up to 128 channels, 512 for one of 4096; backwards any number of tokens
+    for n, C in ((2 ** 28, 128), (2 ** 27, 129), (2 ** 23, 4096)):
+        assert add_fwd(AP(batch=1, seqlen=n, channels=C)) == UNSUP, (n, C)
+    for kw in (dict(batch=1, seqlen=2 ** 31), dict(batch=2 ** 16, seqlen=2 ** 15)):
+        assert add_fwd(AP(channels=1, **kw)) == UNSUP and add_bwd(AP(channels=1, **kw), n=BIG) == UNSUP, kw
+        assert size_of("ssd_add_norm_bwd_workspace_size", AP(channels=1, **kw)) == (UNSUP, 7)
+    for kw in (dict(batch=1, seqlen=2 ** 23), dict(batch=1, seqlen=2 ** 31 - 1), dict(batch=2 ** 15, seqlen=2 ** 15)):
+        code, need = size_of("ssd_add_norm_bwd_workspace_size", AP(**kw))
+        assert code == OK and 0 < need < 2 ** 24 and add_bwd(AP(**kw), n=need - 1) == WS, kw
+
+
 # ---- quantising ----
 
 def QP(batch=2, seqlen=10, channels=64, io=1, tile=0, reserved=0):

@@ -772,3 +772,38 @@ def test_matmul8_tiles_of_128(size, tile, out):
     want, mag = ref.matmul(x.q, x.scale, w.q, w.scale, tile)
     within(y, want, ROUGH if out == "bf16" else matmul_count(size[2]), mag, "y")
     assert (room[n:] == 7.0).all() and torch.equal(y, lib.ssd_matmul8(x, w, out_dtype=IO[out]))
+
+
+# ---- sizes past 2^23 tokens ----
+
+def test_norms_of_many_narrow_tokens():
+    # more tokens than a launch has waves of 512 threads: each comes out as in a call of fewer
+    n, C = 2 ** 23 + 3001, 64
+    d = Draw(44)
+    x = d.normal(1, 2 ** 20, C, dtype=torch.bfloat16).repeat(1, 9, 1)[:, :n].contiguous()
+    x[0, 2 ** 23:] *= 0.5
+    w = d.normal(C) + 1.0
+    parts = (0, 5000), (2 ** 23 - 2000, 2 ** 23 + 2000), (n - 3000, n)
+    bits = lambda t: t.view(torch.uint8)
+    y, y8, h = lib.ssd_add_norm_fwd(x, None, w, want_8bit=True)
+    g8 = lib.ssd_gated_norm_fwd_8bit(x, h, w)
+    assert torch.equal(h, x)
+    for a, b in parts:
+        one = x[:, a:b].contiguous()
+        ya, ya8, _ = lib.ssd_add_norm_fwd(one, None, w, want_8bit=True)
+        ga8 = lib.ssd_gated_norm_fwd_8bit(one, one, w)
+        assert torch.equal(ya, y[:, a:b])
+        for got, want in ((ya8, y8), (ga8, g8)):
+            assert torch.equal(bits(got.q), bits(want.q[:, a:b])) and torch.equal(got.scale, want.scale[:, a:b])
+    del y8, g8
+    got = lib.ssd_add_norm_bwd(h, w, y)
+    rows = torch.cat([torch.arange(a, b) for a, b in parts]).cuda()
+    want, _, mag, _ = ref.norm_bwd(h[:, rows], w, y[:, rows])
+    within(got["dx"][:, rows], want, 200, mag, "dx")
+    dw = torch.zeros(2, C, dtype=torch.float64, device="cuda")
+    for a in range(0, n, 2 ** 20):
+        hh, yy = h[0, a:a + 2 ** 20].double(), y[0, a:a + 2 ** 20].double()
+        t = yy * hh / (hh.square().mean(1, keepdim=True) + 1e-5).sqrt()
+        dw += torch.stack([t.sum(0), t.abs().sum(0)])
+    # a thread adds 513 rows (512 workgroups of 32 side by side), 32 of them are joined: 600 e, and 100 of n
+    within(got["dweight"], f(dw[0]), 700, f(dw[1]), "dweight")
