@@ -120,7 +120,8 @@ typedef struct {
 /*   x : (strided) [batch, seqlen, channels] io dtype.
  * q with scale, or qt with scale_t, or all four; the others NULL.
  * Errors: UNSUPPORTED for more than 2^31 - 1 rows or columns, or sizes past a launch's 2^32
- * threads. */
+ * threads: 16 for each block of a row where q is made alone with tile 0, else 256 for each 128 x
+ * 128. */
 ssd_status ssd_quant8(const ssd_quant8_problem* prob, const void* x, const ssd_strides* x_strides,
                       void* q, float* scale, void* qt, float* scale_t, void* stream);
 

@@ -284,7 +284,7 @@ ssd_status ssd_quant8(const ssd_quant8_problem* prob, const void* x, const ssd_s
       return fail(SSD_ERR_MISALIGNED, "every other tensor pointer must be 16-byte aligned");
     if ((__int128)p.batch * p.seqlen > kMostRows || p.channels > kMostRows)
       return fail(SSD_ERR_UNSUPPORTED, "at most 2^31 - 1 rows and columns");
-    if (!quant8_grid_ok(p.batch * p.seqlen, p.channels))
+    if (!quant8_grid_ok(p.batch * p.seqlen, p.channels, p.tile, qt != nullptr))
       return fail(SSD_ERR_UNSUPPORTED, "grid too large for this build");
     a.batch = p.batch;
     a.L = p.seqlen;

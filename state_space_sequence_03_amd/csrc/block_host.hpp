@@ -52,7 +52,7 @@ struct Quant8Args {
   float *scale, *scale_t;
 };
 hipError_t launch_quant8(const Quant8Args& a, hipStream_t stream);
-int quant8_grid_ok(int64_t rows, int64_t C);
+int quant8_grid_ok(int64_t rows, int64_t C, int tile, int transposed);
 
 struct Matmul8Args {
   int64_t M, N, K;

@@ -240,9 +240,10 @@ static hipError_t quant8_t(const Quant8Args& a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-int quant8_grid_ok(int64_t rows, int64_t C) {
+// Fewer than 2^32 threads in the launch that quant8_t makes: 16 for each block of a row, or 256 for each tile.
+int quant8_grid_ok(int64_t rows, int64_t C, int tile, int transposed) {
   const __int128 nc = (C + kBlock8 - 1) / kBlock8, nr = (rows + kBlock8 - 1) / kBlock8;
-  return rows * nc * 16 + 256 < (int64_t(1) << 32) && nr * nc * 256 < (int64_t(1) << 32);
+  return (!tile && !transposed ? rows * nc * 16 + 256 : nr * nc * 256) < (int64_t(1) << 32);
 }
 
 hipError_t launch_quant8(const Quant8Args& a, hipStream_t stream) {

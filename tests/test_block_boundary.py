@@ -162,6 +162,15 @@ def test_quant8():
     assert quant(QP(), x=PTR + 1) == MISAL and quant(QP(), xs=st(0, -1)) == BADVAL and quant(QP(), xs=st(2 ** 62, 0)) == SHAPE
 
 
+def test_quant8_refuses_what_its_own_launch_cannot_hold():
+    # rows alone: 16 threads for each 128 of a row; tiles: 256 for each 128 x 128
+    assert quant(QP(batch=1, seqlen=2 ** 28, channels=128), qt=0, t=0) == UNSUP
+    for kw in (dict(tile=1), dict(tile=0)):
+        assert quant(QP(batch=1, seqlen=2 ** 28, channels=1024, **kw)) == UNSUP, kw
+        assert quant(QP(batch=1, seqlen=2 ** 28, channels=1024, **kw), q=0, s=0) == UNSUP, kw
+    assert quant(QP(batch=1, seqlen=2 ** 28, channels=1024, tile=1), qt=0, t=0) == UNSUP
+
+
 # ---- matrix product ----
 
 def MP(rows=20, cols=30, depth=256, tile=1, out=1, reserved=0):

@@ -807,3 +807,24 @@ def test_norms_of_many_narrow_tokens():
         dw += torch.stack([t.sum(0), t.abs().sum(0)])
     # a thread adds 513 rows (512 workgroups of 32 side by side), 32 of them are joined: 600 e, and 100 of n
     within(got["dweight"], f(dw[0]), 700, f(dw[1]), "dweight")
+
+
+def test_quant8_of_many_short_rows():
+    # 2^28 rows and more, which tiles hold and rows alone would not
+    n = 2 ** 28 + 200
+    d = Draw(45)
+    near = d.normal(4096, dtype=torch.bfloat16)
+    x = near.repeat(n // 4096 + 1)[:n].view(1, n, 1)
+    for tile in (False, True):
+        _, cols = lib.ssd_quant8(x, tile=tile, want_rows=False, want_cols=True)
+        _, want = lib.ssd_quant8(near.view(1, 4096, 1), tile=tile, want_rows=False, want_cols=True)
+        q, scale = cols.q.view(torch.uint8)[0], cols.scale[:, 0]
+        m = n // 4096
+        assert (q[:4096 * m].view(m, 4096) == want.q.view(torch.uint8)).all()
+        assert (scale[:32 * m].view(m, 32) == want.scale[:, 0]).all()
+        tail = x[0, 4096 * m:].double().cpu().numpy().T
+        scaled, sc, _ = ref.blocks(tail, 128 if tile else 1)
+        in8(cols.q[:, 4096 * m:], scaled, 1, "the last rows")
+        within(cols.scale[32 * m:], sc, 0, sc, "their scales")
+    with pytest.raises(lib.SsdArgumentError):
+        lib.ssd_quant8(x)
