@@ -153,7 +153,8 @@ ssd_status ssd_matmul8_workspace_size(const ssd_matmul8_problem* prob, size_t* b
  *   y     : [rows, cols] out dtype.
  *   workspace : ssd_matmul8_workspace_size bytes (which may be 0: then it may be NULL).
  * Errors: BAD_SHAPE for a depth that is not a multiple of 128; UNSUPPORTED for more than
- * 2^31 - 1 rows or cols, a depth above 2^23, or sizes past a launch's 2^32 threads. */
+ * 2^31 - 1 rows or cols, a depth above 2^23, or sizes past a launch's 2^32 threads (up to 16 rows
+ * 2^27 cols, beyond that 2^24 tiles of 64 x 64 of y or larger ones). */
 ssd_status ssd_matmul8(const ssd_matmul8_problem* prob, const void* x, const float* xs,
                        const void* w, const float* ws, void* y, void* workspace,
                        size_t workspace_bytes, void* stream);

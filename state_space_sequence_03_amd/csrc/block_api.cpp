@@ -81,7 +81,8 @@ ssd_status matmul_supported(const ssd_matmul8_problem& p) {
   // 256 rows of a tile are reached by 32-bit offsets
   if (p.rows > kMostRows || p.cols > kMostRows || p.depth > (1 << 23))
     return fail(SSD_ERR_UNSUPPORTED, "at most 2^31 - 1 rows and columns, and a depth of 2^23");
-  if (!matmul8_grid_ok(p.rows, p.cols)) return fail(SSD_ERR_UNSUPPORTED, "grid too large for this build");
+  if (!matmul8_grid_ok(p.rows, p.cols, p.depth, p.out_dtype == SSD_BF16))
+    return fail(SSD_ERR_UNSUPPORTED, "grid too large for this build");
   return SSD_OK;
 }
 

@@ -66,7 +66,7 @@ struct Matmul8Args {
 };
 hipError_t launch_matmul8(const Matmul8Args& a, hipStream_t stream);
 size_t matmul8_workspace(int64_t M, int64_t N, int64_t K, int out_bf16);
-int matmul8_grid_ok(int64_t M, int64_t N);
+int matmul8_grid_ok(int64_t M, int64_t N, int64_t K, int out_bf16);
 
 hipError_t launch_clip(const ssd_grad* grads, int64_t n, const ssd_clip_options& opt, float* norm,
                        void* workspace, hipStream_t stream);

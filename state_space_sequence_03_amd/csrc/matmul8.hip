@@ -433,10 +433,14 @@ size_t matmul8_workspace(int64_t M, int64_t N, int64_t K, int out_bf16) {
   return p.parts > 1 ? size_t(p.parts) * M * N * sizeof(float) : 0;
 }
 
-// The smallest tiles, 16 columns x 16 rows (up to 16 rows) or 64 x 64, of 512 threads at most.
-int matmul8_grid_ok(int64_t M, int64_t N) {
-  const __int128 tiles = M <= 16 ? (N + 15) / 16 : (__int128)((N + 63) / 64) * ((M + 63) / 64);
-  return tiles * 512 < (int64_t(1) << 32);
+// Fewer than 2^32 threads along the first axis of the plan's launch: 512 for 16 columns x 16 rows (of more than 16 rows,
+// 16 x 32) or 256 x 256, 256 for 64 x 64 or 128 x 128.  (The parts of a depth lie along the second, and what joins
+// them has fewer.)
+int matmul8_grid_ok(int64_t M, int64_t N, int64_t K, int out_bf16) {
+  const Matmul8Form form = matmul8_plan(M, N, K, out_bf16).form;
+  const int64_t side = form == kTile64 ? 64 : form == kTile128 ? 128 : 256;
+  const __int128 groups = form == kFew ? (__int128)((N + 15) / 16) : (__int128)((N + side - 1) / side) * ((M + side - 1) / side);
+  return groups * (form == kFew || form == kTile256 ? 512 : 256) < (int64_t(1) << 32);
 }
 
 template <typename O, int NT, int MT>

@@ -200,6 +200,16 @@ def test_matmul8_pointers():
     assert size_of("ssd_matmul8_workspace_size", MP())[0] == OK
 
 
+def test_matmul8_refuses_what_its_own_launch_cannot_hold():
+    # 512 threads for 16 columns of up to 16 rows, 256 for tiles of 64 x 64 and 128 x 128, 512 for 256 x 256
+    size = "ssd_matmul8_workspace_size"
+    for rows, cols, out in ((16, 2 ** 27 - 16, 1), (17, 2 ** 30 - 64, 0), (2 ** 30 - 64, 64, 1), (131077, 262147, 1), (131077, 262147, 0),
+                            (2 ** 22, 10576, 1)):
+        assert size_of(size, MP(rows, cols, 128, out=out)) == (OK, 0), (rows, cols, out)
+    for rows, cols, out in ((16, 2 ** 27, 1), (17, 2 ** 30, 0), (2 ** 30, 64, 1), (2 ** 20, 2 ** 20, 1), (2 ** 20, 2 ** 20, 0)):
+        assert size_of(size, MP(rows, cols, 128, out=out)) == (UNSUP, 7) and matmul(MP(rows, cols, 128, out=out)) == UNSUP
+
+
 def test_products_of_every_form_are_tested(tmp_path):
     # every form of the plan, its depth whole and split, for results in bf16 and in fp32, has sizes among those that
     # the GPU tests run (by tile and by row each)

@@ -828,3 +828,18 @@ def test_quant8_of_many_short_rows():
         within(cols.scale[32 * m:], sc, 0, sc, "their scales")
     with pytest.raises(lib.SsdArgumentError):
         lib.ssd_quant8(x)
+
+
+def test_matmul8_of_many_elements():
+    # y of 2^35 elements: tiles of 256 x 256, of which a launch holds 2^23
+    M, N, K = 131077, 262147, 128
+    x, w = operands(M, N, K, False, 46)
+    y = lib.ssd_matmul8(x, w)
+    d = Draw(47)
+    some = lambda n: torch.cat([torch.arange(40), torch.randint(n, (200,), generator=d.g), torch.arange(n - 300, n)]).cuda()
+    r, c = some(M), some(N)
+    want, mag = ref.matmul(x.q.view(torch.uint8)[r].view(torch.float8_e4m3fn), x.scale[:, r],
+                           w.q.view(torch.uint8)[c].view(torch.float8_e4m3fn), w.scale[:, c], False)
+    within(y[r][:, c], want, ROUGH, mag, "y")
+    del y
+    torch.cuda.empty_cache()
