@@ -15,7 +15,7 @@
 
 namespace ssd {
 
-constexpr int kTensors = 128;       // 28 bytes each: under the 4 KB of a launch's arguments
+constexpr int kTensors = 128;       // 29 bytes each
 constexpr int64_t kLeastChunk = 8192;
 constexpr int64_t kMostParts = 1024;   // part sums that every workgroup of the second pass adds by itself
 
@@ -28,6 +28,8 @@ struct Tensors {
   int32_t count;
   int32_t chunk8;                // chunk / 8
 };
+// with the other arguments of clip_scale_kernel
+static_assert(sizeof(Tensors) + 5 * 8 + 8 + 8 <= 4096, "a launch's arguments have 4 KB");
 
 // The tensor of workgroup b.
 __device__ __forceinline__ int tensor_of(const Tensors& t, int b) {
