@@ -12,9 +12,9 @@
 // Bound by HBM: every input is read once, a token's elements stay in registers between
 // the sum and the outputs, in pieces of eight channels, NV per thread.  The gates (an exp2
 // and a reciprocal per element, quarter rate) keep the vector ALU busy beside it.
-// bf16 with an fp32 residual, 2 x 8192 x 2560 to 8 bits 87 us (5.3 TB/s of the 5.07 that a
-// large copy reaches: more is read than written), gradients over 2 x 4096 66 us (5.1 TB/s, 5 of
-// them part sums); gated norm of 2 x 8192 x 5120 to 8 bits 90 us (4.7 TB/s).
+// bf16 with an fp32 residual, 2 x 8192 x 2560 to 8 bits 86 us (5.4 TB/s; a large copy, half of
+// which is written, 5.07), gradients over 2 x 4096 65 us (5.1 TB/s, 5 of them part sums); gated
+// norm of 2 x 8192 x 5120 to 8 bits 90 us (4.7 TB/s), of 2 groups of 128 24 us (0.9 TB/s: see item_grid).
 #include "block_device.hpp"
 #include "block_host.hpp"
 
@@ -259,6 +259,8 @@ struct ItemGrid {
 //   three pieces per thread, the fewest idle lanes first (256 threads of 3 pieces 92 us, 128 of 5 95, 512 of 2
 //   114, 320 of 2 105), and two tokens in a row: more of them make whole rounds of workgroups that load, compute
 //   and store in step (256 of 3: four 90, but 16384 x 8 x 512 70 in place of 67, 2048 x 5120 17 in place of 16).
+// With several groups a workgroup's places are for groups of one token, and those past the last group stand idle
+// (16384 x 2 x 128 24 us, 8 x 128 27, 2 x 1024 45, 8 x 512 72).
 ItemGrid item_grid(int64_t rows, int64_t S, int64_t G, bool gate) {
   ItemGrid g;
   const int pieces = (int)((S + kBlock8 - 1) / kBlock8 * (kBlock8 / 8));

@@ -4,7 +4,7 @@
 //     norm, rounded to fp32, is not finite)
 //
 // Bound by HBM: every gradient is read twice, since no factor is known before the last
-// one has been read, and written once: 241 M bf16 gradients into fp32 411 us, 1.93 GB at
+// one has been read, and written once: 241 M bf16 gradients into fp32 410 us, 1.93 GB at
 // 4.7 TB/s (a large copy: 5.07).  A launch takes the pointers of up to kTensors
 // tensors in its arguments, so a call needs no copy to the device and can be captured;
 // longer lists take more launches.  Sums of squares are 64-bit from the first addition

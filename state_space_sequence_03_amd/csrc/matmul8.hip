@@ -11,9 +11,10 @@
 //
 // Many rows are bound by the matrix cores and, as closely, by LDS: a tile of 256 x 256 reads
 // 192 KB and takes in 66 KB from memory for every 2048 cycles of products.  16384 x 10576 x 2560
-// in bf16: 413 us, 2.15 PFLOP/s (without the stores 75 us less, without loads 70, without the
-// scaling into the sums 45; a library's product of the same operands with one scale for all 425 us;
-// the card's best rate there, at 8192 x 8192 x 8192, 2.84 PFLOP/s).  Few rows are bound by the
+// in bf16: 412 us, 2.15 PFLOP/s (without the stores 75 us less, without loads 70, without the
+// scaling into the sums 45; a library's product of the same operands with one scale for all 392 us beside
+// it; the card's best rate, at 8192 x 8192 x 8192, 2.84 PFLOP/s).  Tiles of 128 x 128: 16384 x 2560 x 5120
+// in bf16 213 us, 2.02 PFLOP/s; 10576 x 2560 x 8192 by row in fp32 407 us, 1.09 PFLOP/s.  Few rows are bound by the
 // weight's way from memory: one row, 10576 x 2560, 7.1 us, 3.8 TB/s.
 #include <type_traits>
 
